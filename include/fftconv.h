@@ -321,6 +321,146 @@ FFTCONV_API int fftconv_device_status(fftconv_plan_t plan, fftconv_stream_t stre
 FFTCONV_API int fftconv_selftest_bounded_wait(fftconv_plan_t plan, int64_t polls, int arrive,
                                   fftconv_stream_t stream);
 
+/* ------------------------------------------------- linear attention ---
+ *
+ * Causal linear attention with one decay per head, the recurrent mixer that
+ * stands beside the long convolution: with g = exp(log_decay[h]) and a = scale,
+ * for every sequence and head h
+ *
+ *     S_t = g S_{t-1} + k_t v_t^T            (K x V, fp32, S_{-1} = initial or 0)
+ *     o_t = a q_t S_t = a sum_{s<=t} g^(t-s) (q_t . k_s) v_s + a g^(t+1) q_t S_{-1}
+ *
+ * (a convolution whose kernel is exponential in the lag and weighted by the
+ * data).  fp16 / bf16 tensors; products on the tensor cores, sums and states
+ * in fp32.
+ *
+ * Tensors: q [B, T, Hq, K], k [B, T, Hk, K], v [B, T, Hv, V], o [B, T, H, V]
+ * with the last index contiguous and the strides given in elements (multiples
+ * of 8 where the extent is above 1, never 0 there).  Hq, Hk and Hv each divide
+ * H: head h reads query head h / (H / Hq), and so on (queries and keys, or
+ * keys and values, shared by groups of heads).  K and V are multiples of 8 up
+ * to 128.  States are [sequences, H, K, V] fp32, contiguous.
+ * nseq = 0: B sequences of T tokens.  nseq > 0: packed, B = 1, and cu_seqlens
+ * (device int32, nseq + 1 ascending offsets into the T tokens) gives sequence
+ * i the tokens [cu[i], cu[i+1]); empty sequences are allowed; tokens outside
+ * [cu[0], cu[nseq]) are not used.  Offsets outside [0, T] are clamped.
+ * log_decay: device fp32 [H], at most 0 in ordinary use (-inf: no memory).
+ * A non-finite k or v at token s reaches every later output of its sequence,
+ * and may reach outputs up to 127 tokens before s (the tile it shares a
+ * product with), never another sequence.
+ *
+ * Workspace: fftconv_linear_attention_workspace_bytes bytes of device memory,
+ * 256-byte aligned, private to the call until its work is done (two calls, or
+ * two captured graphs, that may run at once need two).  It depends on the
+ * shape and on the current device's number of SMs. */
+typedef struct {
+    int64_t B, T, nseq;
+    int64_t H, Hq, Hk, Hv;
+    int64_t K, V;
+    int32_t dtype;               /* FFTCONV_F16 or FFTCONV_BF16 */
+    float scale;
+    int32_t zero_rest;           /* packed: o's rows of tokens outside every sequence: nonzero: set
+                                    to zero, 0: left as they were */
+    int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];   /* batch, token, head */
+} fftconv_linear_attention_t;
+
+FFTCONV_API size_t fftconv_linear_attention_workspace_bytes(const fftconv_linear_attention_t* shape, int backward);
+
+/* o (with o_stride) and, unless final_state is NULL, the states after the
+ * last tokens (a sequence without tokens keeps its initial state).
+ * initial_state may be NULL (zeros).  cu_seqlens is NULL when nseq = 0.
+ * o must not overlap an input; final_state may be initial_state itself.
+ * Asynchronous on `stream`; allocates nothing. */
+FFTCONV_API int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void* q, const void* k,
+                                         const void* v, const float* log_decay, const float* initial_state,
+                                         const int32_t* cu_seqlens, void* o, float* final_state, void* workspace,
+                                         size_t workspace_bytes, fftconv_stream_t stream);
+
+/* Gradients for the incoming do_ (with o_stride) and dfinal (fp32, NULL:
+ * zeros).  With dS_t = a q_t do_t^T + g dS_{t+1} and dS of the last token
+ * including dfinal:
+ *     dq_t = a S_t do_t,   dk_t = dS_t v_t,   dv_t = dS_t^T k_t,
+ *     dinitial = g dS_0  (dfinal for a sequence without tokens).
+ * dq, dk, dv: contiguous, of q's, k's and v's shape; heads that are shared
+ * are summed over their group in fp32.  dinitial: fp32 or NULL.  log_decay
+ * has no gradient.  Rows of tokens outside every packed sequence are zero.
+ * The result does not depend on the order in which blocks run.
+ * Asynchronous on `stream`; allocates nothing. */
+FFTCONV_API int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, const void* q,
+                                                  const void* k, const void* v, const float* log_decay,
+                                                  const float* initial_state, const int32_t* cu_seqlens,
+                                                  const void* do_, const float* dfinal, void* dq, void* dk, void* dv,
+                                                  float* dinitial, void* workspace, size_t workspace_bytes,
+                                                  fftconv_stream_t stream);
+
+/* One token of B sequences: S <- g S + k v^T in place, o = a q S.
+ *   q [B, Hq, K], k [B, Hk, K], v [B, Hv, V]: q_stride, k_stride, v_stride are
+ *     the element strides of batch and head; o [B, H, V] contiguous.
+ *   state : [pool, H, K, V] fp32, contiguous.  slots NULL: pool = B and row b
+ *     uses state b.  Otherwise slots (device int32 [B]) names row b's state; a
+ *     row whose slot is outside [0, pool), or that an earlier row names
+ *     already, is idle: its o is zero and it touches no state.
+ * All in fp32 up to o's rounding.  Asynchronous on `stream`; allocates
+ * nothing. */
+FFTCONV_API int fftconv_linear_attention_step(const void* q, const void* k, const void* v, const float* log_decay,
+                                              float* state, const int32_t* slots, void* o, int64_t B, int64_t pool,
+                                              int64_t H, int64_t Hq, int64_t Hk, int64_t Hv, int64_t K, int64_t V,
+                                              fftconv_dtype_t dtype, float scale, const int64_t* q_stride,
+                                              const int64_t* k_stride, const int64_t* v_stride,
+                                              fftconv_stream_t stream);
+
+/* Synchronise `stream` and return FFTCONV_ERR_TIMEOUT if a bounded device-side
+ * wait of a linear attention kernel gave up on the current device since the
+ * last call (its outputs are then incomplete), else FFTCONV_OK. */
+FFTCONV_API int fftconv_linear_attention_status(fftconv_stream_t stream);
+
+/* ------------------------------------------------------- group norm ---
+ *
+ * Group normalisation, channels last, with an activation or an activated
+ * gate.  x is N samples of S positions of C channels in G groups of C / G;
+ * the mean and the (biased) variance of a sample's group run over its S
+ * positions and C / G channels:
+ *
+ *     n = (x - mean) / sqrt(var + eps) * weight + bias
+ *     y = act(n)          or, with a gate,        y = n * act(gate)
+ *
+ * (S = 1: the head norm and gate behind a mixer's output.)
+ * x and gate: N * S rows of C elements, ld_x and ld_gate elements apart; y
+ * contiguous.  fp32 / fp16 / bf16, statistics and sums in fp32.  weight and
+ * bias: [C], both or neither, in x's type or fp32 (weight_dtype).  gate may be
+ * NULL.  mean, rstd: fp32 [N, G], written by the forward call (NULL: not kept)
+ * and read by the backward call.
+ * Pointers are aligned to 16 bytes.  Rows whose stride, width and group width
+ * are multiples of 16 bytes are read in vectors of that size, others
+ * element by element.
+ * Workspace: fftconv_group_norm_workspace_bytes, 256-byte aligned, private to
+ * the call until its work is done. */
+typedef enum {
+    FFTCONV_ACT_NONE = 0,
+    FFTCONV_ACT_SILU = 1,
+    FFTCONV_ACT_SIGMOID = 2
+} fftconv_activation_t;
+
+FFTCONV_API size_t fftconv_group_norm_workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, int backward);
+
+FFTCONV_API int fftconv_group_norm(const void* x, const void* gate, const void* weight, const void* bias, void* y,
+                                   float* mean, float* rstd, int64_t N, int64_t S, int64_t C, int64_t G, int64_t ld_x,
+                                   int64_t ld_gate, fftconv_dtype_t dtype, fftconv_dtype_t weight_dtype,
+                                   fftconv_activation_t act, float eps, void* workspace, size_t workspace_bytes,
+                                   fftconv_stream_t stream);
+
+/* Gradients for dy (rows ld_dy apart): dx and dgate contiguous (dgate NULL
+ * without a gate), dweight and dbias fp32 [C] (both or neither; they need
+ * weight and bias).  The result does not depend on the order in which blocks
+ * run.  Asynchronous on `stream`; allocates nothing. */
+FFTCONV_API int fftconv_group_norm_backward(const void* x, const void* gate, const void* weight, const void* bias,
+                                            const void* dy, const float* mean, const float* rstd, void* dx,
+                                            void* dgate, float* dweight, float* dbias, int64_t N, int64_t S,
+                                            int64_t C, int64_t G, int64_t ld_x, int64_t ld_gate, int64_t ld_dy,
+                                            fftconv_dtype_t dtype, fftconv_dtype_t weight_dtype,
+                                            fftconv_activation_t act, void* workspace, size_t workspace_bytes,
+                                            fftconv_stream_t stream);
+
 /* Static description of a status code. */
 FFTCONV_API const char* fftconv_status_string(int status);
 

@@ -57,6 +57,16 @@ _SIGNATURES = {
     "fftconv_filter_to_rfft": (ctypes.c_int, [_vp, _vp, _vp, _vp]),
     "fftconv_device_status": (ctypes.c_int, [_vp, _vp]),
     "fftconv_selftest_bounded_wait": (ctypes.c_int, [_vp, _i64, ctypes.c_int, _vp]),
+    "fftconv_linear_attention_workspace_bytes": (_sz, [_vp, ctypes.c_int]),
+    "fftconv_linear_attention": (ctypes.c_int, [_vp] * 9 + [_vp, _sz, _vp]),
+    "fftconv_linear_attention_backward": (ctypes.c_int, [_vp] * 13 + [_vp, _sz, _vp]),
+    "fftconv_linear_attention_step": (ctypes.c_int, [_vp] * 7 + [_i64] * 8 + [ctypes.c_int, ctypes.c_float]
+                                      + [_vp] * 4),
+    "fftconv_linear_attention_status": (ctypes.c_int, [_vp]),
+    "fftconv_group_norm_workspace_bytes": (_sz, [_i64] * 4 + [ctypes.c_int]),
+    "fftconv_group_norm": (ctypes.c_int, [_vp] * 7 + [_i64] * 6 + [ctypes.c_int] * 3 + [ctypes.c_float, _vp, _sz,
+                                                                                        _vp]),
+    "fftconv_group_norm_backward": (ctypes.c_int, [_vp] * 11 + [_i64] * 7 + [ctypes.c_int] * 3 + [_vp, _sz, _vp]),
     "fftconv_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fftconv_last_error": (ctypes.c_char_p, []),
     "fftconv_version": (ctypes.c_char_p, []),
@@ -362,3 +372,8 @@ def fftconv(u, k, w=None, v=None, mask=None, order: int = 0):
         return _autograd_function().apply(u, k, w, v, plan)
     Kf = plan.precompute(k)
     return plan.forward(u, Kf, w=w, v=v, mask=mask)
+
+
+from .linear_attention import (linear_attention, linear_attention_status,  # noqa: E402
+                               linear_attention_step)
+from .group_norm import group_norm  # noqa: E402

@@ -1,0 +1,1321 @@
+// linear_attention.cu -- causal linear attention with a decay for each head:
+// the chunked prompt form on the tensor cores, forward and backward.
+//
+// Mathematics.  With g = exp(log_decay[h]), a query side x, a key side y and
+// a value side z, the kernel evaluates over the tokens of one sequence, in
+// either direction of time,
+//
+//     o_t = a sum_{s at or before t} g^|t-s| (x_t . y_s) z_s + (carry term)
+//
+// in chunks of 128 tokens: P = (x y^T) * a g^|i-j| inside the chunk (masked to
+// its triangle), o = P z + g^(...) x C with the carried state C (key dim x
+// value dim, fp32 in registers), and C <- g^n C + sum_j g^(...) y_j z_j^T.
+// The forward pass is (x, y, z) = (q, k, v) forward in time.  The gradients
+// are the same sums:
+//     dq = (do, v, k) forward in time, carry = S^T
+//     dk = (v, do, q), dv = (k, q, do) backward in time, carry = dS^T and dS,
+// so the backward pass is one launch with three roles.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdio>
+#include <string>
+
+#include "../../include/fftconv.h"
+#include "internal.h"
+#include "tc_ptx.cuh"
+
+namespace fftconv {
+namespace {
+
+using namespace tc;
+
+constexpr int kChunk = 128;                   // tokens of a chunk: the rows of one MMA
+constexpr int kStateWarps = 8;
+constexpr int kLoadWarp = 4 + kStateWarps, kMmaWarp = kLoadWarp + 1;
+constexpr int kThreads = (kMmaWarp + 1) * 32; // 4 warps rows, 8 warps state, loads, MMA issue
+constexpr uint32_t kWaitLimit = 1u << 20;
+constexpr int kMaxRoles = 3;
+
+__device__ int g_status;                      // FFTCONV_ERR_TIMEOUT once a wait gave up
+
+struct Role {
+    int x, y, z;                              // tensor maps of the three sides
+    int x_div, y_div, z_div;                  // heads of the call per head of the tensor
+    int rev;                                  // backward in time
+    int out_f32;                              // fp32 partial sums of shared heads
+    int kd, vd;                               // key and value dims
+    int init_t;                               // init is stored [vd][kd]
+    float a_in, a_carry, key_scale;
+    void* out;
+    int64_t out_b, out_t, out_h;
+    const float* init;                        // [seq][H][kd][vd], or null: zeros
+    float* fin;                               // carry behind the last token, or null
+    float* seg;                               // segment states [segment][H][kd][vd]
+};
+
+struct Params {
+    CUtensorMap maps[7];
+    Role role[kMaxRoles];
+    const float* log_decay;
+    const int32_t* cu;
+    int64_t T;
+    int nroles, H, nseq, nper, seg_len, max_seg;   // nper: segments of a sequence (unpacked)
+};
+
+// Which sequence and which of its tokens segment `sid` stands for.
+struct Segment {
+    int seq, idx, count, n;                   // n: tokens
+    int t0, b;                                // first token's coordinates
+};
+
+// Called by one whole warp.  Sequences without tokens have one empty segment.
+__device__ Segment find_segment(const Params& p, int sid) {
+    Segment s{-1, 0, 0, 0, 0, 0};
+    if (!p.cu) {
+        s.seq = sid / p.nper;
+        s.idx = sid - s.seq * p.nper;
+        s.count = p.nper;
+        s.b = s.seq;
+        s.t0 = s.idx * p.seg_len;
+        s.n = min(p.seg_len, (int)p.T - s.t0);
+        return s;
+    }
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int base = 0; base < p.nseq; base += 32) {
+        const int i = base + lane;
+        int start = 0, len = 0, cnt = 0;
+        if (i < p.nseq) {
+            start = min(max(p.cu[i], 0), (int)p.T);
+            len = min(max(p.cu[i + 1], start), (int)p.T) - start;
+            cnt = max(1, (len + p.seg_len - 1) / p.seg_len);
+        }
+        int incl = cnt;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, d);
+            if (lane >= d) incl += v;
+        }
+        const int lo = before + incl - cnt;
+        const unsigned hit = __ballot_sync(0xffffffffu, sid >= lo && sid < lo + cnt);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            s.seq = base + src;
+            s.idx = sid - __shfl_sync(0xffffffffu, lo, src);
+            s.count = __shfl_sync(0xffffffffu, cnt, src);
+            len = __shfl_sync(0xffffffffu, len, src);
+            s.t0 = __shfl_sync(0xffffffffu, start, src) + s.idx * p.seg_len;
+            s.n = min(p.seg_len, len - s.idx * p.seg_len);
+            return s;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return s;                                 // past the last segment: seq = -1
+}
+
+// g^n for g = exp(ld), the product ld * n carried in two fp32 parts.  Decays
+// below exp(-1e4) are 0 from the first power on, like -inf.
+__device__ __forceinline__ float decay_power(float ld, float n) {
+    ld = ld < -1e4f ? -1e4f : ld;
+    const float p = ld * n;
+    const float e = expf(p);
+    return n == 0.f ? 1.f : fmaf(e, fmaf(ld, n, -p), e);
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+    tmem_st16(a, r);
+    tmem_st16(a + 16, r + 16);
+}
+
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int d, int h, int t, int b,
+                                         uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(d), "r"(h), "r"(t), "r"(b), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// 16-bit arithmetic of the two types: packing with round to nearest even, and
+// the two halves as fp32.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    if constexpr (F16)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+    if constexpr (F16) {
+        __half2 h;
+        *reinterpret_cast<uint32_t*>(&h) = v;
+        return __half22float2(h);
+    } else {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+}
+
+// 2^e with the largest exponent that keeps amax * 2^e below 2^15 (1 for 0,
+// inf and NaN): the exact scale of an fp16 operand.
+__device__ __forceinline__ float fp16_scale(float amax) {
+    const int ex = (int)((__float_as_uint(amax) >> 23) & 255);
+    if (ex == 0 || ex == 255) return 1.f;
+    const int e = min(max(14 - (ex - 127), -60), 60);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+template <int KP, int VP>
+struct Layout {
+    static constexpr int XBytes = KP * kChunk * 2, ZBytes = VP * kChunk * 2;
+    static constexpr int StageBytes = 2 * XBytes + ZBytes;
+    static constexpr int CarryBytes = KP * VP * 2;
+    static constexpr int Stages = StageBytes <= 49152 ? 4 : StageBytes <= 65536 ? 3 : 2;
+    static constexpr int OffCarry = Stages * StageBytes;
+    static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d|, d = j - i in [-127, 127]
+    static constexpr int OffPow = OffTab + 256 * 4;           // g^e, e <= 128
+    static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
+    static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, scales, TMEM base
+    static constexpr int OffBar = OffMisc + 112;
+    static constexpr int Bytes = OffBar + (2 * Stages + 12) * 8;
+    // TMEM columns
+    static constexpr int S = 0, O = 128, C = O + VP, Kt = C + VP;
+    static constexpr int KtParts = (512 - Kt) / 64;           // parts that have columns of their own
+    static_assert(Bytes <= 232448, "shared memory");
+    static_assert(KtParts >= 2, "TMEM columns");
+};
+
+// One CTA: one (segment, head, role).  Warps 0-3 own the token rows (P, the
+// output), warps 4-11 the rows of the state (kept in registers: its decay, its
+// 16-bit copy for the next product, the weighted keys), warp 12 issues the
+// loads, warp 13 the MMAs.
+//
+// Rounding: P and the carry's copy are rounded once to the 16-bit type (their
+// products are the two halves of the output, each with the error of one
+// rounding of it); the weighted keys are split into two (fp16) or three
+// (bf16) 16-bit parts, 22 or 24 bits, because the state is an fp32 result.
+// fp16 operands are scaled by exact powers of two (P by row, the carry's copy
+// by its largest value, the weighted keys by channel), so that nothing
+// overflows fp16's range or falls below it.
+template <int KP, int VP, bool F16, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__ Params p) {
+    using L = Layout<KP, VP>;
+    constexpr int kParts = F16 ? 2 : 3;
+    constexpr bool kLate = kParts > L::KtParts;               // the last part waits for part 0's columns
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float* tab = reinterpret_cast<float*>(smem + L::OffTab);
+    float* pw = reinterpret_cast<float*>(smem + L::OffPow);
+    float* kw = reinterpret_cast<float*>(smem + L::OffKw);
+    volatile int* misc = reinterpret_cast<volatile int*>(smem + L::OffMisc);
+    volatile int* abort_flag = misc + 7;
+    volatile float* carry_inv = reinterpret_cast<volatile float*>(misc + 8);      // [2] by chunk parity
+    volatile float* amax_sh = reinterpret_cast<volatile float*>(misc + 10);       // [2][8]
+    uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(smem + L::OffMisc + 4 * 26);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OffBar);
+    uint64_t* empty = full + L::Stages;
+    uint64_t* bar_s = empty + L::Stages;
+    uint64_t* bar_o = bar_s + 1;
+    uint64_t* bar_pv = bar_s + 2;
+    uint64_t* bar_st = bar_s + 3;
+    uint64_t* bar_kt = bar_s + 4;
+    uint64_t* carry_ready = bar_s + 5;
+    uint64_t* b_ready = bar_s + 6;
+    uint64_t* p_ready = bar_s + 7;
+    uint64_t* o_free = bar_s + 8;
+    uint64_t* late_ready = bar_s + 9;
+    uint64_t* wgb_bar = bar_s + 10;
+    uint64_t* bar_fin = bar_s + 11;
+
+    const int tid = threadIdx.x;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int lane = tid & 31;
+    const int role_i = blockIdx.x % p.nroles;
+    const int h = (blockIdx.x / p.nroles) % p.H;
+    const int sid = blockIdx.x / (p.nroles * p.H);
+    const Role& r = p.role[role_i];
+    const bool rev = r.rev != 0;
+
+    if (warp == 0) {
+        const Segment s = find_segment(p, sid);
+        if (lane == 0) {
+            misc[0] = s.seq;
+            misc[1] = s.idx;
+            misc[2] = s.count;
+            misc[3] = s.n;
+            misc[4] = s.t0;
+            misc[5] = s.b;
+        }
+    } else if (warp == kLoadWarp && lane == 0) {
+        for (int i = 0; i < L::Stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 5; ++i) mbar_init(bar_s + i, 1);
+        for (int i = 5; i < 11; ++i) mbar_init(bar_s + i, bar_s + i == p_ready || bar_s + i == o_free ? 4 : kStateWarps);
+        mbar_init(bar_fin, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    } else if (warp == kMmaWarp) {
+        tmem_alloc(tmem_sh, 512);
+        tmem_relinquish();
+    } else if (warp >= 4 && warp < 8) {
+        const float ld = p.log_decay[h];
+        const int i = tid - 128;
+        const float w = decay_power(ld, (float)i);
+        pw[i] = w;
+        if (i == 127) pw[128] = decay_power(ld, 128.f);
+        tab[127 + (rev ? i : -i)] = r.a_in * w;
+        if (i) tab[127 - (rev ? i : -i)] = 0.f;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_sh, 0);
+    const int seq = misc[0], idx = misc[1], count = misc[2], n = misc[3], t0 = misc[4], b = misc[5];
+    const bool first = rev ? idx == count - 1 : idx == 0;     // in the direction of time of the role
+    const bool last = rev ? idx == 0 : idx == count - 1;
+    const int nch = (seq < 0 || (STATE_ONLY && last)) ? 0 : (n + kChunk - 1) / kChunk;
+    const bool has_init = !STATE_ONLY && (first ? r.init != nullptr : true);
+    const bool want_fin = STATE_ONLY || (last && r.fin != nullptr);
+
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1, abort_flag, kWaitLimit));
+    };
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicExch(&g_status, FFTCONV_ERR_TIMEOUT);
+    };
+    auto arrive = [&](uint64_t* bar) {                        // one arrival a warp
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
+    // chunk c of the role's direction: its first token and number of tokens
+    auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kChunk; };
+    auto chunk_n = [&](int c) { return min(kChunk, n - chunk_at(c)); };
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------- loads ---
+        if (lane == 0 && nch > 0) {
+            const CUtensorMap *mx = &p.maps[r.x], *my = &p.maps[r.y], *mz = &p.maps[r.z];
+            const int hx = h / r.x_div, hy = h / r.y_div, hz = h / r.z_div;
+            int issued = 0;
+            for (int c = 0; c < nch; ++c) {
+                const int st = c % L::Stages;
+                if (c >= L::Stages &&
+                    !mbar_wait_bounded(&empty[st], ((c / L::Stages) - 1) & 1, abort_flag, kWaitLimit)) {
+                    fail();
+                    break;
+                }
+                uint8_t* base = smem + st * L::StageBytes;
+                const int t = t0 + chunk_at(c);
+                mbar_expect_tx(&full[st], STATE_ONLY ? L::StageBytes - L::XBytes : L::StageBytes);
+                if (!STATE_ONLY)
+                    for (int d = 0; d < KP; d += 64) tma_load(base + d * 256, mx, d, hx, t, b, &full[st]);
+                for (int d = 0; d < KP; d += 64) tma_load(base + L::XBytes + d * 256, my, d, hy, t, b, &full[st]);
+                for (int d = 0; d < VP; d += 64) tma_load(base + 2 * L::XBytes + d * 256, mz, d, hz, t, b, &full[st]);
+                issued = c + 1;
+            }
+            // nothing of this CTA's loads is in flight when it ends
+            for (int c = max(0, issued - L::Stages); c < issued; ++c)
+                for (uint32_t i = 0; i < kWaitLimit; ++i)
+                    if (mbar_try_wait(&full[c % L::Stages], (c / L::Stages) & 1)) break;
+        }
+    } else if (warp == kMmaWarp) {
+        // --------------------------------------------------- MMA issue ---
+        constexpr uint32_t kFmt = F16 ? 0u : (1u << 7) | (1u << 10);
+        constexpr uint32_t kTransB = 1u << 16;
+        const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
+        const uint32_t id_z = idesc_f16_f32(128, VP) | kFmt | kTransB;
+        const uint32_t sb = smem_u32(smem);
+        const uint64_t d_carry = make_desc(sb + L::OffCarry, KP * 128, 1024, 2);
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+            const int st = c % L::Stages;
+            const int ks = (chunk_n(c) + 15) / 16;
+            const bool carry = c > 0 || has_init;
+            const bool state = c + 1 < nch || want_fin;
+            const uint32_t base = sb + st * L::StageBytes;
+            const uint64_t d_x = make_desc(base, 16, 1024, 2);
+            const uint64_t d_y = make_desc(base + L::XBytes, 16, 1024, 2);
+            const uint64_t d_z = make_desc(base + 2 * L::XBytes, 16384, 1024, 2);
+            ok = wait(&full[st], c / L::Stages);
+            if (ok && !STATE_ONLY) {
+                if (c > 0) ok = wait(bar_pv, c - 1);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < KP / 16; ++k) {
+                    const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                    mma_ss_warp(tbase + L::S, d_x + step, d_y + step, id_s, k > 0);
+                }
+                tc_commit_warp(bar_s);
+                ok = wait(carry_ready, c) && (c == 0 || wait(o_free, c - 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (carry)
+                    for (int k = 0; k < KP / 16; ++k) {
+                        const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                        mma_ss_warp(tbase + L::O, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
+                    }
+                tc_commit_warp(bar_o);
+            }
+            if (ok) ok = wait(b_ready, c);
+            if (!ok) break;
+            tc_fence_after();
+            // the chunk's own state, its smallest parts first: the MMA
+            // truncates each sum, so few steps should meet a large one
+            auto weighted = [&](uint32_t cols, uint32_t acc) {
+                for (int k = 0; k < ks; ++k)
+                    mma_ts_warp(tbase + L::C, tbase + cols + k * 8, d_z + (uint64_t)(k * 128), id_z, k > 0 ? 1u : acc);
+            };
+            if (state) {
+                if constexpr (kLate) {
+                    weighted(L::Kt, 0u);
+                    weighted(L::Kt + 64, 1u);
+                    tc_commit_warp(bar_kt);
+                } else {
+                    for (int part = kParts - 1; part >= 0; --part)
+                        weighted(L::Kt + part * 64, part == kParts - 1 ? 0u : 1u);
+                    tc_commit_warp(bar_st);
+                }
+            }
+            if (!STATE_ONLY) {
+                ok = wait(p_ready, c);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < ks; ++k)
+                    mma_ts_warp(tbase + L::O, tbase + L::S + k * 8, d_z + (uint64_t)(k * 128), id_z,
+                                k > 0 || carry ? 1u : 0u);
+                tc_commit_warp(bar_pv);
+            }
+            if (state && kLate) {
+                ok = wait(late_ready, c);
+                if (!ok) break;
+                tc_fence_after();
+                weighted(L::Kt, 1u);
+                tc_commit_warp(bar_st);
+            }
+            tc_commit_warp(&empty[st]);
+        }
+        if (!ok) fail();
+        // no MMA is in flight when TMEM is freed (also after a failed wait)
+        tc_commit_warp(bar_fin);
+        for (uint32_t i = 0; i < kWaitLimit; ++i)
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar_fin, 0))) break;
+    } else if (warp < 4) {
+        // -------------------------------------------------- token rows ---
+        if constexpr (!STATE_ONLY) {
+            const int i = tid;
+            const uint32_t row = (uint32_t)(warp * 32) << 16;
+            for (int c = 0; c < nch; ++c) {
+                const int nv = chunk_n(c);
+                const bool carry = c > 0 || has_init;
+                const int jlo = rev ? i : 0, jhi = rev ? nv - 1 : i;
+                // columns 32 blk .. 32 blk + 31: 0 masked, 1 on the border, 2 inside
+                auto kind = [&](int blk) {
+                    if (rev ? blk < warp : blk > warp) return 0;
+                    if (blk == warp || (rev && blk * 32 + 32 > nv)) return blk * 32 < nv ? 1 : 0;
+                    return 2;
+                };
+                auto weigh = [&](uint32_t (&s)[32], int blk, int kd) {
+                    const float* w = tab + 127 + blk * 32 - i;
+                    if (kd == 2) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * w[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int col = blk * 32 + j;
+                            s[j] = col >= jlo && col <= jhi ? __float_as_uint(__uint_as_float(s[j]) * w[j]) : 0u;
+                        }
+                    }
+                };
+                if (!wait(bar_s, c)) { fail(); break; }
+                tc_fence_after();
+                float scale = 1.f;
+                if constexpr (F16) {
+                    float amax = 0.f;
+                    for (int blk = 0; blk < 4; ++blk) {
+                        const int kd = kind(blk);
+                        if (kd == 0) continue;
+                        uint32_t s[32];
+                        tmem_ld32(tbase + row + L::S + blk * 32, s);
+                        tc_wait_ld();
+                        weigh(s, blk, kd);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
+                    }
+                    scale = fp16_scale(amax);
+                }
+                for (int blk = 0; blk < 4; ++blk) {
+                    const int kd = kind(blk);
+                    uint32_t pk[16];
+                    if (kd == 0) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) pk[j] = 0u;
+                    } else {
+                        uint32_t s[32];
+                        tmem_ld32(tbase + row + L::S + blk * 32, s);
+                        tc_wait_ld();
+                        weigh(s, blk, kd);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            pk[j] = pack<F16>(__uint_as_float(s[2 * j]) * scale, __uint_as_float(s[2 * j + 1]) * scale);
+                    }
+                    tmem_st16(tbase + row + L::S + blk * 16, pk);
+                }
+                if (!wait(bar_o, c)) { fail(); break; }
+                tc_fence_after();
+                if (carry) {
+                    const int e = min(128, max(0, rev ? nv - 1 - i : i + 1));
+                    float f = r.a_carry * pw[e];
+                    if constexpr (F16) f *= carry_inv[c & 1] * scale;
+                    for (int blk = 0; blk < VP / 32; ++blk) {
+                        uint32_t s[32];
+                        tmem_ld32(tbase + row + L::O + blk * 32, s);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * f);
+                        tmem_st32(tbase + row + L::O + blk * 32, s);
+                    }
+                }
+                tc_wait_st();
+                tc_fence_before();
+                arrive(p_ready);
+                if (!wait(bar_pv, c)) { fail(); break; }
+                tc_fence_after();
+                const float inv = F16 ? 1.f / scale : 1.f;
+                const int64_t at = (int64_t)b * r.out_b + (int64_t)(t0 + chunk_at(c) + i) * r.out_t + (int64_t)h * r.out_h;
+                for (int blk = 0; blk < VP / 32; ++blk) {
+                    uint32_t s[32];
+                    tmem_ld32(tbase + row + L::O + blk * 32, s);
+                    tc_wait_ld();
+                    if (blk == VP / 32 - 1) {
+                        tc_fence_before();
+                        arrive(o_free);
+                    }
+                    if constexpr (F16) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * inv);
+                    }
+                    if (i >= nv) {
+                        // rows behind the sequence's end are not stored
+                    } else if (r.out_f32) {
+                        float* o = reinterpret_cast<float*>(r.out) + at + blk * 32;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            if (blk * 32 + j < r.vd)
+                                *reinterpret_cast<uint4*>(o + j) = make_uint4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+                    } else {
+                        uint16_t* o = reinterpret_cast<uint16_t*>(r.out) + at + blk * 32;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            if (blk * 32 + j < r.vd) {
+                                uint4 v;
+                                v.x = pack<F16>(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+                                v.y = pack<F16>(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
+                                v.z = pack<F16>(__uint_as_float(s[j + 4]), __uint_as_float(s[j + 5]));
+                                v.w = pack<F16>(__uint_as_float(s[j + 6]), __uint_as_float(s[j + 7]));
+                                *reinterpret_cast<uint4*>(o + j) = v;
+                            }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+    } else {
+        // -------------------------------------------------- state rows ---
+        // two warps share 32 rows of the state: each keeps half of the
+        // columns in registers and weighs half of the tokens
+        constexpr int kCols = VP / 2;
+        const int ts = tid - 128, bw = (warp - 4) & 3, half = (warp - 4) >> 2;
+        const int d = bw * 32 + lane;                         // key channel: row of the state
+        const int col0 = half * kCols;
+        const uint32_t row = (uint32_t)(bw * 32) << 16;
+        const bool live = bw * 32 < KP;                       // warp-uniform
+        const int64_t mat = (int64_t)r.kd * r.vd;
+        const int64_t at_seq = ((int64_t)seq * p.H + h) * mat, at_seg = ((int64_t)sid * p.H + h) * mat;
+        float rs = 1.f;                                       // (fp16) power of two on this row's weighted keys
+        uint32_t sync_phase = 0;
+        auto sync_b = [&]() -> bool {                         // bounded barrier of the state warps
+            arrive(wgb_bar);
+            return wait(wgb_bar, sync_phase++);
+        };
+        auto initial = [&](int col) -> float {
+            if (d >= r.kd || col >= r.vd) return 0.f;
+            if (!first) return r.seg[at_seg + (int64_t)d * r.vd + col];
+            return r.init ? r.init[at_seq + (r.init_t ? (int64_t)col * r.kd + d : (int64_t)d * r.vd + col)] : 0.f;
+        };
+        float state[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) state[j] = has_init && live ? initial(col0 + j) : 0.f;
+        // state <- g^n state + (own state of chunk c), once its products are done
+        auto advance = [&](int c) -> bool {
+            if (!wait(bar_st, c)) return false;
+            tc_fence_after();
+            if (live) {
+                const float keep = pw[chunk_n(c)], inv = 1.f / rs;
+#pragma unroll
+                for (int blk = 0; blk < kCols / 32; ++blk) {
+                    uint32_t s[32];
+                    tmem_ld32(tbase + row + L::C + col0 + blk * 32, s);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float own = F16 ? __uint_as_float(s[j]) * inv : __uint_as_float(s[j]);
+                        state[blk * 32 + j] = fmaf(keep, state[blk * 32 + j], own);
+                    }
+                }
+            }
+            return true;
+        };
+        int kw_n = -1;
+        bool ok = true;
+        for (int c = 0; c < nch; ++c) {
+            const int st = c % L::Stages;
+            const int nv = chunk_n(c);
+            const bool carry = c > 0 || has_init;
+            const bool more = c + 1 < nch || want_fin;        // the state behind this chunk is wanted
+            uint8_t* base = smem + st * L::StageBytes;
+            if (more && nv != kw_n) {
+                ok = sync_b();
+                if (!ok) break;
+                if (ts < 128) kw[ts] = ts < nv ? r.key_scale * pw[rev ? ts + 1 : nv - 1 - ts] : 0.f;
+                kw_n = nv;
+                ok = sync_b();
+                if (!ok) break;
+            }
+            if (c > 0) ok = advance(c - 1);
+            if (!ok) break;
+            if constexpr (!STATE_ONLY) {
+                if (carry) {
+                    float cs = 1.f;
+                    if constexpr (F16) {
+                        // common scale of the carry's 16-bit copy, from its largest value
+                        float amax = 0.f;
+#pragma unroll
+                        for (int j = 0; j < kCols; ++j) amax = fmaxf(amax, fabsf(state[j]));
+                        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+                        if (lane == 0) amax_sh[(c & 1) * 8 + warp - 4] = __uint_as_float(top);
+                        ok = sync_b();
+                        if (!ok) break;
+#pragma unroll
+                        for (int w = 0; w < kStateWarps; ++w) amax = fmaxf(amax, amax_sh[(c & 1) * 8 + w]);
+                        cs = fp16_scale(amax);
+                        if (ts == 0) carry_inv[c & 1] = 1.f / cs;
+                    }
+                    if (live) {
+                        uint8_t* dst = smem + L::OffCarry + d * 128;
+#pragma unroll
+                        for (int q = 0; q < kCols / 8; ++q) {
+                            uint4 v;
+                            auto two = [&](int j) { return pack<F16>(state[q * 8 + j] * cs, state[q * 8 + j + 1] * cs); };
+                            v.x = two(0);
+                            v.y = two(2);
+                            v.z = two(4);
+                            v.w = two(6);
+                            const int ch = col0 / 8 + q;
+                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (KP * 128) + (((ch & 7) ^ (d & 7)) << 4)) = v;
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                arrive(carry_ready);
+            }
+            ok = wait(&full[st], c / L::Stages);
+            if (!ok) break;
+            // rows behind a packed sequence belong to another one: their
+            // values must not meet the zeros of P and the weighted keys
+            if (p.cu && nv < kChunk) {
+                const int rows = (nv + 15) / 16 * 16 - nv;
+                for (int e = ts; e < rows * (VP / 8); e += kStateWarps * 32) {
+                    const int rr = nv + e / (VP / 8), ch = e % (VP / 8);
+                    *reinterpret_cast<uint4*>(base + 2 * L::XBytes + (ch >> 3) * 16384 + rr * 128 + (ch & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            // this thread's channel of the keys
+            const uint8_t* kcol = base + L::XBytes + (d >> 6) * 16384 + (d & 7) * 2;
+            const int cb = (d & 63) >> 3;
+            auto key = [&](int j) -> uint32_t {
+                return *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
+            };
+            if (F16 && more && live) {
+                // scale the row so that its largest weighted key is just below 2^15
+                uint32_t m = 0;
+#pragma unroll 16
+                for (int j = 0; j < kChunk; ++j) {
+                    const uint32_t v = key(j) & 0x7fffu;
+                    m = j < nv ? max(m, v) : m;
+                }
+                rs = 1.f;
+                if (m < 0x7c00u)
+                    rs = fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) * fabsf(r.key_scale) *
+                                    fmaxf(1.f, pw[nv]));
+            }
+            uint32_t late[kLate ? 32 : 1];
+            if (more && live) {
+#pragma unroll
+                for (int jb = 0; jb < 4; ++jb) {
+                    uint32_t part[3][8];
+#pragma unroll
+                    for (int j2 = 0; j2 < 8; ++j2) {
+                        const int j = half * 64 + jb * 16 + j2 * 2;
+                        const float2 w = *reinterpret_cast<const float2*>(kw + j);
+                        const float2 kk = unpack<F16>(key(j) | (key(j + 1) << 16));
+                        // a select, not a product: what lies behind the end may be inf or NaN
+                        float f0 = j < nv ? kk.x * w.x : 0.f, f1 = j + 1 < nv ? kk.y * w.y : 0.f;
+                        if constexpr (F16) {
+                            f0 *= rs;
+                            f1 *= rs;
+                        }
+#pragma unroll
+                        for (int q = 0; q < kParts; ++q) {
+                            part[q][j2] = pack<F16>(f0, f1);
+                            const float2 back = unpack<F16>(part[q][j2]);
+                            f0 -= back.x;
+                            f1 -= back.y;
+                        }
+                    }
+                    const uint32_t at = tbase + row + L::Kt + (half * 4 + jb) * 8;
+                    if constexpr (kLate) {
+                        tmem_st8(at, part[2]);
+                        tmem_st8(at + 64, part[1]);
+#pragma unroll
+                        for (int j2 = 0; j2 < 8; ++j2) late[jb * 8 + j2] = part[0][j2];
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < kParts; ++q) tmem_st8(at + q * 64, part[q]);
+                    }
+                }
+            }
+            tc_wait_st();
+            tc_fence_before();
+            arrive(b_ready);
+            if constexpr (kLate) {
+                if (more) {
+                    ok = wait(bar_kt, c);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (live) {
+                        tmem_st16(tbase + row + L::Kt + half * 32, late);
+                        tmem_st16(tbase + row + L::Kt + half * 32 + 16, late + 16);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    arrive(late_ready);
+                }
+            }
+        }
+        if (ok && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
+            float* dst = STATE_ONLY ? r.seg + at_seg : r.fin + at_seq;
+            if (nch > 0)
+                ok = advance(nch - 1);
+            else
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) state[j] = live ? initial(col0 + j) : 0.f;
+            if (ok && d < r.kd && live) {
+#pragma unroll
+                for (int j = 0; j < kCols; j += 4)
+                    if (col0 + j < r.vd)
+                        *reinterpret_cast<float4*>(dst + (int64_t)d * r.vd + col0 + j) =
+                            make_float4(state[j], state[j + 1], state[j + 2], state[j + 3]);
+            }
+        }
+        if (!ok) fail();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// Segment states of split sequences: from each segment's own state (zero
+// start) to the state in front of it, in the role's direction of time.
+__global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params p) {
+    const Role& r = p.role[blockIdx.z];
+    const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    int len = (int)p.T, sid0 = seq * p.nper, count = p.nper;
+    if (p.cu) {
+        __shared__ int before[8];
+        int mine = 0;
+        auto cnt = [&](int i, int& n) {
+            const int a = min(max(p.cu[i], 0), (int)p.T);
+            n = min(max(p.cu[i + 1], a), (int)p.T) - a;
+            return max(1, (n + p.seg_len - 1) / p.seg_len);
+        };
+        for (int i = threadIdx.x; i < seq; i += 256) {
+            int n;
+            mine += cnt(i, n);
+        }
+        mine = __reduce_add_sync(0xffffffffu, mine);
+        if ((threadIdx.x & 31) == 0) before[threadIdx.x >> 5] = mine;
+        __syncthreads();
+        sid0 = 0;
+        for (int i = 0; i < 8; ++i) sid0 += before[i];
+        count = cnt(seq, len);
+    }
+    if (count < 2 || sid0 + count > p.max_seg) return;
+    const int64_t mat = (int64_t)r.kd * r.vd;
+    const int e = blockIdx.y * 256 + threadIdx.x;
+    if (e >= mat) return;
+    const float ld = p.log_decay[h];
+    const float whole = decay_power(ld, (float)p.seg_len);
+    const float tail = decay_power(ld, (float)(len - (count - 1) * p.seg_len));
+    float run = 0.f;
+    if (r.init) {
+        const int row = e / r.vd, col = e % r.vd;
+        run = r.init[((int64_t)seq * p.H + h) * mat + (r.init_t ? col * r.kd + row : e)];
+    }
+    const int64_t step = (int64_t)p.H * mat;
+    float* at = r.seg + ((int64_t)sid0 * p.H + h) * mat + e;
+    // the loads of four segments go out together: their addresses do not
+    // depend on the running state
+    for (int s = 0; s < count; s += 4) {
+        float local[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (s + q < count - 1) local[q] = at[(int64_t)(r.rev ? count - 1 - s - q : s + q) * step];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (s + q >= count) break;
+            const int i = r.rev ? count - 1 - s - q : s + q;
+            at[(int64_t)i * step] = run;
+            if (s + q < count - 1) run = fmaf(i == count - 1 ? tail : whole, run, local[q]);
+        }
+    }
+}
+
+__device__ __forceinline__ void used_tokens(const int32_t* cu, int nseq, int64_t T, int64_t& lo, int64_t& hi) {
+    lo = min((int64_t)max(cu[0], 0), T);
+    hi = min(max((int64_t)cu[nseq], lo), T);
+}
+
+// Gradients of shared heads: the fp32 partial results of a group of heads,
+// summed in order and rounded once.  rows = B * T; VEC elements a thread.
+template <bool F16>
+__global__ void __launch_bounds__(256) la_sum_heads(const float* part, uint16_t* out, int64_t rows, int Hx, int rep,
+                                                    int D, const int32_t* cu, int nseq) {
+    const int64_t per_row = (int64_t)Hx * (D / 4);
+    int64_t lo = 0, hi = rows;
+    if (cu) used_tokens(cu, nseq, rows, lo, hi);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * per_row; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / per_row, x = i % per_row;
+        const int hx = (int)(x / (D / 4)), d = (int)(x % (D / 4)) * 4;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row >= lo && row < hi) {
+            const float* src = part + (row * Hx * rep + (int64_t)hx * rep) * D + d;
+            for (int j = 0; j < rep; ++j) {
+                const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)j * D);
+                sum.x += v.x;
+                sum.y += v.y;
+                sum.z += v.z;
+                sum.w += v.w;
+            }
+        }
+        uint2 v;
+        v.x = pack<F16>(sum.x, sum.y);
+        v.y = pack<F16>(sum.z, sum.w);
+        *reinterpret_cast<uint2*>(out + (row * Hx + hx) * D + d) = v;
+    }
+}
+
+// Zero the rows of tokens that no packed sequence holds.
+__global__ void __launch_bounds__(256) la_zero_rest(uint16_t* out, int64_t T, int H, int D, int64_t st, int64_t sh,
+                                                    const int32_t* cu, int nseq) {
+    int64_t lo, hi;
+    used_tokens(cu, nseq, T, lo, hi);
+    const int64_t per_row = (int64_t)H * (D / 8), count = (lo + T - hi) * per_row;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < count; i += (int64_t)gridDim.x * 256) {
+        int64_t t = i / per_row;
+        const int64_t x = i % per_row;
+        if (t >= lo) t += hi - lo;
+        *reinterpret_cast<uint4*>(out + t * st + x / (D / 8) * sh + x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// ------------------------------------------------------------------ host ---
+
+int fail(int status, const std::string& msg) {
+    set_last_error(msg.c_str());
+    return status;
+}
+int cuda_fail(cudaError_t e, const char* what) {
+    return fail(FFTCONV_ERR_CUDA, std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+    static const EncodeTiled fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult got;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &got) !=
+                cudaSuccess ||
+            got != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeTiled>(f);
+    }();
+    return fn;
+}
+
+// [B, T, H, D] with element strides: tiles of 128 tokens x 64 channels of one
+// head, rows of 128 bytes in the 128-byte swizzle; what lies outside is zero.
+int make_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64_t T, int64_t H, int64_t D,
+             const int64_t* stride) {
+    // the encoder is a driver call: it needs the device's context bound to
+    // this thread, which autograd's threads have not done before their first
+    // runtime call
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)
+        return fail(FFTCONV_ERR_CUDA, "no current device");
+    const EncodeTiled fn = encode_tiled();
+    if (!fn) return fail(FFTCONV_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
+    auto bytes = [](int64_t extent, int64_t s) { return (cuuint64_t)(extent > 1 ? s * 2 : 16); };
+    const cuuint64_t strides[3] = {bytes(H, stride[2]), bytes(T, stride[1]), bytes(B, stride[0])};
+    const cuuint32_t box[4] = {64, 1, kChunk, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult e = fn(m, dtype == FFTCONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                          4, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (e != CUDA_SUCCESS) return fail(FFTCONV_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)e));
+    return FFTCONV_OK;
+}
+
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) n = 148;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+template <int KP, int VP, bool F16, bool STATE_ONLY>
+cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};                    // devices whose kernel has its shared memory size
+    auto* kern = la_kernel<KP, VP, F16, STATE_ONLY>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<KP, VP>::Bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    }
+    void* args[] = {const_cast<Params*>(&p)};
+    return cudaLaunchKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(kThreads), args,
+                            Layout<KP, VP>::Bytes, s);
+}
+
+template <bool STATE_ONLY>
+cudaError_t launch_kernel(const Params& p, bool f16, int kp, int vp, int64_t ctas, cudaStream_t s) {
+    const int which = (kp == 128 ? 4 : 0) + (vp == 128 ? 2 : 0) + (f16 ? 1 : 0);
+    switch (which) {
+        case 0: return launch<64, 64, false, STATE_ONLY>(p, ctas, s);
+        case 1: return launch<64, 64, true, STATE_ONLY>(p, ctas, s);
+        case 2: return launch<64, 128, false, STATE_ONLY>(p, ctas, s);
+        case 3: return launch<64, 128, true, STATE_ONLY>(p, ctas, s);
+        case 4: return launch<128, 64, false, STATE_ONLY>(p, ctas, s);
+        case 5: return launch<128, 64, true, STATE_ONLY>(p, ctas, s);
+        case 6: return launch<128, 128, false, STATE_ONLY>(p, ctas, s);
+        default: return launch<128, 128, true, STATE_ONLY>(p, ctas, s);
+    }
+}
+
+// How a call's sequences are cut into segments, one CTA for each (segment,
+// head, role).
+struct Split {
+    int64_t seg_len, nper, max_seg;           // nper: segments of a sequence (unpacked)
+    bool on;
+};
+
+// A sequence is one CTA's serial walk, so few sequences x heads leave SMs
+// idle; cutting along time costs a second pass over keys and values (the
+// segments' own states) and the states' round trip.  It pays where one walk
+// takes over 1.6 times what an even share of all tokens would.
+Split split_of(const fftconv_linear_attention_t& d, int nroles) {
+    const int64_t sms = sm_count(), seqs = d.nseq > 0 ? d.nseq : d.B;
+    const int64_t tasks = seqs * d.H * nroles;
+    auto up = [](int64_t x) { return (x + kChunk - 1) / kChunk * kChunk; };
+    Split s{up(d.T), 1, seqs, false};
+    int64_t len;
+    if (d.nseq > 0) {
+        // lengths are known on the device only
+        const int64_t share = (d.T * d.H * nroles + sms - 1) / sms;
+        len = up(share + share * 3 / 5);
+    } else {
+        const int64_t share = (d.B * d.T * d.H * nroles + sms - 1) / sms;
+        if (d.T * ((tasks + sms - 1) / sms) <= share + share * 3 / 5 + 4 * kChunk) return s;
+        const int64_t pieces = sms / tasks < 2 ? 2 : sms / tasks;
+        len = up((d.T + pieces - 1) / pieces);
+    }
+    if (len < 4 * kChunk) len = 4 * kChunk;
+    if (len >= d.T) return s;
+    s.seg_len = len;
+    s.nper = (d.T + len - 1) / len;
+    s.max_seg = d.nseq > 0 ? d.T / len + d.nseq : d.B * s.nper;
+    s.on = true;
+    return s;
+}
+
+int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
+
+int check_shape(const fftconv_linear_attention_t* d) {
+    if (!d) return fail(FFTCONV_ERR_INVALID_ARG, "shape is NULL");
+    if (d->B < 0 || d->T < 0 || d->nseq < 0) return fail(FFTCONV_ERR_INVALID_ARG, "B, T or nseq is negative");
+    if (d->H <= 0 || d->Hq <= 0 || d->Hk <= 0 || d->Hv <= 0 || d->H % d->Hq || d->H % d->Hk || d->H % d->Hv)
+        return fail(FFTCONV_ERR_INVALID_ARG, "Hq, Hk and Hv must be positive and divide H");
+    if (d->dtype != FFTCONV_F16 && d->dtype != FFTCONV_BF16)
+        return fail(d->dtype == FFTCONV_F32 ? FFTCONV_ERR_UNSUPPORTED : FFTCONV_ERR_INVALID_ARG,
+                    "linear attention takes fp16 or bf16 tensors");
+    if (d->K <= 0 || d->V <= 0) return fail(FFTCONV_ERR_INVALID_ARG, "K and V must be positive");
+    if (d->K % 8 || d->V % 8 || d->K > 128 || d->V > 128)
+        return fail(FFTCONV_ERR_UNSUPPORTED, "K and V must be multiples of 8 up to 128");
+    if (d->nseq > 0 && d->B != 1) return fail(FFTCONV_ERR_INVALID_ARG, "packed sequences need B = 1");
+    if (d->T >= (int64_t(1) << 31) - 256 || d->B >= (int64_t(1) << 31) || d->H >= 65536 || d->nseq >= (1 << 24))
+        return fail(FFTCONV_ERR_UNSUPPORTED, "B, T, H or nseq too large");
+    const double seqs = d->nseq > 0 ? (double)d->nseq : (double)d->B;
+    if (seqs * (double)d->H * 3.0 + (double)d->B * (double)d->T * (double)d->H * 3.0 / 512.0 >= 2147483647.0)
+        return fail(FFTCONV_ERR_UNSUPPORTED, "too many sequences and heads for one launch");
+    return FFTCONV_OK;
+}
+
+int check_stride(const char* name, const int64_t* s, int64_t B, int64_t T, int64_t H) {
+    const int64_t extent[3] = {B, T, H};
+    for (int i = 0; i < 3; ++i)
+        if (extent[i] > 1 && (s[i] <= 0 || s[i] % 8 || s[i] >= (int64_t(1) << 38)))
+            return fail(FFTCONV_ERR_ALIGNMENT,
+                        std::string(name) + ": strides must be positive multiples of 8 elements (16 bytes)");
+    return FFTCONV_OK;
+}
+
+// The elements a strided tensor spans.
+int64_t span(const int64_t* s, int64_t B, int64_t T, int64_t H, int64_t D) {
+    return (B - 1) * (B > 1 ? s[0] : 0) + (T - 1) * (T > 1 ? s[1] : 0) + (H - 1) * (H > 1 ? s[2] : 0) + D;
+}
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+    if (!a || !b || na <= 0 || nb <= 0) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+size_t workspace_bytes(const fftconv_linear_attention_t& d, bool backward) {
+    if (d.B == 0 || d.T == 0) return 0;
+    const int nroles = backward ? 3 : 1;
+    const Split s = split_of(d, nroles);
+    int64_t n = 0;
+    if (s.on) n += nroles * pad256(s.max_seg * d.H * d.K * d.V * 4);
+    if (backward) {
+        if (d.Hq < d.H) n += pad256(d.T * d.B * d.H * d.K * 4);
+        if (d.Hk < d.H) n += pad256(d.T * d.B * d.H * d.K * 4);
+        if (d.Hv < d.H) n += pad256(d.T * d.B * d.H * d.V * 4);
+    }
+    return (size_t)n;
+}
+
+void fill(Params& p, const fftconv_linear_attention_t& d, const Split& s, const float* log_decay, const int32_t* cu,
+          int nroles) {
+    p.log_decay = log_decay;
+    p.cu = d.nseq > 0 ? cu : nullptr;
+    p.T = d.T;
+    p.nroles = nroles;
+    p.H = (int)d.H;
+    p.nseq = (int)d.nseq;
+    p.nper = (int)s.nper;
+    p.seg_len = (int)s.seg_len;
+    p.max_seg = (int)s.max_seg;
+}
+
+// The launches of up to three roles of one padded shape.
+cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, const Split& s, cudaStream_t stream) {
+    const Role& r = p.role[0];
+    const int kp = r.kd > 64 ? 128 : 64, vp = r.vd > 64 ? 128 : 64;
+    const bool f16 = d.dtype == FFTCONV_F16;
+    const int64_t ctas = s.max_seg * d.H * p.nroles;
+    if (s.on) {
+        cudaError_t e = launch_kernel<true>(p, f16, kp, vp, ctas, stream);
+        if (e != cudaSuccess) return e;
+        const int64_t seqs = d.nseq > 0 ? d.nseq : d.B;
+        void* args[] = {const_cast<Params*>(&p)};
+        e = cudaLaunchKernel(reinterpret_cast<const void*>(la_combine),
+                             dim3((unsigned)(seqs * d.H), (unsigned)((d.K * d.V + 255) / 256), (unsigned)p.nroles),
+                             dim3(256), args, 0, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel<false>(p, f16, kp, vp, ctas, stream);
+}
+
+cudaError_t copy_states(float* dst, const float* src, int64_t count, cudaStream_t s) {
+    if (!dst || !count || dst == src) return cudaSuccess;
+    if (src) return cudaMemcpyAsync(dst, src, (size_t)count * 4, cudaMemcpyDeviceToDevice, s);
+    return cudaMemsetAsync(dst, 0, (size_t)count * 4, s);
+}
+
+cudaError_t zero_rest(void* out, const fftconv_linear_attention_t& d, int64_t H, int64_t D, const int64_t* st,
+                      const int32_t* cu, cudaStream_t s) {
+    const int64_t blocks = (d.T * H * D / 8 + 255) / 256;
+    la_zero_rest<<<(unsigned)(blocks < 592 ? blocks : 592), 256, 0, s>>>((uint16_t*)out, d.T, (int)H, (int)D, st[1],
+                                                                        st[2], cu, (int)d.nseq);
+    return cudaPeekAtLastError();
+}
+
+}  // namespace
+}  // namespace fftconv
+
+using namespace fftconv;
+
+extern "C" {
+
+size_t fftconv_linear_attention_workspace_bytes(const fftconv_linear_attention_t* shape, int backward) {
+    if (check_shape(shape) != FFTCONV_OK) return 0;
+    return workspace_bytes(*shape, backward != 0);
+}
+
+int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void* q, const void* k, const void* v,
+                             const float* log_decay, const float* initial_state, const int32_t* cu_seqlens, void* o,
+                             float* final_state, void* workspace, size_t workspace_size, fftconv_stream_t stream) {
+    set_last_error("");
+    if (int e = check_shape(shape)) return e;
+    const fftconv_linear_attention_t& d = *shape;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int64_t seqs = d.nseq > 0 ? d.nseq : d.B, states = seqs * d.H * d.K * d.V;
+    if (d.nseq > 0 && !cu_seqlens) return fail(FFTCONV_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    if (d.nseq == 0 && cu_seqlens) return fail(FFTCONV_ERR_INVALID_ARG, "cu_seqlens given with nseq = 0");
+    if (seqs == 0) return FFTCONV_OK;
+    if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARG, "log_decay is NULL");
+    if (!aligned16(initial_state) || !aligned16(final_state))
+        return fail(FFTCONV_ERR_ALIGNMENT, "states must be 16-byte aligned");
+    if (final_state != initial_state && overlap(final_state, states * 4, initial_state, states * 4))
+        return fail(FFTCONV_ERR_INVALID_ARG, "final_state overlaps initial_state");
+    if (d.T == 0) {
+        const cudaError_t e = copy_states(final_state, initial_state, states, s);
+        return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "state copy");
+    }
+    if (!q || !k || !v || !o) return fail(FFTCONV_ERR_INVALID_ARG, "q, k, v and o must be non-NULL");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+        return fail(FFTCONV_ERR_ALIGNMENT, "q, k, v and o must be 16-byte aligned");
+    if (int e = check_stride("q", d.q_stride, d.B, d.T, d.Hq)) return e;
+    if (int e = check_stride("k", d.k_stride, d.B, d.T, d.Hk)) return e;
+    if (int e = check_stride("v", d.v_stride, d.B, d.T, d.Hv)) return e;
+    if (int e = check_stride("o", d.o_stride, d.B, d.T, d.H)) return e;
+    const int64_t no = span(d.o_stride, d.B, d.T, d.H, d.V) * 2;
+    if (overlap(o, no, q, span(d.q_stride, d.B, d.T, d.Hq, d.K) * 2) ||
+        overlap(o, no, k, span(d.k_stride, d.B, d.T, d.Hk, d.K) * 2) ||
+        overlap(o, no, v, span(d.v_stride, d.B, d.T, d.Hv, d.V) * 2) || overlap(o, no, initial_state, states * 4) ||
+        overlap(o, no, final_state, states * 4))
+        return fail(FFTCONV_ERR_INVALID_ARG, "o overlaps another tensor");
+    const Split sp = split_of(d, 1);
+    const size_t need = workspace_bytes(d, false);
+    if (need && (!workspace || workspace_size < need))
+        return fail(FFTCONV_ERR_INVALID_ARG, "workspace of " + std::to_string(workspace_size) + " bytes, " +
+                                                 std::to_string(need) + " needed");
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return fail(FFTCONV_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+
+    Params p{};
+    fill(p, d, sp, log_decay, cu_seqlens, 1);
+    if (int e = make_map(&p.maps[0], q, d.dtype, d.B, d.T, d.Hq, d.K, d.q_stride)) return e;
+    if (int e = make_map(&p.maps[1], k, d.dtype, d.B, d.T, d.Hk, d.K, d.k_stride)) return e;
+    if (int e = make_map(&p.maps[2], v, d.dtype, d.B, d.T, d.Hv, d.V, d.v_stride)) return e;
+    Role& r = p.role[0];
+    r.x = 0; r.y = 1; r.z = 2;
+    r.x_div = (int)(d.H / d.Hq); r.y_div = (int)(d.H / d.Hk); r.z_div = (int)(d.H / d.Hv);
+    r.kd = (int)d.K; r.vd = (int)d.V;
+    r.a_in = r.a_carry = d.scale;
+    r.key_scale = 1.f;
+    r.out = o;
+    r.out_b = d.o_stride[0]; r.out_t = d.o_stride[1]; r.out_h = d.o_stride[2];
+    r.init = initial_state;
+    r.fin = final_state;
+    r.seg = (float*)workspace;
+    cudaError_t e = cudaSuccess;
+    if (d.nseq > 0 && d.zero_rest) e = zero_rest(o, d, d.H, d.V, d.o_stride, cu_seqlens, s);
+    if (e == cudaSuccess) e = run_roles(p, d, sp, s);
+    return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "linear attention launch");
+}
+
+int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, const void* q, const void* k,
+                                      const void* v, const float* log_decay, const float* initial_state,
+                                      const int32_t* cu_seqlens, const void* do_, const float* dfinal, void* dq,
+                                      void* dk, void* dv, float* dinitial, void* workspace, size_t workspace_size,
+                                      fftconv_stream_t stream) {
+    set_last_error("");
+    if (int e = check_shape(shape)) return e;
+    const fftconv_linear_attention_t& d = *shape;
+    cudaStream_t s = (cudaStream_t)stream;
+    const int64_t seqs = d.nseq > 0 ? d.nseq : d.B, states = seqs * d.H * d.K * d.V;
+    if (d.nseq > 0 && !cu_seqlens) return fail(FFTCONV_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    if (d.nseq == 0 && cu_seqlens) return fail(FFTCONV_ERR_INVALID_ARG, "cu_seqlens given with nseq = 0");
+    if (seqs == 0) return FFTCONV_OK;
+    if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARG, "log_decay is NULL");
+    if (!aligned16(initial_state) || !aligned16(dfinal) || !aligned16(dinitial))
+        return fail(FFTCONV_ERR_ALIGNMENT, "states must be 16-byte aligned");
+    if (dinitial != dfinal && overlap(dinitial, states * 4, dfinal, states * 4))
+        return fail(FFTCONV_ERR_INVALID_ARG, "dinitial overlaps dfinal");
+    if (d.T == 0) {
+        const cudaError_t e = copy_states(dinitial, dfinal, states, s);
+        return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "state copy");
+    }
+    if (!q || !k || !v || !do_ || !dq || !dk || !dv)
+        return fail(FFTCONV_ERR_INVALID_ARG, "q, k, v, do_, dq, dk and dv must be non-NULL");
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(do_) || !aligned16(dq) || !aligned16(dk) ||
+        !aligned16(dv))
+        return fail(FFTCONV_ERR_ALIGNMENT, "tensors must be 16-byte aligned");
+    if (int e = check_stride("q", d.q_stride, d.B, d.T, d.Hq)) return e;
+    if (int e = check_stride("k", d.k_stride, d.B, d.T, d.Hk)) return e;
+    if (int e = check_stride("v", d.v_stride, d.B, d.T, d.Hv)) return e;
+    if (int e = check_stride("do_", d.o_stride, d.B, d.T, d.H)) return e;
+    const int64_t tok = d.B * d.T;
+    {
+        const void* in[6] = {q, k, v, do_, initial_state, dfinal};
+        const int64_t nin[6] = {span(d.q_stride, d.B, d.T, d.Hq, d.K) * 2, span(d.k_stride, d.B, d.T, d.Hk, d.K) * 2,
+                                span(d.v_stride, d.B, d.T, d.Hv, d.V) * 2, span(d.o_stride, d.B, d.T, d.H, d.V) * 2,
+                                states * 4, states * 4};
+        const void* out[4] = {dq, dk, dv, dinitial};
+        const int64_t nout[4] = {tok * d.Hq * d.K * 2, tok * d.Hk * d.K * 2, tok * d.Hv * d.V * 2, states * 4};
+        for (int i = 0; i < 4; ++i) {
+            for (int j = 0; j < 6; ++j)
+                if (!(i == 3 && j == 5) && overlap(out[i], nout[i], in[j], nin[j]))
+                    return fail(FFTCONV_ERR_INVALID_ARG, "a gradient overlaps an input");
+            for (int j = 0; j < i; ++j)
+                if (overlap(out[i], nout[i], out[j], nout[j]))
+                    return fail(FFTCONV_ERR_INVALID_ARG, "two gradients overlap");
+        }
+    }
+    const Split sp = split_of(d, 3);
+    const size_t need = workspace_bytes(d, true);
+    if (need && (!workspace || workspace_size < need))
+        return fail(FFTCONV_ERR_INVALID_ARG, "workspace of " + std::to_string(workspace_size) + " bytes, " +
+                                                 std::to_string(need) + " needed");
+    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return fail(FFTCONV_ERR_ALIGNMENT, "workspace not 256-byte aligned");
+
+    uint8_t* ws = (uint8_t*)workspace;
+    auto take = [&](int64_t bytes) {
+        uint8_t* at = ws;
+        ws += pad256(bytes);
+        return at;
+    };
+    float* seg[3] = {nullptr, nullptr, nullptr};
+    if (sp.on)
+        for (int i = 0; i < 3; ++i) seg[i] = (float*)take(sp.max_seg * d.H * d.K * d.V * 4);
+    float* part[3] = {nullptr, nullptr, nullptr};
+    if (d.Hq < d.H) part[0] = (float*)take(tok * d.H * d.K * 4);
+    if (d.Hk < d.H) part[1] = (float*)take(tok * d.H * d.K * 4);
+    if (d.Hv < d.H) part[2] = (float*)take(tok * d.H * d.V * 4);
+
+    Params p{};
+    fill(p, d, sp, log_decay, cu_seqlens, 3);
+    if (int e = make_map(&p.maps[0], q, d.dtype, d.B, d.T, d.Hq, d.K, d.q_stride)) return e;
+    if (int e = make_map(&p.maps[1], k, d.dtype, d.B, d.T, d.Hk, d.K, d.k_stride)) return e;
+    if (int e = make_map(&p.maps[2], v, d.dtype, d.B, d.T, d.Hv, d.V, d.v_stride)) return e;
+    if (int e = make_map(&p.maps[3], do_, d.dtype, d.B, d.T, d.H, d.V, d.o_stride)) return e;
+    const int div[4] = {(int)(d.H / d.Hq), (int)(d.H / d.Hk), (int)(d.H / d.Hv), 1};
+    void* out[3] = {dq, dk, dv};
+    const int64_t heads[3] = {d.Hq, d.Hk, d.Hv}, dims[3] = {d.K, d.K, d.V};
+    const int sides[3][3] = {{3, 2, 1}, {2, 3, 0}, {1, 0, 3}};
+    for (int i = 0; i < 3; ++i) {
+        Role& r = p.role[i];
+        r.x = sides[i][0]; r.y = sides[i][1]; r.z = sides[i][2];
+        r.x_div = div[r.x]; r.y_div = div[r.y]; r.z_div = div[r.z];
+        r.rev = i > 0;
+        r.kd = (int)(i < 2 ? d.V : d.K);
+        r.vd = (int)dims[i];
+        r.a_in = d.scale;
+        r.a_carry = i == 0 ? d.scale : 1.f;
+        r.key_scale = i == 0 ? 1.f : d.scale;
+        r.init = i == 0 ? initial_state : dfinal;
+        r.init_t = i < 2;
+        r.fin = i == 2 ? dinitial : nullptr;
+        r.seg = seg[i];
+        r.out_f32 = part[i] != nullptr;
+        r.out = part[i] ? (void*)part[i] : out[i];
+        const int64_t hh = part[i] ? d.H : heads[i];
+        r.out_h = dims[i];
+        r.out_t = hh * dims[i];
+        r.out_b = d.T * hh * dims[i];
+    }
+    cudaError_t e = cudaSuccess;
+    if (d.nseq > 0)
+        for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+            const int64_t st[3] = {0, heads[i] * dims[i], dims[i]};
+            if (!part[i]) e = zero_rest(out[i], d, heads[i], dims[i], st, cu_seqlens, s);
+        }
+    if (e == cudaSuccess) {
+        if ((d.K > 64) == (d.V > 64)) {
+            e = run_roles(p, d, sp, s);
+        } else {
+            // dq and dk have the dims (V, K), dv has (K, V): two padded shapes
+            Params a = p;
+            a.nroles = 2;
+            e = run_roles(a, d, sp, s);
+            if (e == cudaSuccess) {
+                a.nroles = 1;
+                a.role[0] = p.role[2];
+                e = run_roles(a, d, sp, s);
+            }
+        }
+    }
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+        if (!part[i]) continue;
+        const int64_t work = (tok * heads[i] * (dims[i] / 4) + 255) / 256;
+        const unsigned grid = (unsigned)(work < 148 * 32 ? work : 148 * 32);
+        const int rep = (int)(d.H / heads[i]);
+        const int32_t* cu = d.nseq > 0 ? cu_seqlens : nullptr;
+        if (d.dtype == FFTCONV_F16)
+            la_sum_heads<true><<<grid, 256, 0, s>>>(part[i], (uint16_t*)out[i], tok, (int)heads[i], rep, (int)dims[i],
+                                                    cu, (int)d.nseq);
+        else
+            la_sum_heads<false><<<grid, 256, 0, s>>>(part[i], (uint16_t*)out[i], tok, (int)heads[i], rep,
+                                                     (int)dims[i], cu, (int)d.nseq);
+        e = cudaPeekAtLastError();
+    }
+    return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "linear attention backward launch");
+}
+
+int fftconv_linear_attention_status(fftconv_stream_t stream) {
+    set_last_error("");
+    cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+    int st = 0;
+    const int zero = 0;
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbolAsync(&st, g_status, sizeof(int), 0, cudaMemcpyDeviceToHost, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaMemcpyToSymbolAsync(g_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "linear attention status");
+    return st;
+}
+
+}  // extern "C"
