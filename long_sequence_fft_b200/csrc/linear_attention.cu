@@ -36,8 +36,6 @@ using namespace tc;
 
 constexpr int kChunk = 128;                   // tokens of a chunk: the rows of one MMA
 constexpr int kStateWarps = 8;
-constexpr int kLoadWarp = 4 + kStateWarps, kMmaWarp = kLoadWarp + 1;
-constexpr int kThreads = (kMmaWarp + 1) * 32; // 4 warps rows, 8 warps state, loads, MMA issue
 constexpr uint32_t kWaitLimit = 1u << 20;
 constexpr int kMaxRoles = 3;
 
@@ -189,30 +187,57 @@ __device__ __forceinline__ float fp16_scale(float amax) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 template <int KP, int VP>
 struct Layout {
+    // the weighted keys: in shared memory (64 channels), or, where the tiles
+    // leave no room, transposed in TMEM
+    static constexpr bool KtSmem = KP == 64;
+    // groups of row warps, which take chunks in turn, each with a score tile;
+    // TMEM has room for one at 128 x 128
+    static constexpr int Groups = KP == 128 && VP == 128 ? 1 : 2;
+    static constexpr int OutBufs = KP == 64 && VP == 64 ? 2 : 1;
+    static constexpr int RowWarps = 4 * Groups;
+    static constexpr int LoadWarp = RowWarps + kStateWarps, MmaWarp = LoadWarp + 1, StateMmaWarp = LoadWarp + 2;
+    static constexpr int Threads = (RowWarps + kStateWarps + 3) * 32;
     static constexpr int XBytes = KP * kChunk * 2, ZBytes = VP * kChunk * 2;
     static constexpr int StageBytes = 2 * XBytes + ZBytes;
+    static constexpr int KtBytes = KtSmem ? 3 * XBytes : 0;
     static constexpr int CarryBytes = KP * VP * 2;
-    static constexpr int Stages = StageBytes <= 49152 ? 4 : StageBytes <= 65536 ? 3 : 2;
-    static constexpr int OffCarry = Stages * StageBytes;
+    static constexpr int Stages = StageBytes <= 49152 ? 3 : 2;
+    static constexpr int OffStage = KtBytes;
+    static constexpr int OffCarry = OffStage + Stages * StageBytes;
     static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d|, d = j - i in [-127, 127]
     static constexpr int OffPow = OffTab + 256 * 4;           // g^e, e <= 128
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
-    static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, scales, TMEM base
-    static constexpr int OffBar = OffMisc + 112;
-    static constexpr int Bytes = OffBar + (2 * Stages + 12) * 8;
+    static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, TMEM base, scales
+    static constexpr int OffBar = OffMisc + 128;
+    static constexpr int OffScale = OffBar + 32 * 8;          // (fp16, KtSmem) channel scales and their maxima
+    static constexpr int Bytes = OffScale + (KtSmem ? KP * 4 + kStateWarps * KP * 2 : 0);
     // TMEM columns
-    static constexpr int S = 0, O = 128, C = O + VP, Kt = C + VP;
-    static constexpr int KtParts = (512 - Kt) / 64;           // parts that have columns of their own
+    static constexpr int S = 0, O = Groups * 128, C = O + OutBufs * VP, Kt = C + VP;
     static_assert(Bytes <= 232448, "shared memory");
-    static_assert(KtParts >= 2, "TMEM columns");
+    static_assert(Kt + (KtSmem ? 0 : 128) <= 512, "TMEM columns");
 };
 
-// One CTA: one (segment, head, role).  Warps 0-3 own the token rows (P, the
-// output), warps 4-11 the rows of the state (kept in registers: its decay, its
-// 16-bit copy for the next product, the weighted keys), warp 12 issues the
-// loads, warp 13 the MMAs.
+// One CTA: one (segment, head, role).  Row warps (one or two groups of four
+// that take chunks in turn) own the token rows: P and the output.  Eight
+// state warps keep the state in registers (its decay, its 16-bit copy for the
+// next product) and weigh the keys.  One warp issues the loads, one the MMAs
+// of the rows (scores, carry product, P z), one those of the chunk's own
+// state.  Only the carry product waits for the state, so chunks overlap.
 //
 // Rounding: P and the carry's copy are rounded once to the 16-bit type (their
 // products are the two halves of the output, each with the error of one
@@ -222,33 +247,36 @@ struct Layout {
 // by its largest value, the weighted keys by channel), so that nothing
 // overflows fp16's range or falls below it.
 template <int KP, int VP, bool F16, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __grid_constant__ Params p) {
     using L = Layout<KP, VP>;
     constexpr int kParts = F16 ? 2 : 3;
-    constexpr bool kLate = kParts > L::KtParts;               // the last part waits for part 0's columns
+    constexpr int NA = L::Groups;
+    constexpr bool kLate = !L::KtSmem && kParts == 3;         // the last part waits for the first one's columns
     extern __shared__ __align__(1024) uint8_t smem[];
     float* tab = reinterpret_cast<float*>(smem + L::OffTab);
     float* pw = reinterpret_cast<float*>(smem + L::OffPow);
     float* kw = reinterpret_cast<float*>(smem + L::OffKw);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::OffMisc);
-    volatile int* abort_flag = misc + 7;
-    volatile float* carry_inv = reinterpret_cast<volatile float*>(misc + 8);      // [2] by chunk parity
-    volatile float* amax_sh = reinterpret_cast<volatile float*>(misc + 10);       // [2][8]
-    uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(smem + L::OffMisc + 4 * 26);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::OffBar);
-    uint64_t* empty = full + L::Stages;
-    uint64_t* bar_s = empty + L::Stages;
-    uint64_t* bar_o = bar_s + 1;
-    uint64_t* bar_pv = bar_s + 2;
-    uint64_t* bar_st = bar_s + 3;
-    uint64_t* bar_kt = bar_s + 4;
-    uint64_t* carry_ready = bar_s + 5;
-    uint64_t* b_ready = bar_s + 6;
-    uint64_t* p_ready = bar_s + 7;
-    uint64_t* o_free = bar_s + 8;
-    uint64_t* late_ready = bar_s + 9;
-    uint64_t* wgb_bar = bar_s + 10;
-    uint64_t* bar_fin = bar_s + 11;
+    volatile int* abort_flag = misc + 6;
+    uint32_t* tmem_sh = reinterpret_cast<uint32_t*>(smem + L::OffMisc) + 7;
+    volatile float* carry_inv = reinterpret_cast<volatile float*>(misc + 8);      // [4] by chunk
+    volatile float* amax_sh = reinterpret_cast<volatile float*>(misc + 12);       // [2][8]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OffBar);
+    uint64_t* full = bars;                                    // [Stages] loads
+    uint64_t* empty = bars + 3;                               // [Stages] both MMA warps are done with a stage
+    uint64_t* bar_s = bars + 6;                               // [Groups] scores
+    uint64_t* bar_o = bars + 8;                               // [Groups] carry product
+    uint64_t* bar_pv = bars + 10;                             // [Groups] output
+    uint64_t* p_ready = bars + 12;                            // [Groups] P written, carry product weighted
+    uint64_t* o_free = bars + 14;                             // [Groups] output read
+    uint64_t* bar_st = bars + 16;                             // the chunk's own state
+    uint64_t* bar_kt = bars + 17;                             // its first parts (late only)
+    uint64_t* kt_ready = bars + 18;
+    uint64_t* late_ready = bars + 19;
+    uint64_t* carry_ready = bars + 20;
+    uint64_t* z_ready = bars + 21;                            // rows behind a packed sequence zeroed
+    uint64_t* wgb_bar = bars + 22;
+    uint64_t* bar_fin = bars + 23;                            // [2]
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -269,22 +297,26 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
             misc[4] = s.t0;
             misc[5] = s.b;
         }
-    } else if (warp == kLoadWarp && lane == 0) {
-        for (int i = 0; i < L::Stages; ++i) {
+    } else if (warp == L::LoadWarp && lane == 0) {
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], STATE_ONLY ? 1 : 2);
         }
-        for (int i = 0; i < 5; ++i) mbar_init(bar_s + i, 1);
-        for (int i = 5; i < 11; ++i) mbar_init(bar_s + i, bar_s + i == p_ready || bar_s + i == o_free ? 4 : kStateWarps);
-        mbar_init(bar_fin, 1);
+        for (int i = 6; i < 12; ++i) mbar_init(bars + i, 1);
+        for (int i = 12; i < 16; ++i) mbar_init(bars + i, 4);
+        mbar_init(bar_st, 1);
+        mbar_init(bar_kt, 1);
+        for (int i = 18; i < 23; ++i) mbar_init(bars + i, kStateWarps);
+        mbar_init(&bar_fin[0], 1);
+        mbar_init(&bar_fin[1], 1);
         *abort_flag = 0;
         fence_barrier_init();
-    } else if (warp == kMmaWarp) {
+    } else if (warp == L::MmaWarp) {
         tmem_alloc(tmem_sh, 512);
         tmem_relinquish();
-    } else if (warp >= 4 && warp < 8) {
+    } else if (warp >= L::RowWarps && warp < L::RowWarps + 4) {
         const float ld = p.log_decay[h];
-        const int i = tid - 128;
+        const int i = tid - L::RowWarps * 32;
         const float w = decay_power(ld, (float)i);
         pw[i] = w;
         if (i == 127) pw[128] = decay_power(ld, 128.f);
@@ -302,8 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
     const bool has_init = !STATE_ONLY && (first ? r.init != nullptr : true);
     const bool want_fin = STATE_ONLY || (last && r.fin != nullptr);
 
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity & 1, abort_flag, kWaitLimit));
+    auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1, abort_flag, kWaitLimit));
     };
     auto fail = [&]() {
         *abort_flag = 1;
@@ -316,8 +348,10 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
     // chunk c of the role's direction: its first token and number of tokens
     auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kChunk; };
     auto chunk_n = [&](int c) { return min(kChunk, n - chunk_at(c)); };
+    constexpr uint32_t kFmt = F16 ? 0u : (1u << 7) | (1u << 10);
+    constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;
 
-    if (warp == kLoadWarp) {
+    if (warp == L::LoadWarp) {
         // ------------------------------------------------------- loads ---
         if (lane == 0 && nch > 0) {
             const CUtensorMap *mx = &p.maps[r.x], *my = &p.maps[r.y], *mz = &p.maps[r.z];
@@ -330,12 +364,12 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                     fail();
                     break;
                 }
-                uint8_t* base = smem + st * L::StageBytes;
+                uint8_t* base = smem + L::OffStage + st * L::StageBytes;
                 const int t = t0 + chunk_at(c);
                 mbar_expect_tx(&full[st], STATE_ONLY ? L::StageBytes - L::XBytes : L::StageBytes);
+                for (int d = 0; d < KP; d += 64) tma_load(base + L::XBytes + d * 256, my, d, hy, t, b, &full[st]);
                 if (!STATE_ONLY)
                     for (int d = 0; d < KP; d += 64) tma_load(base + d * 256, mx, d, hx, t, b, &full[st]);
-                for (int d = 0; d < KP; d += 64) tma_load(base + L::XBytes + d * 256, my, d, hy, t, b, &full[st]);
                 for (int d = 0; d < VP; d += 64) tma_load(base + 2 * L::XBytes + d * 256, mz, d, hz, t, b, &full[st]);
                 issued = c + 1;
             }
@@ -344,100 +378,146 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                 for (uint32_t i = 0; i < kWaitLimit; ++i)
                     if (mbar_try_wait(&full[c % L::Stages], (c / L::Stages) & 1)) break;
         }
-    } else if (warp == kMmaWarp) {
-        // --------------------------------------------------- MMA issue ---
-        constexpr uint32_t kFmt = F16 ? 0u : (1u << 7) | (1u << 10);
-        constexpr uint32_t kTransB = 1u << 16;
-        const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
-        const uint32_t id_z = idesc_f16_f32(128, VP) | kFmt | kTransB;
-        const uint32_t sb = smem_u32(smem);
-        const uint64_t d_carry = make_desc(sb + L::OffCarry, KP * 128, 1024, 2);
-        bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
-            const int st = c % L::Stages;
-            const int ks = (chunk_n(c) + 15) / 16;
-            const bool carry = c > 0 || has_init;
-            const bool state = c + 1 < nch || want_fin;
-            const uint32_t base = sb + st * L::StageBytes;
-            const uint64_t d_x = make_desc(base, 16, 1024, 2);
-            const uint64_t d_y = make_desc(base + L::XBytes, 16, 1024, 2);
-            const uint64_t d_z = make_desc(base + 2 * L::XBytes, 16384, 1024, 2);
-            ok = wait(&full[st], c / L::Stages);
-            if (ok && !STATE_ONLY) {
-                if (c > 0) ok = wait(bar_pv, c - 1);
-                if (!ok) break;
+    } else if (warp == L::MmaWarp) {
+        // ------------------------------------------- MMAs of the rows ---
+        if constexpr (!STATE_ONLY) {
+            const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
+            const uint32_t id_z = idesc_f16_f32(128, VP) | kFmt | kTransB;
+            const uint32_t sb = smem_u32(smem);
+            const uint64_t d_carry = make_desc(sb + L::OffCarry, KP * 128, 1024, 2);
+            bool ok = true;
+            int scored = 0;                                   // chunks whose score product is out
+            // scores of chunk `scored`; the score tile's last P is used up
+            auto score = [&]() {
+                const uint32_t base = sb + L::OffStage + scored % L::Stages * L::StageBytes;
+                const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::XBytes, 16, 1024, 2);
                 tc_fence_after();
                 for (int k = 0; k < KP / 16; ++k) {
                     const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                    mma_ss_warp(tbase + L::S, d_x + step, d_y + step, id_s, k > 0);
+                    mma_ss_warp(tbase + L::S + scored % NA * 128, d_x + step, d_y + step, id_s, k > 0);
                 }
-                tc_commit_warp(bar_s);
-                ok = wait(carry_ready, c) && (c == 0 || wait(o_free, c - 1));
+                tc_commit_warp(&bar_s[scored % NA]);
+                ++scored;
+            };
+            // wait for `bar`, and send out the next chunk's scores meanwhile
+            // where a second score tile is free and the loads are there
+            auto wait_busy = [&](uint64_t* bar, uint32_t phase, int c) -> bool {
+                if constexpr (NA == 2) {
+                    for (uint32_t i = 0; scored == c + 1 && scored < nch && i < kWaitLimit; ++i) {
+                        if (__all_sync(0xffffffffu, mbar_test_wait(&full[scored % L::Stages], scored / L::Stages & 1) &&
+                                                        (scored < 2 || mbar_test_wait(&bar_pv[scored % 2],
+                                                                                      scored / 2 - 1 & 1)))) {
+                            score();
+                            break;
+                        }
+                        if (__all_sync(0xffffffffu, mbar_test_wait(bar, phase & 1))) return true;
+                        if ((i & 31) == 31 && __any_sync(0xffffffffu, ld_shared_volatile(abort_flag))) return false;
+                    }
+                }
+                return wait(bar, phase);
+            };
+            for (int c = 0; c < nch; ++c) {
+                const int st = c % L::Stages, ga = c % NA;
+                const int ks = (chunk_n(c) + 15) / 16;
+                const bool carry = c > 0 || has_init;
+                const uint32_t base = sb + L::OffStage + st * L::StageBytes;
+                const uint64_t d_x = make_desc(base, 16, 1024, 2);
+                const uint64_t d_z = make_desc(base + 2 * L::XBytes, 16384, 1024, 2);
+                const uint32_t t_o = tbase + L::O + c % L::OutBufs * VP;
+                if (scored == c) {
+                    ok = wait(&full[st], c / L::Stages) && (c < NA || wait(&bar_pv[ga], c / NA - 1));
+                    if (!ok) break;
+                    score();
+                }
+                ok = wait_busy(carry_ready, c, c);
+                if (ok && c >= L::OutBufs) ok = wait(&o_free[(c - L::OutBufs) % NA], (c - L::OutBufs) / NA);
                 if (!ok) break;
                 tc_fence_after();
                 if (carry)
                     for (int k = 0; k < KP / 16; ++k) {
                         const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                        mma_ss_warp(tbase + L::O, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
+                        mma_ss_warp(t_o, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
                     }
-                tc_commit_warp(bar_o);
+                tc_commit_warp(&bar_o[ga]);
+                ok = wait_busy(&p_ready[ga], c / NA, c);
+                if (ok && p.cu && chunk_n(c) < kChunk) ok = wait(z_ready, 0);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < ks; ++k)
+                    mma_ts_warp(t_o, tbase + L::S + ga * 128 + k * 8, d_z + (uint64_t)(k * 128), id_z,
+                                k > 0 || carry ? 1u : 0u);
+                tc_commit_warp(&bar_pv[ga]);
+                tc_commit_warp(&empty[st]);
             }
-            if (ok) ok = wait(b_ready, c);
+            if (!ok) fail();
+            // no MMA is in flight when TMEM is freed (also after a failed wait)
+            tc_commit_warp(&bar_fin[0]);
+            for (uint32_t i = 0; i < kWaitLimit; ++i)
+                if (__all_sync(0xffffffffu, mbar_try_wait(&bar_fin[0], 0))) break;
+        }
+    } else if (warp == L::StateMmaWarp) {
+        // ------------------------------ MMAs of the chunks' own states ---
+        // The smallest parts first: the MMA truncates each sum, so few steps
+        // should meet a large one.
+        const uint32_t id = idesc_f16_f32(128, VP) | kFmt | kTransB | (L::KtSmem ? kTransA : 0u);
+        const uint32_t sb = smem_u32(smem);
+        bool ok = true;
+        for (int c = 0; c < nch; ++c) {
+            const int st = c % L::Stages;
+            const int ks = (chunk_n(c) + 15) / 16;
+            const uint64_t d_z = make_desc(sb + L::OffStage + st * L::StageBytes + 2 * L::XBytes, 16384, 1024, 2);
+            auto weighted = [&](int place, uint32_t acc) {
+                if constexpr (L::KtSmem) {
+                    // (rows 64..127 of the result are unused: whatever lies behind the part)
+                    const uint64_t d_k = make_desc(sb + place * L::XBytes, 16384, 1024, 2);
+                    for (int k = 0; k < ks; ++k)
+                        mma_ss_warp(tbase + L::C, d_k + (uint64_t)(k * 128), d_z + (uint64_t)(k * 128), id,
+                                    k > 0 ? 1u : acc);
+                } else {
+                    for (int k = 0; k < ks; ++k)
+                        mma_ts_warp(tbase + L::C, tbase + L::Kt + place * 64 + k * 8, d_z + (uint64_t)(k * 128), id,
+                                    k > 0 ? 1u : acc);
+                }
+            };
+            ok = wait(kt_ready, c);
             if (!ok) break;
             tc_fence_after();
-            // the chunk's own state, its smallest parts first: the MMA
-            // truncates each sum, so few steps should meet a large one
-            auto weighted = [&](uint32_t cols, uint32_t acc) {
-                for (int k = 0; k < ks; ++k)
-                    mma_ts_warp(tbase + L::C, tbase + cols + k * 8, d_z + (uint64_t)(k * 128), id_z, k > 0 ? 1u : acc);
-            };
-            if (state) {
+            if (c + 1 < nch || want_fin) {
                 if constexpr (kLate) {
-                    weighted(L::Kt, 0u);
-                    weighted(L::Kt + 64, 1u);
+                    weighted(0, 0u);
+                    weighted(1, 1u);
                     tc_commit_warp(bar_kt);
+                    ok = wait(late_ready, c);
+                    if (!ok) break;
+                    tc_fence_after();
+                    weighted(0, 1u);
                 } else {
-                    for (int part = kParts - 1; part >= 0; --part)
-                        weighted(L::Kt + part * 64, part == kParts - 1 ? 0u : 1u);
-                    tc_commit_warp(bar_st);
+                    for (int part = kParts - 1; part >= 0; --part) weighted(part, part == kParts - 1 ? 0u : 1u);
                 }
-            }
-            if (!STATE_ONLY) {
-                ok = wait(p_ready, c);
-                if (!ok) break;
-                tc_fence_after();
-                for (int k = 0; k < ks; ++k)
-                    mma_ts_warp(tbase + L::O, tbase + L::S + k * 8, d_z + (uint64_t)(k * 128), id_z,
-                                k > 0 || carry ? 1u : 0u);
-                tc_commit_warp(bar_pv);
-            }
-            if (state && kLate) {
-                ok = wait(late_ready, c);
-                if (!ok) break;
-                tc_fence_after();
-                weighted(L::Kt, 1u);
                 tc_commit_warp(bar_st);
             }
             tc_commit_warp(&empty[st]);
         }
         if (!ok) fail();
-        // no MMA is in flight when TMEM is freed (also after a failed wait)
-        tc_commit_warp(bar_fin);
+        tc_commit_warp(&bar_fin[1]);
         for (uint32_t i = 0; i < kWaitLimit; ++i)
-            if (__all_sync(0xffffffffu, mbar_try_wait(bar_fin, 0))) break;
-    } else if (warp < 4) {
+            if (__all_sync(0xffffffffu, mbar_try_wait(&bar_fin[1], 0))) break;
+    } else if (warp < L::RowWarps) {
         // -------------------------------------------------- token rows ---
         if constexpr (!STATE_ONLY) {
-            const int i = tid;
-            const uint32_t row = (uint32_t)(warp * 32) << 16;
-            for (int c = 0; c < nch; ++c) {
+            const int ga = warp >> 2, wr = warp & 3;
+            const int i = wr * 32 + lane;
+            const uint32_t row = (uint32_t)(wr * 32) << 16;
+            const uint32_t t_s = tbase + row + L::S + ga * 128;
+            for (int c = ga; c < nch; c += NA) {
                 const int nv = chunk_n(c);
                 const bool carry = c > 0 || has_init;
                 const int jlo = rev ? i : 0, jhi = rev ? nv - 1 : i;
+                const uint32_t t_o = tbase + row + L::O + c % L::OutBufs * VP;
                 // columns 32 blk .. 32 blk + 31: 0 masked, 1 on the border, 2 inside
                 auto kind = [&](int blk) {
-                    if (rev ? blk < warp : blk > warp) return 0;
-                    if (blk == warp || (rev && blk * 32 + 32 > nv)) return blk * 32 < nv ? 1 : 0;
+                    if (rev ? blk < wr : blk > wr) return 0;
+                    if (blk == wr || (rev && blk * 32 + 32 > nv)) return blk * 32 < nv ? 1 : 0;
                     return 2;
                 };
                 auto weigh = [&](uint32_t (&s)[32], int blk, int kd) {
@@ -453,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                         }
                     }
                 };
-                if (!wait(bar_s, c)) { fail(); break; }
+                if (!wait(&bar_s[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
                 float scale = 1.f;
                 if constexpr (F16) {
@@ -462,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                         const int kd = kind(blk);
                         if (kd == 0) continue;
                         uint32_t s[32];
-                        tmem_ld32(tbase + row + L::S + blk * 32, s);
+                        tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
                         weigh(s, blk, kd);
 #pragma unroll
@@ -478,44 +558,45 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                         for (int j = 0; j < 16; ++j) pk[j] = 0u;
                     } else {
                         uint32_t s[32];
-                        tmem_ld32(tbase + row + L::S + blk * 32, s);
+                        tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
                         weigh(s, blk, kd);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             pk[j] = pack<F16>(__uint_as_float(s[2 * j]) * scale, __uint_as_float(s[2 * j + 1]) * scale);
                     }
-                    tmem_st16(tbase + row + L::S + blk * 16, pk);
+                    // P (16 bit) lies over score columns that this thread has read
+                    tmem_st16(t_s + blk * 16, pk);
                 }
-                if (!wait(bar_o, c)) { fail(); break; }
+                if (!wait(&bar_o[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
                 if (carry) {
                     const int e = min(128, max(0, rev ? nv - 1 - i : i + 1));
                     float f = r.a_carry * pw[e];
-                    if constexpr (F16) f *= carry_inv[c & 1] * scale;
+                    if constexpr (F16) f *= carry_inv[c & 3] * scale;
                     for (int blk = 0; blk < VP / 32; ++blk) {
                         uint32_t s[32];
-                        tmem_ld32(tbase + row + L::O + blk * 32, s);
+                        tmem_ld32(t_o + blk * 32, s);
                         tc_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * f);
-                        tmem_st32(tbase + row + L::O + blk * 32, s);
+                        tmem_st32(t_o + blk * 32, s);
                     }
                 }
                 tc_wait_st();
                 tc_fence_before();
-                arrive(p_ready);
-                if (!wait(bar_pv, c)) { fail(); break; }
+                arrive(&p_ready[ga]);
+                if (!wait(&bar_pv[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
                 const float inv = F16 ? 1.f / scale : 1.f;
                 const int64_t at = (int64_t)b * r.out_b + (int64_t)(t0 + chunk_at(c) + i) * r.out_t + (int64_t)h * r.out_h;
                 for (int blk = 0; blk < VP / 32; ++blk) {
                     uint32_t s[32];
-                    tmem_ld32(tbase + row + L::O + blk * 32, s);
+                    tmem_ld32(t_o + blk * 32, s);
                     tc_wait_ld();
                     if (blk == VP / 32 - 1) {
                         tc_fence_before();
-                        arrive(o_free);
+                        arrive(&o_free[ga]);
                     }
                     if constexpr (F16) {
 #pragma unroll
@@ -548,10 +629,9 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
         }
     } else {
         // -------------------------------------------------- state rows ---
-        // two warps share 32 rows of the state: each keeps half of the
-        // columns in registers and weighs half of the tokens
+        // two warps share 32 rows of the state: each keeps half of the columns
         constexpr int kCols = VP / 2;
-        const int ts = tid - 128, bw = (warp - 4) & 3, half = (warp - 4) >> 2;
+        const int ts = tid - L::RowWarps * 32, sw = warp - L::RowWarps, bw = sw & 3, half = sw >> 2;
         const int d = bw * 32 + lane;                         // key channel: row of the state
         const int col0 = half * kCols;
         const uint32_t row = (uint32_t)(bw * 32) << 16;
@@ -559,6 +639,8 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
         const int64_t mat = (int64_t)r.kd * r.vd;
         const int64_t at_seq = ((int64_t)seq * p.H + h) * mat, at_seg = ((int64_t)sid * p.H + h) * mat;
         float rs = 1.f;                                       // (fp16) power of two on this row's weighted keys
+        float* rs_sh = reinterpret_cast<float*>(smem + L::OffScale);
+        uint16_t* kmax_sh = reinterpret_cast<uint16_t*>(smem + L::OffScale + KP * 4);
         uint32_t sync_phase = 0;
         auto sync_b = [&]() -> bool {                         // bounded barrier of the state warps
             arrive(wgb_bar);
@@ -599,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
             const int nv = chunk_n(c);
             const bool carry = c > 0 || has_init;
             const bool more = c + 1 < nch || want_fin;        // the state behind this chunk is wanted
-            uint8_t* base = smem + st * L::StageBytes;
+            uint8_t* base = smem + L::OffStage + st * L::StageBytes;
             if (more && nv != kw_n) {
                 ok = sync_b();
                 if (!ok) break;
@@ -619,14 +701,17 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
 #pragma unroll
                         for (int j = 0; j < kCols; ++j) amax = fmaxf(amax, fabsf(state[j]));
                         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-                        if (lane == 0) amax_sh[(c & 1) * 8 + warp - 4] = __uint_as_float(top);
+                        if (lane == 0) amax_sh[(c & 1) * 8 + sw] = __uint_as_float(top);
                         ok = sync_b();
                         if (!ok) break;
 #pragma unroll
                         for (int w = 0; w < kStateWarps; ++w) amax = fmaxf(amax, amax_sh[(c & 1) * 8 + w]);
                         cs = fp16_scale(amax);
-                        if (ts == 0) carry_inv[c & 1] = 1.f / cs;
                     }
+                    // the last carry product has read the copy
+                    if (c > 0) ok = wait(&bar_o[(c - 1) % NA], (c - 1) / NA);
+                    if (!ok) break;
+                    if (F16 && ts == 0) carry_inv[c & 3] = 1.f / cs;
                     if (live) {
                         uint8_t* dst = smem + L::OffCarry + d * 128;
 #pragma unroll
@@ -643,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                     }
                     fence_proxy_async_smem();
                 }
+                tc_fence_before();
                 arrive(carry_ready);
             }
             ok = wait(&full[st], c / L::Stages);
@@ -657,74 +743,150 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
+                arrive(z_ready);
             }
-            // this thread's channel of the keys
-            const uint8_t* kcol = base + L::XBytes + (d >> 6) * 16384 + (d & 7) * 2;
-            const int cb = (d & 63) >> 3;
-            auto key = [&](int j) -> uint32_t {
-                return *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
-            };
-            if (F16 && more && live) {
-                // scale the row so that its largest weighted key is just below 2^15
-                uint32_t m = 0;
-#pragma unroll 16
-                for (int j = 0; j < kChunk; ++j) {
-                    const uint32_t v = key(j) & 0x7fffu;
-                    m = j < nv ? max(m, v) : m;
-                }
-                rs = 1.f;
-                if (m < 0x7c00u)
-                    rs = fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) * fabsf(r.key_scale) *
-                                    fmaxf(1.f, pw[nv]));
-            }
+            const uint8_t* keys = base + L::XBytes;
             uint32_t late[kLate ? 32 : 1];
-            if (more && live) {
+            if constexpr (L::KtSmem) {
+                // eight channels of four tokens a thread, in the tile's own
+                // layout (the MMA reads it with the channel as its row)
+                const int ch = ts & 7;
+                if (F16 && more) {
+                    // scale each channel so that its largest weighted key is just below 2^15
+                    __half2 m[4];
 #pragma unroll
-                for (int jb = 0; jb < 4; ++jb) {
-                    uint32_t part[3][8];
+                    for (int q = 0; q < 4; ++q) m[q] = __float2half2_rn(0.f);
 #pragma unroll
-                    for (int j2 = 0; j2 < 8; ++j2) {
-                        const int j = half * 64 + jb * 16 + j2 * 2;
-                        const float2 w = *reinterpret_cast<const float2*>(kw + j);
-                        const float2 kk = unpack<F16>(key(j) | (key(j + 1) << 16));
-                        // a select, not a product: what lies behind the end may be inf or NaN
-                        float f0 = j < nv ? kk.x * w.x : 0.f, f1 = j + 1 < nv ? kk.y * w.y : 0.f;
-                        if constexpr (F16) {
-                            f0 *= rs;
-                            f1 *= rs;
-                        }
+                    for (int q = 0; q < 4; ++q) {
+                        const int j = (ts >> 3) + q * 32;
+                        if (j < nv) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(keys + j * 128 + ((ch ^ (j & 7)) << 4));
+                            const __half2* x = reinterpret_cast<const __half2*>(&v);
 #pragma unroll
-                        for (int q = 0; q < kParts; ++q) {
-                            part[q][j2] = pack<F16>(f0, f1);
-                            const float2 back = unpack<F16>(part[q][j2]);
-                            f0 -= back.x;
-                            f1 -= back.y;
+                            for (int e = 0; e < 4; ++e) m[e] = __hmax2(m[e], __habs2(x[e]));
                         }
                     }
-                    const uint32_t at = tbase + row + L::Kt + (half * 4 + jb) * 8;
-                    if constexpr (kLate) {
-                        tmem_st8(at, part[2]);
-                        tmem_st8(at + 64, part[1]);
 #pragma unroll
-                        for (int j2 = 0; j2 < 8; ++j2) late[jb * 8 + j2] = part[0][j2];
-                    } else {
+                    for (int e = 0; e < 4; ++e) {
+                        m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], 8));
+                        m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], 16));
+                    }
+                    if (lane < 8) *reinterpret_cast<uint4*>(kmax_sh + sw * KP + ch * 8) = *reinterpret_cast<uint4*>(m);
+                    ok = sync_b();
+                    if (!ok) break;
+                    if (ts < KP) {
+                        uint32_t top = 0;                     // fp16 magnitudes order like integers
 #pragma unroll
-                        for (int q = 0; q < kParts; ++q) tmem_st8(at + q * 64, part[q]);
+                        for (int w = 0; w < kStateWarps; ++w) top = max(top, (uint32_t)kmax_sh[w * KP + ts]);
+                        rs_sh[ts] = top < 0x7c00u ? fp16_scale(__half2float(__ushort_as_half((unsigned short)top)) *
+                                                               fabsf(r.key_scale) * fmaxf(1.f, pw[nv]))
+                                                  : 1.f;
+                    }
+                    ok = sync_b();
+                    if (!ok) break;
+                    if (live) rs = rs_sh[d];
+                }
+                if (more) {
+                    float sc[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sc[e] = F16 ? rs_sh[ch * 8 + e] : 1.f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int j = (ts >> 3) + q * 32;
+                        const uint32_t off = j * 128 + ((ch ^ (j & 7)) << 4);
+                        const uint4 v = *reinterpret_cast<const uint4*>(keys + off);
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        const float w = kw[j];
+                        uint32_t part[3][4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 kk = unpack<F16>(x[e]);
+                            // a select, not a product: what lies behind the end may be inf or NaN
+                            float f0 = j < nv ? kk.x * w : 0.f, f1 = j < nv ? kk.y * w : 0.f;
+                            if constexpr (F16) {
+                                f0 *= sc[2 * e];
+                                f1 *= sc[2 * e + 1];
+                            }
+#pragma unroll
+                            for (int t = 0; t < kParts; ++t) {
+                                part[t][e] = pack<F16>(f0, f1);
+                                const float2 back = unpack<F16>(part[t][e]);
+                                f0 -= back.x;
+                                f1 -= back.y;
+                            }
+                        }
+#pragma unroll
+                        for (int t = 0; t < kParts; ++t)
+                            *reinterpret_cast<uint4*>(smem + t * L::XBytes + off) =
+                                make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
+                    }
+                    fence_proxy_async_smem();
+                }
+            } else {
+                // one channel of 64 tokens a thread, transposed into TMEM
+                const uint8_t* kcol = keys + (d >> 6) * 16384 + (d & 7) * 2;
+                const int cb = (d & 63) >> 3;
+                auto key = [&](int j) -> uint32_t {
+                    return *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
+                };
+                if (F16 && more) {
+                    // scale the row so that its largest weighted key is just below 2^15
+                    uint32_t m = 0;
+#pragma unroll 16
+                    for (int j = 0; j < kChunk; ++j) {
+                        const uint32_t v = key(j) & 0x7fffu;
+                        m = j < nv ? max(m, v) : m;
+                    }
+                    rs = 1.f;
+                    if (m < 0x7c00u)
+                        rs = fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) * fabsf(r.key_scale) *
+                                        fmaxf(1.f, pw[nv]));
+                }
+                if (more) {
+#pragma unroll
+                    for (int jb = 0; jb < 4; ++jb) {
+                        uint32_t part[3][8];
+#pragma unroll
+                        for (int j2 = 0; j2 < 8; ++j2) {
+                            const int j = half * 64 + jb * 16 + j2 * 2;
+                            const float2 w = *reinterpret_cast<const float2*>(kw + j);
+                            const float2 kk = unpack<F16>(key(j) | (key(j + 1) << 16));
+                            float f0 = j < nv ? kk.x * w.x : 0.f, f1 = j + 1 < nv ? kk.y * w.y : 0.f;
+                            if constexpr (F16) {
+                                f0 *= rs;
+                                f1 *= rs;
+                            }
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q) {
+                                part[q][j2] = pack<F16>(f0, f1);
+                                const float2 back = unpack<F16>(part[q][j2]);
+                                f0 -= back.x;
+                                f1 -= back.y;
+                            }
+                        }
+                        const uint32_t at = tbase + row + L::Kt + (half * 4 + jb) * 8;
+                        if constexpr (kLate) {
+                            tmem_st8(at, part[2]);
+                            tmem_st8(at + 64, part[1]);
+#pragma unroll
+                            for (int j2 = 0; j2 < 8; ++j2) late[jb * 8 + j2] = part[0][j2];
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < kParts; ++q) tmem_st8(at + q * 64, part[q]);
+                        }
                     }
                 }
+                tc_wait_st();
             }
-            tc_wait_st();
             tc_fence_before();
-            arrive(b_ready);
+            arrive(kt_ready);
             if constexpr (kLate) {
                 if (more) {
                     ok = wait(bar_kt, c);
                     if (!ok) break;
                     tc_fence_after();
-                    if (live) {
-                        tmem_st16(tbase + row + L::Kt + half * 32, late);
-                        tmem_st16(tbase + row + L::Kt + half * 32 + 16, late + 16);
-                    }
+                    tmem_st16(tbase + row + L::Kt + half * 32, late);
+                    tmem_st16(tbase + row + L::Kt + half * 32 + 16, late + 16);
                     tc_wait_st();
                     tc_fence_before();
                     arrive(late_ready);
@@ -750,7 +912,7 @@ __global__ void __launch_bounds__(kThreads, 1) la_kernel(const __grid_constant__
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == L::MmaWarp) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
@@ -936,7 +1098,7 @@ cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
     void* args[] = {const_cast<Params*>(&p)};
-    return cudaLaunchKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(kThreads), args,
+    return cudaLaunchKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(Layout<KP, VP>::Threads), args,
                             Layout<KP, VP>::Bytes, s);
 }
 
