@@ -44,6 +44,7 @@ __device__ int g_status;                      // FFTCONV_ERR_TIMEOUT once a wait
 struct Role {
     int x, y, z;                              // tensor maps of the three sides
     int x_div, y_div, z_div;                  // heads of the call per head of the tensor
+    int out_map;                              // tensor map of the output
     int rev;                                  // backward in time
     int out_f32;                              // fp32 partial sums of shared heads
     int kd, vd;                               // key and value dims
@@ -156,6 +157,15 @@ __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int d, int h, int t, int b) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
+                 "r"(d), "r"(h), "r"(t), "r"(b), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// until the issuing thread's stores have read their shared memory
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // 16-bit arithmetic of the two types: packing with round to nearest even, and
 // the two halves as fp32.
 template <bool F16>
@@ -176,6 +186,16 @@ __device__ __forceinline__ float2 unpack(uint32_t v) {
     } else {
         return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 pack8(const uint32_t* s) {
+    uint4 v;
+    v.x = pack<F16>(__uint_as_float(s[0]), __uint_as_float(s[1]));
+    v.y = pack<F16>(__uint_as_float(s[2]), __uint_as_float(s[3]));
+    v.z = pack<F16>(__uint_as_float(s[4]), __uint_as_float(s[5]));
+    v.w = pack<F16>(__uint_as_float(s[6]), __uint_as_float(s[7]));
+    return v;
 }
 
 // 2^e with the largest exponent that keeps amax * 2^e below 2^15 (1 for 0,
@@ -200,60 +220,63 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
     return ok != 0;
 }
 
-template <int KP, int VP>
+// Parts of the weighted keys and how they lie in TMEM: EXACT where the state
+// itself is a result (fp32, so all 24 bits of a weighted bf16 key count),
+// else 16 bits, far below the rounding of what the state then goes into.
+template <int KP, int VP, bool F16, bool EXACT>
 struct Layout {
-    // the weighted keys: in shared memory (64 channels), or, where the tiles
-    // leave no room, transposed in TMEM
-    static constexpr bool KtSmem = KP == 64;
-    // groups of row warps, which take chunks in turn, each with a score tile;
-    // TMEM has room for one at 128 x 128
-    static constexpr int Groups = KP == 128 && VP == 128 ? 1 : 2;
-    static constexpr int OutBufs = KP == 64 && VP == 64 ? 2 : 1;
+    // 64 channels: two parts are stacked on the 128 rows of one MMA, and the
+    // state is kept as the two rows' sum; 128 channels: one MMA a part
+    static constexpr bool Stacked = KP == 64;
+    static constexpr int Parts = F16 || !EXACT ? 2 : 3;
+    static constexpr bool Late = !Stacked && Parts == 3;      // the last part waits for the first one's columns
+    static constexpr int KtCols = Stacked ? (Parts == 3 ? 128 : 64) : 128;
+    // groups of row warps, which take chunks in turn, each with a score tile
+    static constexpr int Groups = VP == 64 ? 2 : 1;
+    static constexpr int OutBufs = KP == 64 && VP == 64 && KtCols == 64 ? 2 : 1;
     static constexpr int RowWarps = 4 * Groups;
     static constexpr int LoadWarp = RowWarps + kStateWarps, MmaWarp = LoadWarp + 1, StateMmaWarp = LoadWarp + 2;
     static constexpr int Threads = (RowWarps + kStateWarps + 3) * 32;
     static constexpr int XBytes = KP * kChunk * 2, ZBytes = VP * kChunk * 2;
     static constexpr int StageBytes = 2 * XBytes + ZBytes;
-    static constexpr int KtBytes = KtSmem ? 3 * XBytes : 0;
-    static constexpr int CarryBytes = KP * VP * 2;
-    static constexpr int Stages = StageBytes <= 49152 ? 3 : 2;
-    static constexpr int OffStage = KtBytes;
-    static constexpr int OffCarry = OffStage + Stages * StageBytes;
+    static constexpr int CarryBytes = 128 * VP * 2;
+    static constexpr int Stages = StageBytes <= 49152 ? 4 : StageBytes <= 65536 ? 3 : 2;
+    static constexpr int OffCarry = Stages * StageBytes;
     static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d|, d = j - i in [-127, 127]
-    static constexpr int OffPow = OffTab + 256 * 4;           // g^e, e <= 128
+    static constexpr int OffCol = OffTab + 256 * 4;           // column weights of an unmasked block of P
+    static constexpr int OffPow = OffCol + 32 * 4;            // g^e, e <= 128
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, TMEM base, scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int OffScale = OffBar + 32 * 8;          // (fp16, KtSmem) channel scales and their maxima
-    static constexpr int Bytes = OffScale + (KtSmem ? KP * 4 + kStateWarps * KP * 2 : 0);
+    static constexpr int OffMax = OffBar + 26 * 8;            // (fp16) channel maxima of each half's tokens
+    static constexpr int Bytes = OffMax + (F16 ? 2 * KP * 2 : 0);
     // TMEM columns
     static constexpr int S = 0, O = Groups * 128, C = O + OutBufs * VP, Kt = C + VP;
     static_assert(Bytes <= 232448, "shared memory");
-    static_assert(Kt + (KtSmem ? 0 : 128) <= 512, "TMEM columns");
+    static_assert(Kt + KtCols <= 512, "TMEM columns");
 };
 
 // One CTA: one (segment, head, role).  Row warps (one or two groups of four
-// that take chunks in turn) own the token rows: P and the output.  Eight
-// state warps keep the state in registers (its decay, its 16-bit copy for the
-// next product) and weigh the keys.  One warp issues the loads, one the MMAs
-// of the rows (scores, carry product, P z), one those of the chunk's own
+// that take chunks in turn) own the token rows: P and the output, which
+// leaves through the query tile's shared memory.  Eight state warps keep the
+// state in registers (its decay, its 16-bit copy for the next product) and
+// weigh the keys, transposed into TMEM.  One warp issues the loads, one the
+// MMAs of the rows (scores, carry product, P z), one those of the chunk's own
 // state.  Only the carry product waits for the state, so chunks overlap.
 //
 // Rounding: P and the carry's copy are rounded once to the 16-bit type (their
 // products are the two halves of the output, each with the error of one
-// rounding of it); the weighted keys are split into two (fp16) or three
-// (bf16) 16-bit parts, 22 or 24 bits, because the state is an fp32 result.
-// fp16 operands are scaled by exact powers of two (P by row, the carry's copy
-// by its largest value, the weighted keys by channel), so that nothing
-// overflows fp16's range or falls below it.
-template <int KP, int VP, bool F16, bool STATE_ONLY>
-__global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __grid_constant__ Params p) {
-    using L = Layout<KP, VP>;
-    constexpr int kParts = F16 ? 2 : 3;
+// rounding of it); the weighted keys are split into two or three 16-bit parts
+// (Layout).  fp16 operands are scaled by exact powers of two (P by row, the
+// carry's copy by its largest value, the weighted keys by channel), so that
+// nothing overflows fp16's range or falls below it.
+template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
+__global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_kernel(const __grid_constant__ Params p) {
+    using L = Layout<KP, VP, F16, EXACT>;
     constexpr int NA = L::Groups;
-    constexpr bool kLate = !L::KtSmem && kParts == 3;         // the last part waits for the first one's columns
     extern __shared__ __align__(1024) uint8_t smem[];
     float* tab = reinterpret_cast<float*>(smem + L::OffTab);
+    float* colw = reinterpret_cast<float*>(smem + L::OffCol);
     float* pw = reinterpret_cast<float*>(smem + L::OffPow);
     float* kw = reinterpret_cast<float*>(smem + L::OffKw);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + L::OffMisc);
@@ -263,20 +286,20 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
     volatile float* amax_sh = reinterpret_cast<volatile float*>(misc + 12);       // [2][8]
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OffBar);
     uint64_t* full = bars;                                    // [Stages] loads
-    uint64_t* empty = bars + 3;                               // [Stages] both MMA warps are done with a stage
-    uint64_t* bar_s = bars + 6;                               // [Groups] scores
-    uint64_t* bar_o = bars + 8;                               // [Groups] carry product
-    uint64_t* bar_pv = bars + 10;                             // [Groups] output
-    uint64_t* p_ready = bars + 12;                            // [Groups] P written, carry product weighted
-    uint64_t* o_free = bars + 14;                             // [Groups] output read
-    uint64_t* bar_st = bars + 16;                             // the chunk's own state
-    uint64_t* bar_kt = bars + 17;                             // its first parts (late only)
-    uint64_t* kt_ready = bars + 18;
-    uint64_t* late_ready = bars + 19;
-    uint64_t* carry_ready = bars + 20;
-    uint64_t* z_ready = bars + 21;                            // rows behind a packed sequence zeroed
-    uint64_t* wgb_bar = bars + 22;
-    uint64_t* bar_fin = bars + 23;                            // [2]
+    uint64_t* empty = bars + 4;                               // [Stages] MMAs and output are done with a stage
+    uint64_t* bar_s = bars + 8;                               // [Groups] scores
+    uint64_t* bar_o = bars + 10;                              // [Groups] carry product
+    uint64_t* bar_pv = bars + 12;                             // [Groups] output
+    uint64_t* p_ready = bars + 14;                            // [Groups] P written, carry product weighted
+    uint64_t* o_free = bars + 16;                             // [Groups] output read
+    uint64_t* bar_st = bars + 18;                             // the chunk's own state
+    uint64_t* bar_kt = bars + 19;                             // its first parts (Late only)
+    uint64_t* kt_ready = bars + 20;
+    uint64_t* late_ready = bars + 21;
+    uint64_t* carry_ready = bars + 22;
+    uint64_t* z_ready = bars + 23;                            // rows behind a packed sequence zeroed
+    uint64_t* wgb_bar = bars + 24;
+    uint64_t* bar_fin = bars + 25;                            // both MMA warps
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -298,17 +321,16 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
             misc[5] = s.b;
         }
     } else if (warp == L::LoadWarp && lane == 0) {
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], STATE_ONLY ? 1 : 2);
+            mbar_init(&empty[i], STATE_ONLY ? 1 : 6);         // two MMA warps, four row warps
         }
-        for (int i = 6; i < 12; ++i) mbar_init(bars + i, 1);
-        for (int i = 12; i < 16; ++i) mbar_init(bars + i, 4);
+        for (int i = 8; i < 14; ++i) mbar_init(bars + i, 1);
+        for (int i = 14; i < 18; ++i) mbar_init(bars + i, 4);
         mbar_init(bar_st, 1);
         mbar_init(bar_kt, 1);
-        for (int i = 18; i < 23; ++i) mbar_init(bars + i, kStateWarps);
-        mbar_init(&bar_fin[0], 1);
-        mbar_init(&bar_fin[1], 1);
+        for (int i = 20; i < 25; ++i) mbar_init(bars + i, kStateWarps);
+        mbar_init(bar_fin, STATE_ONLY ? 1 : 2);
         *abort_flag = 0;
         fence_barrier_init();
     } else if (warp == L::MmaWarp) {
@@ -322,6 +344,7 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
         if (i == 127) pw[128] = decay_power(ld, 128.f);
         tab[127 + (rev ? i : -i)] = r.a_in * w;
         if (i) tab[127 - (rev ? i : -i)] = 0.f;
+        if (i < 32) colw[rev ? i : 31 - i] = r.a_in * w;
     }
     tc_fence_before();
     __syncthreads();
@@ -330,9 +353,12 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
     const int seq = misc[0], idx = misc[1], count = misc[2], n = misc[3], t0 = misc[4], b = misc[5];
     const bool first = rev ? idx == count - 1 : idx == 0;     // in the direction of time of the role
     const bool last = rev ? idx == 0 : idx == count - 1;
-    const int nch = (seq < 0 || (STATE_ONLY && last)) ? 0 : (n + kChunk - 1) / kChunk;
+    // a split sequence's last state only matters where it is a result
+    const int nch = (seq < 0 || (STATE_ONLY && last && (count == 1 || r.fin == nullptr)))
+                        ? 0
+                        : (n + kChunk - 1) / kChunk;
     const bool has_init = !STATE_ONLY && (first ? r.init != nullptr : true);
-    const bool want_fin = STATE_ONLY || (last && r.fin != nullptr);
+    const bool want_fin = STATE_ONLY || (count == 1 && r.fin != nullptr);
 
     auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1, abort_flag, kWaitLimit));
@@ -349,7 +375,16 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
     auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kChunk; };
     auto chunk_n = [&](int c) { return min(kChunk, n - chunk_at(c)); };
     constexpr uint32_t kFmt = F16 ? 0u : (1u << 7) | (1u << 10);
-    constexpr uint32_t kTransA = 1u << 15, kTransB = 1u << 16;
+    constexpr uint32_t kTransB = 1u << 16;
+    // ks products of 16 tokens: A in TMEM, B the value tile
+    auto token_mma = [&](uint32_t d, uint32_t a, uint64_t d_z, uint32_t id, int ks, uint32_t acc) {
+        if (ks == 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) mma_ts_warp(d, a + k * 8, d_z + (uint64_t)(k * 128), id, k > 0 ? 1u : acc);
+        } else {
+            for (int k = 0; k < ks; ++k) mma_ts_warp(d, a + k * 8, d_z + (uint64_t)(k * 128), id, k > 0 ? 1u : acc);
+        }
+    };
 
     if (warp == L::LoadWarp) {
         // ------------------------------------------------------- loads ---
@@ -364,7 +399,7 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                     fail();
                     break;
                 }
-                uint8_t* base = smem + L::OffStage + st * L::StageBytes;
+                uint8_t* base = smem + st * L::StageBytes;
                 const int t = t0 + chunk_at(c);
                 mbar_expect_tx(&full[st], STATE_ONLY ? L::StageBytes - L::XBytes : L::StageBytes);
                 for (int d = 0; d < KP; d += 64) tma_load(base + L::XBytes + d * 256, my, d, hy, t, b, &full[st]);
@@ -384,14 +419,15 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
             const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
             const uint32_t id_z = idesc_f16_f32(128, VP) | kFmt | kTransB;
             const uint32_t sb = smem_u32(smem);
-            const uint64_t d_carry = make_desc(sb + L::OffCarry, KP * 128, 1024, 2);
+            const uint64_t d_carry = make_desc(sb + L::OffCarry, 128 * 128, 1024, 2);
             bool ok = true;
             int scored = 0;                                   // chunks whose score product is out
             // scores of chunk `scored`; the score tile's last P is used up
             auto score = [&]() {
-                const uint32_t base = sb + L::OffStage + scored % L::Stages * L::StageBytes;
+                const uint32_t base = sb + scored % L::Stages * L::StageBytes;
                 const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::XBytes, 16, 1024, 2);
                 tc_fence_after();
+#pragma unroll
                 for (int k = 0; k < KP / 16; ++k) {
                     const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
                     mma_ss_warp(tbase + L::S + scored % NA * 128, d_x + step, d_y + step, id_s, k > 0);
@@ -420,7 +456,7 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                 const int st = c % L::Stages, ga = c % NA;
                 const int ks = (chunk_n(c) + 15) / 16;
                 const bool carry = c > 0 || has_init;
-                const uint32_t base = sb + L::OffStage + st * L::StageBytes;
+                const uint32_t base = sb + st * L::StageBytes;
                 const uint64_t d_x = make_desc(base, 16, 1024, 2);
                 const uint64_t d_z = make_desc(base + 2 * L::XBytes, 16384, 1024, 2);
                 const uint32_t t_o = tbase + L::O + c % L::OutBufs * VP;
@@ -433,75 +469,64 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                 if (ok && c >= L::OutBufs) ok = wait(&o_free[(c - L::OutBufs) % NA], (c - L::OutBufs) / NA);
                 if (!ok) break;
                 tc_fence_after();
-                if (carry)
-                    for (int k = 0; k < KP / 16; ++k) {
-                        const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                if (carry) {
+                    // (64 channels: the query's four steps against both halves of the state)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int kx = k % (KP / 16);
+                        const uint64_t step = (uint64_t)((kx >> 2) * 16384 + (kx & 3) * 32) >> 4;
                         mma_ss_warp(t_o, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
                     }
+                }
                 tc_commit_warp(&bar_o[ga]);
                 ok = wait_busy(&p_ready[ga], c / NA, c);
                 if (ok && p.cu && chunk_n(c) < kChunk) ok = wait(z_ready, 0);
                 if (!ok) break;
                 tc_fence_after();
-                for (int k = 0; k < ks; ++k)
-                    mma_ts_warp(t_o, tbase + L::S + ga * 128 + k * 8, d_z + (uint64_t)(k * 128), id_z,
-                                k > 0 || carry ? 1u : 0u);
+                token_mma(t_o, tbase + L::S + ga * 128, d_z, id_z, ks, carry ? 1u : 0u);
                 tc_commit_warp(&bar_pv[ga]);
                 tc_commit_warp(&empty[st]);
             }
             if (!ok) fail();
-            // no MMA is in flight when TMEM is freed (also after a failed wait)
-            tc_commit_warp(&bar_fin[0]);
-            for (uint32_t i = 0; i < kWaitLimit; ++i)
-                if (__all_sync(0xffffffffu, mbar_try_wait(&bar_fin[0], 0))) break;
+            tc_commit_warp(bar_fin);
         }
     } else if (warp == L::StateMmaWarp) {
         // ------------------------------ MMAs of the chunks' own states ---
         // The smallest parts first: the MMA truncates each sum, so few steps
         // should meet a large one.
-        const uint32_t id = idesc_f16_f32(128, VP) | kFmt | kTransB | (L::KtSmem ? kTransA : 0u);
-        const uint32_t sb = smem_u32(smem);
+        const uint32_t id = idesc_f16_f32(128, VP) | kFmt | kTransB;
+        const uint32_t sb = smem_u32(smem), t_c = tbase + L::C, t_kt = tbase + L::Kt;
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int st = c % L::Stages;
             const int ks = (chunk_n(c) + 15) / 16;
-            const uint64_t d_z = make_desc(sb + L::OffStage + st * L::StageBytes + 2 * L::XBytes, 16384, 1024, 2);
-            auto weighted = [&](int place, uint32_t acc) {
-                if constexpr (L::KtSmem) {
-                    // (rows 64..127 of the result are unused: whatever lies behind the part)
-                    const uint64_t d_k = make_desc(sb + place * L::XBytes, 16384, 1024, 2);
-                    for (int k = 0; k < ks; ++k)
-                        mma_ss_warp(tbase + L::C, d_k + (uint64_t)(k * 128), d_z + (uint64_t)(k * 128), id,
-                                    k > 0 ? 1u : acc);
-                } else {
-                    for (int k = 0; k < ks; ++k)
-                        mma_ts_warp(tbase + L::C, tbase + L::Kt + place * 64 + k * 8, d_z + (uint64_t)(k * 128), id,
-                                    k > 0 ? 1u : acc);
-                }
-            };
+            const uint64_t d_z = make_desc(sb + st * L::StageBytes + 2 * L::XBytes, 16384, 1024, 2);
             ok = wait(kt_ready, c);
             if (!ok) break;
             tc_fence_after();
             if (c + 1 < nch || want_fin) {
-                if constexpr (kLate) {
-                    weighted(0, 0u);
-                    weighted(1, 1u);
+                if constexpr (L::KtCols == 64) {
+                    token_mma(t_c, t_kt, d_z, id, ks, 0u);
+                } else {
+                    token_mma(t_c, t_kt + 64, d_z, id, ks, 0u);
+                    token_mma(t_c, t_kt, d_z, id, ks, 1u);
+                }
+                if constexpr (L::Late) {
                     tc_commit_warp(bar_kt);
                     ok = wait(late_ready, c);
                     if (!ok) break;
                     tc_fence_after();
-                    weighted(0, 1u);
-                } else {
-                    for (int part = kParts - 1; part >= 0; --part) weighted(part, part == kParts - 1 ? 0u : 1u);
+                    token_mma(t_c, t_kt, d_z, id, ks, 1u);
                 }
                 tc_commit_warp(bar_st);
             }
             tc_commit_warp(&empty[st]);
         }
         if (!ok) fail();
-        tc_commit_warp(&bar_fin[1]);
+        tc_commit_warp(bar_fin);
+        // no MMA of either warp is in flight when TMEM is freed (also after a failed wait)
         for (uint32_t i = 0; i < kWaitLimit; ++i)
-            if (__all_sync(0xffffffffu, mbar_try_wait(&bar_fin[1], 0))) break;
+            if (__all_sync(0xffffffffu, mbar_try_wait(bar_fin, 0))) break;
     } else if (warp < L::RowWarps) {
         // -------------------------------------------------- token rows ---
         if constexpr (!STATE_ONLY) {
@@ -520,16 +545,27 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                     if (blk == wr || (rev && blk * 32 + 32 > nv)) return blk * 32 < nv ? 1 : 0;
                     return 2;
                 };
-                auto weigh = [&](uint32_t (&s)[32], int blk, int kd) {
-                    const float* w = tab + 127 + blk * 32 - i;
+                auto weigh = [&](uint32_t (&s)[32], int blk, int kd, float scale) {
                     if (kd == 2) {
+                        // g^|i-j| as (row to the block's near edge) x (edge to
+                        // column): both at most 1, four columns a load
+                        const float f = pw[rev ? blk * 32 - i : i - blk * 32 - 31] * scale;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * w[j]);
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 w = *reinterpret_cast<const float4*>(colw + j);
+                            s[j] = __float_as_uint(__uint_as_float(s[j]) * (f * w.x));
+                            s[j + 1] = __float_as_uint(__uint_as_float(s[j + 1]) * (f * w.y));
+                            s[j + 2] = __float_as_uint(__uint_as_float(s[j + 2]) * (f * w.z));
+                            s[j + 3] = __float_as_uint(__uint_as_float(s[j + 3]) * (f * w.w));
+                        }
                     } else {
+                        const float* w = tab + 127 + blk * 32 - i;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
                             const int col = blk * 32 + j;
-                            s[j] = col >= jlo && col <= jhi ? __float_as_uint(__uint_as_float(s[j]) * w[j]) : 0u;
+                            float x = __uint_as_float(s[j]) * w[j];
+                            if constexpr (F16) x *= scale;
+                            s[j] = col >= jlo && col <= jhi ? __float_as_uint(x) : 0u;
                         }
                     }
                 };
@@ -544,7 +580,7 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                         uint32_t s[32];
                         tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
-                        weigh(s, blk, kd);
+                        weigh(s, blk, kd, 1.f);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
                     }
@@ -560,10 +596,10 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                         uint32_t s[32];
                         tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
-                        weigh(s, blk, kd);
+                        weigh(s, blk, kd, scale);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            pk[j] = pack<F16>(__uint_as_float(s[2 * j]) * scale, __uint_as_float(s[2 * j + 1]) * scale);
+                            pk[j] = pack<F16>(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
                     }
                     // P (16 bit) lies over score columns that this thread has read
                     tmem_st16(t_s + blk * 16, pk);
@@ -589,7 +625,31 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                 if (!wait(&bar_pv[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
                 const float inv = F16 ? 1.f / scale : 1.f;
-                const int64_t at = (int64_t)b * r.out_b + (int64_t)(t0 + chunk_at(c) + i) * r.out_t + (int64_t)h * r.out_h;
+                const int st = c % L::Stages, t = t0 + chunk_at(c);
+                // Through the query tile, which no MMA reads any more: each
+                // warp stages its 32 rows in 4 KB pieces (rows of 128 bytes,
+                // 128-byte swizzle) and stores them by TMA, which leaves out
+                // what lies outside the tensor.  The last rows of a packed
+                // sequence, which others follow, are stored directly.
+                const bool direct = p.cu && nv < kChunk;
+                constexpr int kSlots = KP / 64;
+                uint8_t* slot0 = smem + st * L::StageBytes + wr * 4096;
+                int piece = 0;
+                auto send = [&](int d0) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store(&p.maps[r.out_map], slot0 + piece % kSlots * 16384, d0, h, t + wr * 32, b);
+                        bulk_commit();
+                    }
+                    ++piece;
+                };
+                auto reuse = [&]() {                          // a piece's place, once its store has read it
+                    if (piece >= kSlots) {
+                        if (lane == 0) bulk_wait_read();
+                        __syncwarp();
+                    }
+                };
                 for (int blk = 0; blk < VP / 32; ++blk) {
                     uint32_t s[32];
                     tmem_ld32(t_o + blk * 32, s);
@@ -602,74 +662,96 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
 #pragma unroll
                         for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * inv);
                     }
-                    if (i >= nv) {
-                        // rows behind the sequence's end are not stored
+                    if (direct) {
+                        const int64_t at = (int64_t)b * r.out_b + (int64_t)(t + i) * r.out_t + (int64_t)h * r.out_h;
+                        if (i < nv && r.out_f32) {
+                            float* o = reinterpret_cast<float*>(r.out) + at + blk * 32;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4)
+                                if (blk * 32 + j < r.vd)
+                                    *reinterpret_cast<uint4*>(o + j) = make_uint4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+                        } else if (i < nv) {
+                            uint16_t* o = reinterpret_cast<uint16_t*>(r.out) + at + blk * 32;
+#pragma unroll
+                            for (int j = 0; j < 32; j += 8)
+                                if (blk * 32 + j < r.vd) *reinterpret_cast<uint4*>(o + j) = pack8<F16>(s + j);
+                        }
+                        __syncwarp();
                     } else if (r.out_f32) {
-                        float* o = reinterpret_cast<float*>(r.out) + at + blk * 32;
+                        reuse();
+                        uint8_t* dst = slot0 + piece % kSlots * 16384 + lane * 128;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4)
-                            if (blk * 32 + j < r.vd)
-                                *reinterpret_cast<uint4*>(o + j) = make_uint4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(dst + ((j ^ (lane & 7)) << 4)) =
+                                make_uint4(s[4 * j], s[4 * j + 1], s[4 * j + 2], s[4 * j + 3]);
+                        send(blk * 32);
                     } else {
-                        uint16_t* o = reinterpret_cast<uint16_t*>(r.out) + at + blk * 32;
+                        if (!(blk & 1)) reuse();
+                        uint8_t* dst = slot0 + piece % kSlots * 16384 + lane * 128;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            if (blk * 32 + j < r.vd) {
-                                uint4 v;
-                                v.x = pack<F16>(__uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-                                v.y = pack<F16>(__uint_as_float(s[j + 2]), __uint_as_float(s[j + 3]));
-                                v.z = pack<F16>(__uint_as_float(s[j + 4]), __uint_as_float(s[j + 5]));
-                                v.w = pack<F16>(__uint_as_float(s[j + 6]), __uint_as_float(s[j + 7]));
-                                *reinterpret_cast<uint4*>(o + j) = v;
-                            }
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(dst + ((((blk & 1) * 4 + j) ^ (lane & 7)) << 4)) =
+                                pack8<F16>(s + 8 * j);
+                        if (blk & 1) send(blk * 32 - 32);
                     }
-                    __syncwarp();
                 }
+                if (lane == 0) {
+                    bulk_wait_read();                         // (the stage may be loaded again)
+                    mbar_arrive(&empty[st]);
+                }
+                __syncwarp();
             }
+            if (lane == 0) bulk_wait_read();                  // (also after a failed wait)
         }
     } else {
         // -------------------------------------------------- state rows ---
-        // two warps share 32 rows of the state: each keeps half of the columns
+        // Two warps share 32 rows of the MMA: each keeps half of the columns
+        // and weighs half of the tokens.  64 channels: rows 0-63 carry the
+        // sums of the first (and third) part, rows 64-127 of the second.
         constexpr int kCols = VP / 2;
         const int ts = tid - L::RowWarps * 32, sw = warp - L::RowWarps, bw = sw & 3, half = sw >> 2;
-        const int d = bw * 32 + lane;                         // key channel: row of the state
+        const int d = bw * 32 + lane;
+        const int ch = L::Stacked ? d & 63 : d;               // key channel
+        const bool second = L::Stacked && bw >= 2;            // (warp-uniform)
         const int col0 = half * kCols;
         const uint32_t row = (uint32_t)(bw * 32) << 16;
-        const bool live = bw * 32 < KP;                       // warp-uniform
         const int64_t mat = (int64_t)r.kd * r.vd;
         const int64_t at_seq = ((int64_t)seq * p.H + h) * mat, at_seg = ((int64_t)sid * p.H + h) * mat;
-        float rs = 1.f;                                       // (fp16) power of two on this row's weighted keys
-        float* rs_sh = reinterpret_cast<float*>(smem + L::OffScale);
-        uint16_t* kmax_sh = reinterpret_cast<uint16_t*>(smem + L::OffScale + KP * 4);
+        float rs = 1.f;                                       // (fp16) power of two on this channel's weighted keys
+        uint16_t* kmax_sh = reinterpret_cast<uint16_t*>(smem + L::OffMax);
         uint32_t sync_phase = 0;
         auto sync_b = [&]() -> bool {                         // bounded barrier of the state warps
             arrive(wgb_bar);
             return wait(wgb_bar, sync_phase++);
         };
         auto initial = [&](int col) -> float {
-            if (d >= r.kd || col >= r.vd) return 0.f;
-            if (!first) return r.seg[at_seg + (int64_t)d * r.vd + col];
-            return r.init ? r.init[at_seq + (r.init_t ? (int64_t)col * r.kd + d : (int64_t)d * r.vd + col)] : 0.f;
+            if (second || ch >= r.kd || col >= r.vd) return 0.f;
+            if (!first) return r.seg[at_seg + (int64_t)ch * r.vd + col];
+            return r.init ? r.init[at_seq + (r.init_t ? (int64_t)col * r.kd + ch : (int64_t)ch * r.vd + col)] : 0.f;
         };
         float state[kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) state[j] = has_init && live ? initial(col0 + j) : 0.f;
+        for (int j = 0; j < kCols; ++j) state[j] = has_init && nch > 0 ? initial(col0 + j) : 0.f;
+        if (L::Stacked && L::KtCols == 128 && second) {
+            // the third part's rows 64-127 stay zero
+            const uint32_t zero[16] = {};
+            tmem_st16(tbase + row + L::Kt + 64 + half * 32, zero);
+            tmem_st16(tbase + row + L::Kt + 64 + half * 32 + 16, zero);
+        }
         // state <- g^n state + (own state of chunk c), once its products are done
         auto advance = [&](int c) -> bool {
             if (!wait(bar_st, c)) return false;
             tc_fence_after();
-            if (live) {
-                const float keep = pw[chunk_n(c)], inv = 1.f / rs;
+            const float keep = pw[chunk_n(c)], inv = 1.f / rs;
 #pragma unroll
-                for (int blk = 0; blk < kCols / 32; ++blk) {
-                    uint32_t s[32];
-                    tmem_ld32(tbase + row + L::C + col0 + blk * 32, s);
-                    tc_wait_ld();
+            for (int blk = 0; blk < kCols / 32; ++blk) {
+                uint32_t s[32];
+                tmem_ld32(tbase + row + L::C + col0 + blk * 32, s);
+                tc_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float own = F16 ? __uint_as_float(s[j]) * inv : __uint_as_float(s[j]);
-                        state[blk * 32 + j] = fmaf(keep, state[blk * 32 + j], own);
-                    }
+                for (int j = 0; j < 32; ++j) {
+                    const float own = F16 ? __uint_as_float(s[j]) * inv : __uint_as_float(s[j]);
+                    state[blk * 32 + j] = fmaf(keep, state[blk * 32 + j], own);
                 }
             }
             return true;
@@ -681,7 +763,7 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
             const int nv = chunk_n(c);
             const bool carry = c > 0 || has_init;
             const bool more = c + 1 < nch || want_fin;        // the state behind this chunk is wanted
-            uint8_t* base = smem + L::OffStage + st * L::StageBytes;
+            uint8_t* base = smem + st * L::StageBytes;
             if (more && nv != kw_n) {
                 ok = sync_b();
                 if (!ok) break;
@@ -712,19 +794,17 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
                     if (c > 0) ok = wait(&bar_o[(c - 1) % NA], (c - 1) / NA);
                     if (!ok) break;
                     if (F16 && ts == 0) carry_inv[c & 3] = 1.f / cs;
-                    if (live) {
-                        uint8_t* dst = smem + L::OffCarry + d * 128;
+                    uint8_t* dst = smem + L::OffCarry + d * 128;
 #pragma unroll
-                        for (int q = 0; q < kCols / 8; ++q) {
-                            uint4 v;
-                            auto two = [&](int j) { return pack<F16>(state[q * 8 + j] * cs, state[q * 8 + j + 1] * cs); };
-                            v.x = two(0);
-                            v.y = two(2);
-                            v.z = two(4);
-                            v.w = two(6);
-                            const int ch = col0 / 8 + q;
-                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (KP * 128) + (((ch & 7) ^ (d & 7)) << 4)) = v;
-                        }
+                    for (int q = 0; q < kCols / 8; ++q) {
+                        uint4 v;
+                        auto two = [&](int j) { return pack<F16>(state[q * 8 + j] * cs, state[q * 8 + j + 1] * cs); };
+                        v.x = two(0);
+                        v.y = two(2);
+                        v.z = two(4);
+                        v.w = two(6);
+                        const int vc = col0 / 8 + q;
+                        *reinterpret_cast<uint4*>(dst + (vc >> 3) * 16384 + (((vc & 7) ^ (d & 7)) << 4)) = v;
                     }
                     fence_proxy_async_smem();
                 }
@@ -738,149 +818,92 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
             if (p.cu && nv < kChunk) {
                 const int rows = (nv + 15) / 16 * 16 - nv;
                 for (int e = ts; e < rows * (VP / 8); e += kStateWarps * 32) {
-                    const int rr = nv + e / (VP / 8), ch = e % (VP / 8);
-                    *reinterpret_cast<uint4*>(base + 2 * L::XBytes + (ch >> 3) * 16384 + rr * 128 + (ch & 7) * 16) =
+                    const int rr = nv + e / (VP / 8), vc = e % (VP / 8);
+                    *reinterpret_cast<uint4*>(base + 2 * L::XBytes + (vc >> 3) * 16384 + rr * 128 + (vc & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 arrive(z_ready);
             }
-            const uint8_t* keys = base + L::XBytes;
-            uint32_t late[kLate ? 32 : 1];
-            if constexpr (L::KtSmem) {
-                // eight channels of four tokens a thread, in the tile's own
-                // layout (the MMA reads it with the channel as its row)
-                const int ch = ts & 7;
-                if (F16 && more) {
-                    // scale each channel so that its largest weighted key is just below 2^15
-                    __half2 m[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) m[q] = __float2half2_rn(0.f);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int j = (ts >> 3) + q * 32;
-                        if (j < nv) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(keys + j * 128 + ((ch ^ (j & 7)) << 4));
-                            const __half2* x = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) m[e] = __hmax2(m[e], __habs2(x[e]));
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], 8));
-                        m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], 16));
-                    }
-                    if (lane < 8) *reinterpret_cast<uint4*>(kmax_sh + sw * KP + ch * 8) = *reinterpret_cast<uint4*>(m);
-                    ok = sync_b();
-                    if (!ok) break;
-                    if (ts < KP) {
-                        uint32_t top = 0;                     // fp16 magnitudes order like integers
-#pragma unroll
-                        for (int w = 0; w < kStateWarps; ++w) top = max(top, (uint32_t)kmax_sh[w * KP + ts]);
-                        rs_sh[ts] = top < 0x7c00u ? fp16_scale(__half2float(__ushort_as_half((unsigned short)top)) *
-                                                               fabsf(r.key_scale) * fmaxf(1.f, pw[nv]))
-                                                  : 1.f;
-                    }
-                    ok = sync_b();
-                    if (!ok) break;
-                    if (live) rs = rs_sh[d];
-                }
-                if (more) {
-                    float sc[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) sc[e] = F16 ? rs_sh[ch * 8 + e] : 1.f;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int j = (ts >> 3) + q * 32;
-                        const uint32_t off = j * 128 + ((ch ^ (j & 7)) << 4);
-                        const uint4 v = *reinterpret_cast<const uint4*>(keys + off);
-                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                        const float w = kw[j];
-                        uint32_t part[3][4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 kk = unpack<F16>(x[e]);
-                            // a select, not a product: what lies behind the end may be inf or NaN
-                            float f0 = j < nv ? kk.x * w : 0.f, f1 = j < nv ? kk.y * w : 0.f;
-                            if constexpr (F16) {
-                                f0 *= sc[2 * e];
-                                f1 *= sc[2 * e + 1];
-                            }
-#pragma unroll
-                            for (int t = 0; t < kParts; ++t) {
-                                part[t][e] = pack<F16>(f0, f1);
-                                const float2 back = unpack<F16>(part[t][e]);
-                                f0 -= back.x;
-                                f1 -= back.y;
-                            }
-                        }
-#pragma unroll
-                        for (int t = 0; t < kParts; ++t)
-                            *reinterpret_cast<uint4*>(smem + t * L::XBytes + off) =
-                                make_uint4(part[t][0], part[t][1], part[t][2], part[t][3]);
-                    }
-                    fence_proxy_async_smem();
-                }
-            } else {
+            uint32_t late[L::Late ? 32 : 1];
+            if (more) {
                 // one channel of 64 tokens a thread, transposed into TMEM
-                const uint8_t* kcol = keys + (d >> 6) * 16384 + (d & 7) * 2;
-                const int cb = (d & 63) >> 3;
-                auto key = [&](int j) -> uint32_t {
-                    return *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
+                const uint8_t* kcol = base + L::XBytes + (ch >> 6) * 16384 + (ch & 7) * 2 + half * 64 * 128;
+                const int cb = (ch & 63) >> 3;
+                auto keys2 = [&](int j) -> uint32_t {         // tokens j and j + 1 of the half
+                    const uint32_t a = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
+                    const uint32_t e = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + 128 + ((cb ^ (j + 1 & 7)) << 4));
+                    return a | e << 16;
                 };
-                if (F16 && more) {
-                    // scale the row so that its largest weighted key is just below 2^15
-                    uint32_t m = 0;
-#pragma unroll 16
-                    for (int j = 0; j < kChunk; ++j) {
-                        const uint32_t v = key(j) & 0x7fffu;
-                        m = j < nv ? max(m, v) : m;
+                uint32_t raw[F16 ? 32 : 1];
+                if constexpr (F16) {
+                    // scale the channel so that its largest weighted key is just below 2^15
+                    uint32_t m = 0;                           // magnitudes order like integers
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        raw[j] = keys2(2 * j);
+                        const int t = half * 64 + 2 * j;
+                        m = t < nv ? max(m, raw[j] & 0x7fffu) : m;
+                        m = t + 1 < nv ? max(m, raw[j] >> 16 & 0x7fffu) : m;
                     }
-                    rs = 1.f;
-                    if (m < 0x7c00u)
-                        rs = fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) * fabsf(r.key_scale) *
-                                        fmaxf(1.f, pw[nv]));
+                    // (the last chunk's maxima are read: its products are done)
+                    if (!second) kmax_sh[half * KP + ch] = (uint16_t)m;
+                    ok = sync_b();
+                    if (!ok) break;
+                    m = max(m, (uint32_t)kmax_sh[(half ^ 1) * KP + ch]);
+                    rs = m < 0x7c00u ? fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) *
+                                                  fabsf(r.key_scale) * fmaxf(1.f, pw[nv]))
+                                     : 1.f;
                 }
-                if (more) {
 #pragma unroll
-                    for (int jb = 0; jb < 4; ++jb) {
-                        uint32_t part[3][8];
+                for (int jb = 0; jb < 4; ++jb) {
+                    uint32_t part[3][8];
 #pragma unroll
-                        for (int j2 = 0; j2 < 8; ++j2) {
-                            const int j = half * 64 + jb * 16 + j2 * 2;
-                            const float2 w = *reinterpret_cast<const float2*>(kw + j);
-                            const float2 kk = unpack<F16>(key(j) | (key(j + 1) << 16));
-                            float f0 = j < nv ? kk.x * w.x : 0.f, f1 = j + 1 < nv ? kk.y * w.y : 0.f;
+                    for (int j4 = 0; j4 < 8; j4 += 2) {
+                        const int j0 = jb * 16 + j4 * 2;
+                        const float4 w = *reinterpret_cast<const float4*>(kw + half * 64 + j0);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int t = half * 64 + j0 + 2 * e;
+                            float2 f = unpack<F16>(F16 ? raw[jb * 8 + j4 + e] : keys2(j0 + 2 * e));
+                            // a select, not a product: what lies behind the end may be inf or NaN
+                            f.x = t < nv ? f.x * (e ? w.z : w.x) : 0.f;
+                            f.y = t + 1 < nv ? f.y * (e ? w.w : w.y) : 0.f;
                             if constexpr (F16) {
-                                f0 *= rs;
-                                f1 *= rs;
+                                f.x *= rs;
+                                f.y *= rs;
                             }
 #pragma unroll
-                            for (int q = 0; q < kParts; ++q) {
-                                part[q][j2] = pack<F16>(f0, f1);
-                                const float2 back = unpack<F16>(part[q][j2]);
-                                f0 -= back.x;
-                                f1 -= back.y;
+                            for (int q = 0; q < L::Parts; ++q) {
+                                part[q][j4 + e] = pack<F16>(f.x, f.y);
+                                const float2 back = unpack<F16>(part[q][j4 + e]);
+                                f.x -= back.x;
+                                f.y -= back.y;
                             }
-                        }
-                        const uint32_t at = tbase + row + L::Kt + (half * 4 + jb) * 8;
-                        if constexpr (kLate) {
-                            tmem_st8(at, part[2]);
-                            tmem_st8(at + 64, part[1]);
-#pragma unroll
-                            for (int j2 = 0; j2 < 8; ++j2) late[jb * 8 + j2] = part[0][j2];
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < kParts; ++q) tmem_st8(at + q * 64, part[q]);
                         }
                     }
+                    const uint32_t at = tbase + row + L::Kt + half * 32 + jb * 8;
+                    if constexpr (L::Stacked) {
+                        if (second)
+                            tmem_st8(at, part[1]);
+                        else
+                            tmem_st8(at, part[0]);
+                        if (L::KtCols == 128 && !second) tmem_st8(at + 64, part[2]);
+                    } else if constexpr (L::Late) {
+                        tmem_st8(at, part[1]);
+                        tmem_st8(at + 64, part[2]);
+#pragma unroll
+                        for (int j2 = 0; j2 < 8; ++j2) late[jb * 8 + j2] = part[0][j2];
+                    } else {
+                        tmem_st8(at, part[0]);
+                        tmem_st8(at + 64, part[1]);
+                    }
                 }
-                tc_wait_st();
             }
+            tc_wait_st();
             tc_fence_before();
             arrive(kt_ready);
-            if constexpr (kLate) {
+            if constexpr (L::Late) {
                 if (more) {
                     ok = wait(bar_kt, c);
                     if (!ok) break;
@@ -894,17 +917,29 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
             }
         }
         if (ok && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
-            float* dst = STATE_ONLY ? r.seg + at_seg : r.fin + at_seq;
+            float* dst = (STATE_ONLY ? r.seg + at_seg : r.fin + at_seq) + (int64_t)ch * r.vd;
             if (nch > 0)
                 ok = advance(nch - 1);
             else
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) state[j] = live ? initial(col0 + j) : 0.f;
-            if (ok && d < r.kd && live) {
+                for (int j = 0; j < kCols; ++j) state[j] = initial(col0 + j);
+            if constexpr (L::Stacked) {
+                // rows 64-127 hand their half of the sum over, in the carry copy's place
+                if (ok && !STATE_ONLY && nch > 0) ok = wait(&bar_o[(nch - 1) % NA], (nch - 1) / NA);
+                float* sum = reinterpret_cast<float*>(smem + L::OffCarry);      // [VP][64]
+                if (ok && second)
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) sum[(col0 + j) * 64 + ch] = state[j];
+                if (ok) ok = sync_b();
+                if (ok && !second)
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) state[j] += sum[(col0 + j) * 64 + ch];
+            }
+            if (ok && ch < r.kd && !second) {
 #pragma unroll
                 for (int j = 0; j < kCols; j += 4)
                     if (col0 + j < r.vd)
-                        *reinterpret_cast<float4*>(dst + (int64_t)d * r.vd + col0 + j) =
+                        *reinterpret_cast<float4*>(dst + col0 + j) =
                             make_float4(state[j], state[j + 1], state[j + 2], state[j + 3]);
             }
         }
@@ -919,7 +954,8 @@ __global__ void __launch_bounds__(Layout<KP, VP>::Threads, 1) la_kernel(const __
 }
 
 // Segment states of split sequences: from each segment's own state (zero
-// start) to the state in front of it, in the role's direction of time.
+// start) to the state in front of it, in the role's direction of time, and
+// the final state.
 __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params p) {
     const Role& r = p.role[blockIdx.z];
     const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H;
@@ -957,21 +993,24 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
     }
     const int64_t step = (int64_t)p.H * mat;
     float* at = r.seg + ((int64_t)sid0 * p.H + h) * mat + e;
+    // the last segment's own state is there where the final state is wanted
+    const int have = r.fin ? count : count - 1;
     // the loads of four segments go out together: their addresses do not
     // depend on the running state
     for (int s = 0; s < count; s += 4) {
         float local[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-            if (s + q < count - 1) local[q] = at[(int64_t)(r.rev ? count - 1 - s - q : s + q) * step];
+            if (s + q < have) local[q] = at[(int64_t)(r.rev ? count - 1 - s - q : s + q) * step];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (s + q >= count) break;
             const int i = r.rev ? count - 1 - s - q : s + q;
             at[(int64_t)i * step] = run;
-            if (s + q < count - 1) run = fmaf(i == count - 1 ? tail : whole, run, local[q]);
+            if (s + q < have) run = fmaf(i == count - 1 ? tail : whole, run, local[q]);
         }
     }
+    if (r.fin) r.fin[((int64_t)seq * p.H + h) * mat + e] = run;
 }
 
 __device__ __forceinline__ void used_tokens(const int32_t* cu, int nseq, int64_t T, int64_t& lo, int64_t& hi) {
@@ -1051,10 +1090,11 @@ EncodeTiled encode_tiled() {
     return fn;
 }
 
-// [B, T, H, D] with element strides: tiles of 128 tokens x 64 channels of one
-// head, rows of 128 bytes in the 128-byte swizzle; what lies outside is zero.
+// [B, T, H, D] with element strides: tiles of `tokens` x 128 bytes of one
+// head, in the 128-byte swizzle; what lies outside reads as zero and is not
+// written.
 int make_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64_t T, int64_t H, int64_t D,
-             const int64_t* stride) {
+             const int64_t* stride, int tokens = kChunk) {
     // the encoder is a driver call: it needs the device's context bound to
     // this thread, which autograd's threads have not done before their first
     // runtime call
@@ -1064,10 +1104,14 @@ int make_map(CUtensorMap* m, const void* base, int dtype, int64_t B, int64_t T, 
     const EncodeTiled fn = encode_tiled();
     if (!fn) return fail(FFTCONV_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
     const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T, (cuuint64_t)B};
-    auto bytes = [](int64_t extent, int64_t s) { return (cuuint64_t)(extent > 1 ? s * 2 : 16); };
+    const int size = dtype == FFTCONV_F32 ? 4 : 2;
+    auto bytes = [&](int64_t extent, int64_t s) { return (cuuint64_t)(extent > 1 ? s * size : 16); };
     const cuuint64_t strides[3] = {bytes(H, stride[2]), bytes(T, stride[1]), bytes(B, stride[0])};
-    const cuuint32_t box[4] = {64, 1, kChunk, 1}, one[4] = {1, 1, 1, 1};
-    const CUresult e = fn(m, dtype == FFTCONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+    const cuuint32_t box[4] = {(cuuint32_t)(128 / size), 1, (cuuint32_t)tokens, 1}, one[4] = {1, 1, 1, 1};
+    const CUresult e = fn(m,
+                          dtype == FFTCONV_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                          : dtype == FFTCONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                           4, const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1085,36 +1129,39 @@ int sm_count() {
     return n;
 }
 
-template <int KP, int VP, bool F16, bool STATE_ONLY>
+template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
 cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
+    using L = Layout<KP, VP, F16, EXACT>;
     static std::atomic<uint64_t> ready{0};                    // devices whose kernel has its shared memory size
-    auto* kern = la_kernel<KP, VP, F16, STATE_ONLY>;
+    auto* kern = la_kernel<KP, VP, F16, STATE_ONLY, EXACT>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !((ready.load(std::memory_order_relaxed) >> dev) & 1)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<KP, VP>::Bytes);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::Bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
     }
     void* args[] = {const_cast<Params*>(&p)};
-    return cudaLaunchKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(Layout<KP, VP>::Threads), args,
-                            Layout<KP, VP>::Bytes, s);
+    return cudaLaunchKernel(reinterpret_cast<const void*>(kern), dim3((unsigned)ctas), dim3(L::Threads), args, L::Bytes,
+                            s);
+}
+
+template <int KP, int VP, bool STATE_ONLY>
+cudaError_t launch_type(const Params& p, bool f16, bool exact, int64_t ctas, cudaStream_t s) {
+    // (two fp16 parts have 22 bits: one kernel for both)
+    if (f16) return launch<KP, VP, true, STATE_ONLY, false>(p, ctas, s);
+    return exact ? launch<KP, VP, false, STATE_ONLY, true>(p, ctas, s)
+                 : launch<KP, VP, false, STATE_ONLY, false>(p, ctas, s);
 }
 
 template <bool STATE_ONLY>
-cudaError_t launch_kernel(const Params& p, bool f16, int kp, int vp, int64_t ctas, cudaStream_t s) {
-    const int which = (kp == 128 ? 4 : 0) + (vp == 128 ? 2 : 0) + (f16 ? 1 : 0);
-    switch (which) {
-        case 0: return launch<64, 64, false, STATE_ONLY>(p, ctas, s);
-        case 1: return launch<64, 64, true, STATE_ONLY>(p, ctas, s);
-        case 2: return launch<64, 128, false, STATE_ONLY>(p, ctas, s);
-        case 3: return launch<64, 128, true, STATE_ONLY>(p, ctas, s);
-        case 4: return launch<128, 64, false, STATE_ONLY>(p, ctas, s);
-        case 5: return launch<128, 64, true, STATE_ONLY>(p, ctas, s);
-        case 6: return launch<128, 128, false, STATE_ONLY>(p, ctas, s);
-        default: return launch<128, 128, true, STATE_ONLY>(p, ctas, s);
-    }
+cudaError_t launch_kernel(const Params& p, bool f16, bool exact, int kp, int vp, int64_t ctas, cudaStream_t s) {
+    if (kp == 64)
+        return vp == 64 ? launch_type<64, 64, STATE_ONLY>(p, f16, exact, ctas, s)
+                        : launch_type<64, 128, STATE_ONLY>(p, f16, exact, ctas, s);
+    return vp == 64 ? launch_type<128, 64, STATE_ONLY>(p, f16, exact, ctas, s)
+                    : launch_type<128, 128, STATE_ONLY>(p, f16, exact, ctas, s);
 }
 
 // How a call's sequences are cut into segments, one CTA for each (segment,
@@ -1227,8 +1274,10 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
     const int kp = r.kd > 64 ? 128 : 64, vp = r.vd > 64 ? 128 : 64;
     const bool f16 = d.dtype == FFTCONV_F16;
     const int64_t ctas = s.max_seg * d.H * p.nroles;
+    bool exact = false;                       // a state is a result
+    for (int i = 0; i < p.nroles; ++i) exact |= p.role[i].fin != nullptr;
     if (s.on) {
-        cudaError_t e = launch_kernel<true>(p, f16, kp, vp, ctas, stream);
+        cudaError_t e = launch_kernel<true>(p, f16, exact, kp, vp, ctas, stream);
         if (e != cudaSuccess) return e;
         const int64_t seqs = d.nseq > 0 ? d.nseq : d.B;
         void* args[] = {const_cast<Params*>(&p)};
@@ -1237,7 +1286,8 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
                              dim3(256), args, 0, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_kernel<false>(p, f16, kp, vp, ctas, stream);
+    // (packed sequences that are not cut take their final state from this launch)
+    return launch_kernel<false>(p, f16, exact && (!s.on || p.cu), kp, vp, ctas, stream);
 }
 
 cudaError_t copy_states(float* dst, const float* src, int64_t count, cudaStream_t s) {
@@ -1312,8 +1362,10 @@ int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void
     if (int e = make_map(&p.maps[0], q, d.dtype, d.B, d.T, d.Hq, d.K, d.q_stride)) return e;
     if (int e = make_map(&p.maps[1], k, d.dtype, d.B, d.T, d.Hk, d.K, d.k_stride)) return e;
     if (int e = make_map(&p.maps[2], v, d.dtype, d.B, d.T, d.Hv, d.V, d.v_stride)) return e;
+    if (int e = make_map(&p.maps[3], o, d.dtype, d.B, d.T, d.H, d.V, d.o_stride, 32)) return e;
     Role& r = p.role[0];
     r.x = 0; r.y = 1; r.z = 2;
+    r.out_map = 3;
     r.x_div = (int)(d.H / d.Hq); r.y_div = (int)(d.H / d.Hk); r.z_div = (int)(d.H / d.Hv);
     r.kd = (int)d.K; r.vd = (int)d.V;
     r.a_in = r.a_carry = d.scale;
@@ -1429,6 +1481,10 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
         r.out_h = dims[i];
         r.out_t = hh * dims[i];
         r.out_b = d.T * hh * dims[i];
+        r.out_map = 4 + i;
+        const int64_t st[3] = {r.out_b, r.out_t, r.out_h};
+        if (int e = make_map(&p.maps[4 + i], r.out, part[i] ? (int)FFTCONV_F32 : d.dtype, d.B, d.T, hh, dims[i], st, 32))
+            return e;
     }
     cudaError_t e = cudaSuccess;
     if (d.nseq > 0)
