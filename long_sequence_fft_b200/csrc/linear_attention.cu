@@ -188,6 +188,29 @@ __device__ __forceinline__ float2 unpack(uint32_t v) {
     }
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ void scale2(uint32_t& a, uint32_t& b, float2 f) {
+    const float2 r = mul2(make_float2(__uint_as_float(a), __uint_as_float(b)), f);
+    a = __float_as_uint(r.x);
+    b = __float_as_uint(r.y);
+}
+
 template <bool F16>
 __device__ __forceinline__ uint4 pack8(const uint32_t* s) {
     uint4 v;
@@ -223,23 +246,26 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // Parts of the weighted keys and how they lie in TMEM: EXACT where the state
 // itself is a result (fp32, so all 24 bits of a weighted bf16 key count),
 // else 16 bits, far below the rounding of what the state then goes into.
-template <int KP, int VP, bool F16, bool EXACT>
+template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
 struct Layout {
     // 64 channels: two parts are stacked on the 128 rows of one MMA, and the
     // state is kept as the two rows' sum; 128 channels: one MMA a part
     static constexpr bool Stacked = KP == 64;
     static constexpr int Parts = F16 || !EXACT ? 2 : 3;
-    static constexpr bool Late = !Stacked && Parts == 3;      // the last part waits for the first one's columns
-    static constexpr int KtCols = Stacked ? (Parts == 3 ? 128 : 64) : 128;
+    // beside P and the output three parts of 128 channels do not fit: the last
+    // one waits for the first one's columns
+    static constexpr bool Late = !STATE_ONLY && !Stacked && Parts == 3;
+    static constexpr int KtCols = Stacked ? (Parts == 3 ? 128 : 64) : Late ? 128 : Parts * 64;
+    // where the columns suffice, a chunk's keys are weighed while the last one's are multiplied
+    static constexpr int KtBufs = STATE_ONLY || KtCols == 64 ? 2 : 1;
     // groups of row warps, which take chunks in turn, each with a score tile
     static constexpr int Groups = VP == 64 ? 2 : 1;
-    static constexpr int OutBufs = KP == 64 && VP == 64 && KtCols == 64 ? 2 : 1;
     static constexpr int RowWarps = 4 * Groups;
     static constexpr int LoadWarp = RowWarps + kStateWarps, MmaWarp = LoadWarp + 1, StateMmaWarp = LoadWarp + 2;
     static constexpr int Threads = (RowWarps + kStateWarps + 3) * 32;
     static constexpr int XBytes = KP * kChunk * 2, ZBytes = VP * kChunk * 2;
-    static constexpr int StageBytes = 2 * XBytes + ZBytes;
-    static constexpr int CarryBytes = 128 * VP * 2;
+    static constexpr int OffY = STATE_ONLY ? 0 : XBytes, OffZ = OffY + XBytes, StageBytes = OffZ + ZBytes;
+    static constexpr int CarryBytes = STATE_ONLY && !Stacked ? 0 : 128 * VP * 2;
     static constexpr int Stages = StageBytes <= 49152 ? 4 : StageBytes <= 65536 ? 3 : 2;
     static constexpr int OffCarry = Stages * StageBytes;
     static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d|, d = j - i in [-127, 127]
@@ -248,12 +274,12 @@ struct Layout {
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, TMEM base, scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int OffMax = OffBar + 26 * 8;            // (fp16) channel maxima of each half's tokens
-    static constexpr int Bytes = OffMax + (F16 ? 2 * KP * 2 : 0);
+    static constexpr int OffMax = OffBar + 28 * 8;            // (fp16) channel maxima of each half's tokens
+    static constexpr int Bytes = OffMax + (F16 ? KtBufs * 2 * KP * 2 : 0);
     // TMEM columns
-    static constexpr int S = 0, O = Groups * 128, C = O + OutBufs * VP, Kt = C + VP;
+    static constexpr int S = 0, O = S + Groups * 128, C = STATE_ONLY ? 0 : O + VP, Kt = C + VP;
     static_assert(Bytes <= 232448, "shared memory");
-    static_assert(Kt + KtCols <= 512, "TMEM columns");
+    static_assert(Kt + KtBufs * KtCols <= 512, "TMEM columns");
 };
 
 // One CTA: one (segment, head, role).  Row warps (one or two groups of four
@@ -271,8 +297,10 @@ struct Layout {
 // carry's copy by its largest value, the weighted keys by channel), so that
 // nothing overflows fp16's range or falls below it.
 template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
-__global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_kernel(const __grid_constant__ Params p) {
-    using L = Layout<KP, VP, F16, EXACT>;
+__global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Threads, 1)
+    la_kernel(const __grid_constant__ Params p) {
+    using L = Layout<KP, VP, F16, STATE_ONLY, EXACT>;
+    constexpr bool kAhead = L::KtBufs == 2;                   // keys weighed one chunk ahead
     constexpr int NA = L::Groups;
     extern __shared__ __align__(1024) uint8_t smem[];
     float* tab = reinterpret_cast<float*>(smem + L::OffTab);
@@ -299,7 +327,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
     uint64_t* carry_ready = bars + 22;
     uint64_t* z_ready = bars + 23;                            // rows behind a packed sequence zeroed
     uint64_t* wgb_bar = bars + 24;
-    uint64_t* bar_fin = bars + 25;                            // both MMA warps
+    uint64_t* c_free = bars + 25;                             // the chunk's own state read
+    uint64_t* bar_fin = bars + 26;                            // both MMA warps
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -329,7 +358,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
         for (int i = 14; i < 18; ++i) mbar_init(bars + i, 4);
         mbar_init(bar_st, 1);
         mbar_init(bar_kt, 1);
-        for (int i = 20; i < 25; ++i) mbar_init(bars + i, kStateWarps);
+        for (int i = 20; i < 26; ++i) mbar_init(bars + i, kStateWarps);
         mbar_init(bar_fin, STATE_ONLY ? 1 : 2);
         *abort_flag = 0;
         fence_barrier_init();
@@ -401,11 +430,11 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                 }
                 uint8_t* base = smem + st * L::StageBytes;
                 const int t = t0 + chunk_at(c);
-                mbar_expect_tx(&full[st], STATE_ONLY ? L::StageBytes - L::XBytes : L::StageBytes);
-                for (int d = 0; d < KP; d += 64) tma_load(base + L::XBytes + d * 256, my, d, hy, t, b, &full[st]);
+                mbar_expect_tx(&full[st], L::StageBytes);
+                for (int d = 0; d < KP; d += 64) tma_load(base + L::OffY + d * 256, my, d, hy, t, b, &full[st]);
                 if (!STATE_ONLY)
                     for (int d = 0; d < KP; d += 64) tma_load(base + d * 256, mx, d, hx, t, b, &full[st]);
-                for (int d = 0; d < VP; d += 64) tma_load(base + 2 * L::XBytes + d * 256, mz, d, hz, t, b, &full[st]);
+                for (int d = 0; d < VP; d += 64) tma_load(base + L::OffZ + d * 256, mz, d, hz, t, b, &full[st]);
                 issued = c + 1;
             }
             // nothing of this CTA's loads is in flight when it ends
@@ -425,7 +454,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
             // scores of chunk `scored`; the score tile's last P is used up
             auto score = [&]() {
                 const uint32_t base = sb + scored % L::Stages * L::StageBytes;
-                const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::XBytes, 16, 1024, 2);
+                const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::OffY, 16, 1024, 2);
                 tc_fence_after();
 #pragma unroll
                 for (int k = 0; k < KP / 16; ++k) {
@@ -447,6 +476,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                             break;
                         }
                         if (__all_sync(0xffffffffu, mbar_test_wait(bar, phase & 1))) return true;
+                        __nanosleep(40);
                         if ((i & 31) == 31 && __any_sync(0xffffffffu, ld_shared_volatile(abort_flag))) return false;
                     }
                 }
@@ -458,15 +488,15 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                 const bool carry = c > 0 || has_init;
                 const uint32_t base = sb + st * L::StageBytes;
                 const uint64_t d_x = make_desc(base, 16, 1024, 2);
-                const uint64_t d_z = make_desc(base + 2 * L::XBytes, 16384, 1024, 2);
-                const uint32_t t_o = tbase + L::O + c % L::OutBufs * VP;
+                const uint64_t d_z = make_desc(base + L::OffZ, 16384, 1024, 2);
+                const uint32_t t_o = tbase + L::O;
                 if (scored == c) {
                     ok = wait(&full[st], c / L::Stages) && (c < NA || wait(&bar_pv[ga], c / NA - 1));
                     if (!ok) break;
                     score();
                 }
                 ok = wait_busy(carry_ready, c, c);
-                if (ok && c >= L::OutBufs) ok = wait(&o_free[(c - L::OutBufs) % NA], (c - L::OutBufs) / NA);
+                if (ok && c > 0) ok = wait(&o_free[(c - 1) % NA], (c - 1) / NA);
                 if (!ok) break;
                 tc_fence_after();
                 if (carry) {
@@ -495,22 +525,22 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
         // The smallest parts first: the MMA truncates each sum, so few steps
         // should meet a large one.
         const uint32_t id = idesc_f16_f32(128, VP) | kFmt | kTransB;
-        const uint32_t sb = smem_u32(smem), t_c = tbase + L::C, t_kt = tbase + L::Kt;
+        const uint32_t sb = smem_u32(smem), t_c = tbase + L::C;
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int st = c % L::Stages;
             const int ks = (chunk_n(c) + 15) / 16;
-            const uint64_t d_z = make_desc(sb + st * L::StageBytes + 2 * L::XBytes, 16384, 1024, 2);
+            const uint64_t d_z = make_desc(sb + st * L::StageBytes + L::OffZ, 16384, 1024, 2);
+            const uint32_t t_kt = tbase + L::Kt + c % L::KtBufs * L::KtCols;
             ok = wait(kt_ready, c);
             if (!ok) break;
-            tc_fence_after();
             if (c + 1 < nch || want_fin) {
-                if constexpr (L::KtCols == 64) {
-                    token_mma(t_c, t_kt, d_z, id, ks, 0u);
-                } else {
-                    token_mma(t_c, t_kt + 64, d_z, id, ks, 0u);
-                    token_mma(t_c, t_kt, d_z, id, ks, 1u);
-                }
+                if (kAhead && c > 0) ok = wait(c_free, c - 1);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int part = L::KtCols / 64 - 1; part >= 0; --part)
+                    token_mma(t_c, t_kt + part * 64, d_z, id, ks, part == L::KtCols / 64 - 1 ? 0u : 1u);
                 if constexpr (L::Late) {
                     tc_commit_warp(bar_kt);
                     ok = wait(late_ready, c);
@@ -538,7 +568,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                 const int nv = chunk_n(c);
                 const bool carry = c > 0 || has_init;
                 const int jlo = rev ? i : 0, jhi = rev ? nv - 1 : i;
-                const uint32_t t_o = tbase + row + L::O + c % L::OutBufs * VP;
+                const uint32_t t_o = tbase + row + L::O;
                 // columns 32 blk .. 32 blk + 31: 0 masked, 1 on the border, 2 inside
                 auto kind = [&](int blk) {
                     if (rev ? blk < wr : blk > wr) return 0;
@@ -553,10 +583,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
 #pragma unroll
                         for (int j = 0; j < 32; j += 4) {
                             const float4 w = *reinterpret_cast<const float4*>(colw + j);
-                            s[j] = __float_as_uint(__uint_as_float(s[j]) * (f * w.x));
-                            s[j + 1] = __float_as_uint(__uint_as_float(s[j + 1]) * (f * w.y));
-                            s[j + 2] = __float_as_uint(__uint_as_float(s[j + 2]) * (f * w.z));
-                            s[j + 3] = __float_as_uint(__uint_as_float(s[j + 3]) * (f * w.w));
+                            scale2(s[j], s[j + 1], mul2(make_float2(f, f), make_float2(w.x, w.y)));
+                            scale2(s[j + 2], s[j + 3], mul2(make_float2(f, f), make_float2(w.z, w.w)));
                         }
                     } else {
                         const float* w = tab + 127 + blk * 32 - i;
@@ -574,6 +602,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                 float scale = 1.f;
                 if constexpr (F16) {
                     float amax = 0.f;
+#pragma unroll 1
                     for (int blk = 0; blk < 4; ++blk) {
                         const int kd = kind(blk);
                         if (kd == 0) continue;
@@ -586,6 +615,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                     }
                     scale = fp16_scale(amax);
                 }
+#pragma unroll 1
                 for (int blk = 0; blk < 4; ++blk) {
                     const int kd = kind(blk);
                     uint32_t pk[16];
@@ -610,12 +640,13 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                     const int e = min(128, max(0, rev ? nv - 1 - i : i + 1));
                     float f = r.a_carry * pw[e];
                     if constexpr (F16) f *= carry_inv[c & 3] * scale;
+#pragma unroll 1
                     for (int blk = 0; blk < VP / 32; ++blk) {
                         uint32_t s[32];
                         tmem_ld32(t_o + blk * 32, s);
                         tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * f);
+                        for (int j = 0; j < 32; j += 2) scale2(s[j], s[j + 1], make_float2(f, f));
                         tmem_st32(t_o + blk * 32, s);
                     }
                 }
@@ -650,6 +681,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                         __syncwarp();
                     }
                 };
+#pragma unroll 1
                 for (int blk = 0; blk < VP / 32; ++blk) {
                     uint32_t s[32];
                     tmem_ld32(t_o + blk * 32, s);
@@ -660,7 +692,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                     }
                     if constexpr (F16) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(__uint_as_float(s[j]) * inv);
+                        for (int j = 0; j < 32; j += 2) scale2(s[j], s[j + 1], make_float2(inv, inv));
                     }
                     if (direct) {
                         const int64_t at = (int64_t)b * r.out_b + (int64_t)(t + i) * r.out_t + (int64_t)h * r.out_h;
@@ -717,7 +749,9 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
         const uint32_t row = (uint32_t)(bw * 32) << 16;
         const int64_t mat = (int64_t)r.kd * r.vd;
         const int64_t at_seq = ((int64_t)seq * p.H + h) * mat, at_seg = ((int64_t)sid * p.H + h) * mat;
-        float rs = 1.f;                                       // (fp16) power of two on this channel's weighted keys
+        // (fp16) powers of two on this channel's weighted keys: the chunk's at
+        // hand, and the one's whose own state is read next
+        float rs = 1.f, rs_done = 1.f;
         uint16_t* kmax_sh = reinterpret_cast<uint16_t*>(smem + L::OffMax);
         uint32_t sync_phase = 0;
         auto sync_b = [&]() -> bool {                         // bounded barrier of the state warps
@@ -735,14 +769,16 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
         if (L::Stacked && L::KtCols == 128 && second) {
             // the third part's rows 64-127 stay zero
             const uint32_t zero[16] = {};
-            tmem_st16(tbase + row + L::Kt + 64 + half * 32, zero);
-            tmem_st16(tbase + row + L::Kt + 64 + half * 32 + 16, zero);
+            for (int buf = 0; buf < L::KtBufs; ++buf) {
+                tmem_st16(tbase + row + L::Kt + buf * L::KtCols + 64 + half * 32, zero);
+                tmem_st16(tbase + row + L::Kt + buf * L::KtCols + 64 + half * 32 + 16, zero);
+            }
         }
         // state <- g^n state + (own state of chunk c), once its products are done
         auto advance = [&](int c) -> bool {
             if (!wait(bar_st, c)) return false;
             tc_fence_after();
-            const float keep = pw[chunk_n(c)], inv = 1.f / rs;
+            const float keep = pw[chunk_n(c)], inv = 1.f / rs_done;
 #pragma unroll
             for (int blk = 0; blk < kCols / 32; ++blk) {
                 uint32_t s[32];
@@ -756,24 +792,16 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
             }
             return true;
         };
-        int kw_n = -1;
-        bool ok = true;
-        for (int c = 0; c < nch; ++c) {
-            const int st = c % L::Stages;
-            const int nv = chunk_n(c);
+        // the state in front of chunk c, and its copy for the carry product
+        auto carry_on = [&](int c) -> bool {
             const bool carry = c > 0 || has_init;
-            const bool more = c + 1 < nch || want_fin;        // the state behind this chunk is wanted
-            uint8_t* base = smem + st * L::StageBytes;
-            if (more && nv != kw_n) {
-                ok = sync_b();
-                if (!ok) break;
-                if (ts < 128) kw[ts] = ts < nv ? r.key_scale * pw[rev ? ts + 1 : nv - 1 - ts] : 0.f;
-                kw_n = nv;
-                ok = sync_b();
-                if (!ok) break;
+            if (c > 0) {
+                if (!advance(c - 1)) return false;
+                if (kAhead) {
+                    tc_fence_before();
+                    arrive(c_free);
+                }
             }
-            if (c > 0) ok = advance(c - 1);
-            if (!ok) break;
             if constexpr (!STATE_ONLY) {
                 if (carry) {
                     float cs = 1.f;
@@ -784,15 +812,13 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                         for (int j = 0; j < kCols; ++j) amax = fmaxf(amax, fabsf(state[j]));
                         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
                         if (lane == 0) amax_sh[(c & 1) * 8 + sw] = __uint_as_float(top);
-                        ok = sync_b();
-                        if (!ok) break;
+                        if (!sync_b()) return false;
 #pragma unroll
                         for (int w = 0; w < kStateWarps; ++w) amax = fmaxf(amax, amax_sh[(c & 1) * 8 + w]);
                         cs = fp16_scale(amax);
                     }
                     // the last carry product has read the copy
-                    if (c > 0) ok = wait(&bar_o[(c - 1) % NA], (c - 1) / NA);
-                    if (!ok) break;
+                    if (c > 0 && !wait(&bar_o[(c - 1) % NA], (c - 1) / NA)) return false;
                     if (F16 && ts == 0) carry_inv[c & 3] = 1.f / cs;
                     uint8_t* dst = smem + L::OffCarry + d * 128;
 #pragma unroll
@@ -811,92 +837,100 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
                 tc_fence_before();
                 arrive(carry_ready);
             }
-            ok = wait(&full[st], c / L::Stages);
-            if (!ok) break;
+            return true;
+        };
+        // the weighted keys of chunk c
+        int kw_n = -1;
+        auto weigh_keys = [&](int c) -> bool {
+            const int st = c % L::Stages;
+            const int nv = chunk_n(c);
+            const bool more = c + 1 < nch || want_fin;        // the state behind this chunk is wanted
+            uint8_t* base = smem + st * L::StageBytes;
+            if (more && nv != kw_n) {
+                if (!sync_b()) return false;
+                if (ts < 128) kw[ts] = ts < nv ? r.key_scale * pw[rev ? ts + 1 : nv - 1 - ts] : 0.f;
+                kw_n = nv;
+                if (!sync_b()) return false;
+            }
+            if (!wait(&full[st], c / L::Stages)) return false;
             // rows behind a packed sequence belong to another one: their
             // values must not meet the zeros of P and the weighted keys
             if (p.cu && nv < kChunk) {
                 const int rows = (nv + 15) / 16 * 16 - nv;
                 for (int e = ts; e < rows * (VP / 8); e += kStateWarps * 32) {
                     const int rr = nv + e / (VP / 8), vc = e % (VP / 8);
-                    *reinterpret_cast<uint4*>(base + 2 * L::XBytes + (vc >> 3) * 16384 + rr * 128 + (vc & 7) * 16) =
+                    *reinterpret_cast<uint4*>(base + L::OffZ + (vc >> 3) * 16384 + rr * 128 + (vc & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 arrive(z_ready);
             }
-            uint32_t late[L::Late ? 32 : 1];
+            // one channel of 64 tokens a thread, transposed into TMEM
+            const uint8_t* kcol = base + L::OffY + (ch >> 6) * 16384 + (ch & 7) * 2 + half * 64 * 128;
+            const int cb = (ch & 63) >> 3;
+            auto keys2 = [&](int j) -> uint32_t {             // tokens j and j + 1 of the half (j even)
+                const uint32_t a = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
+                const uint32_t e = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + 128 + ((cb ^ (j & 7) ^ 1) << 4));
+                return a | e << 16;
+            };
+            // the parts of the weighted keys of tokens j0 .. j0 + 15 of the half
+            auto weighted = [&](int j0, uint32_t (&part)[3][8], int parts) {
+#pragma unroll
+                for (int j4 = 0; j4 < 8; j4 += 2) {
+                    const float4 w = *reinterpret_cast<const float4*>(kw + half * 64 + j0 + j4 * 2);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = half * 64 + j0 + (j4 + e) * 2;
+                        float2 f = mul2(unpack<F16>(keys2(j0 + (j4 + e) * 2)),
+                                        e ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
+                        if (nv < kChunk) {
+                            // a select, not a product: what lies behind the end may be inf or NaN
+                            if (t >= nv) f.x = 0.f;
+                            if (t + 1 >= nv) f.y = 0.f;
+                        }
+                        if constexpr (F16) f = mul2(f, make_float2(rs, rs));
+#pragma unroll
+                        for (int q = 0; q < 3; ++q) {
+                            if (q >= parts) break;
+                            part[q][j4 + e] = pack<F16>(f.x, f.y);
+                            if (q + 1 < parts) f = fma2(unpack<F16>(part[q][j4 + e]), make_float2(-1.f, -1.f), f);
+                        }
+                    }
+                }
+            };
+            const uint32_t t_kt = tbase + row + L::Kt + c % L::KtBufs * L::KtCols + half * 32;
             if (more) {
-                // one channel of 64 tokens a thread, transposed into TMEM
-                const uint8_t* kcol = base + L::XBytes + (ch >> 6) * 16384 + (ch & 7) * 2 + half * 64 * 128;
-                const int cb = (ch & 63) >> 3;
-                auto keys2 = [&](int j) -> uint32_t {         // tokens j and j + 1 of the half
-                    const uint32_t a = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
-                    const uint32_t e = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + 128 + ((cb ^ (j + 1 & 7)) << 4));
-                    return a | e << 16;
-                };
-                uint32_t raw[F16 ? 32 : 1];
                 if constexpr (F16) {
                     // scale the channel so that its largest weighted key is just below 2^15
                     uint32_t m = 0;                           // magnitudes order like integers
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        raw[j] = keys2(2 * j);
-                        const int t = half * 64 + 2 * j;
-                        m = t < nv ? max(m, raw[j] & 0x7fffu) : m;
-                        m = t + 1 < nv ? max(m, raw[j] >> 16 & 0x7fffu) : m;
+#pragma unroll 4
+                    for (int j = 0; j < 64; j += 2) {
+                        const uint32_t x = keys2(j);
+                        m = half * 64 + j < nv ? max(m, x & 0x7fffu) : m;
+                        m = half * 64 + j + 1 < nv ? max(m, x >> 16 & 0x7fffu) : m;
                     }
-                    // (the last chunk's maxima are read: its products are done)
-                    if (!second) kmax_sh[half * KP + ch] = (uint16_t)m;
-                    ok = sync_b();
-                    if (!ok) break;
-                    m = max(m, (uint32_t)kmax_sh[(half ^ 1) * KP + ch]);
+                    // (the place's last maxima are read: every warp has passed a later barrier)
+                    uint16_t* kmax = kmax_sh + c % L::KtBufs * 2 * KP;
+                    if (!second) kmax[half * KP + ch] = (uint16_t)m;
+                    if (!sync_b()) return false;
+                    m = max(m, (uint32_t)kmax[(half ^ 1) * KP + ch]);
                     rs = m < 0x7c00u ? fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) *
                                                   fabsf(r.key_scale) * fmaxf(1.f, pw[nv]))
                                      : 1.f;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int jb = 0; jb < 4; ++jb) {
                     uint32_t part[3][8];
-#pragma unroll
-                    for (int j4 = 0; j4 < 8; j4 += 2) {
-                        const int j0 = jb * 16 + j4 * 2;
-                        const float4 w = *reinterpret_cast<const float4*>(kw + half * 64 + j0);
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int t = half * 64 + j0 + 2 * e;
-                            float2 f = unpack<F16>(F16 ? raw[jb * 8 + j4 + e] : keys2(j0 + 2 * e));
-                            // a select, not a product: what lies behind the end may be inf or NaN
-                            f.x = t < nv ? f.x * (e ? w.z : w.x) : 0.f;
-                            f.y = t + 1 < nv ? f.y * (e ? w.w : w.y) : 0.f;
-                            if constexpr (F16) {
-                                f.x *= rs;
-                                f.y *= rs;
-                            }
-#pragma unroll
-                            for (int q = 0; q < L::Parts; ++q) {
-                                part[q][j4 + e] = pack<F16>(f.x, f.y);
-                                const float2 back = unpack<F16>(part[q][j4 + e]);
-                                f.x -= back.x;
-                                f.y -= back.y;
-                            }
-                        }
-                    }
-                    const uint32_t at = tbase + row + L::Kt + half * 32 + jb * 8;
+                    weighted(jb * 16, part, L::Parts);
                     if constexpr (L::Stacked) {
                         if (second)
-                            tmem_st8(at, part[1]);
+                            tmem_st8(t_kt + jb * 8, part[1]);
                         else
-                            tmem_st8(at, part[0]);
-                        if (L::KtCols == 128 && !second) tmem_st8(at + 64, part[2]);
-                    } else if constexpr (L::Late) {
-                        tmem_st8(at, part[1]);
-                        tmem_st8(at + 64, part[2]);
-#pragma unroll
-                        for (int j2 = 0; j2 < 8; ++j2) late[jb * 8 + j2] = part[0][j2];
+                            tmem_st8(t_kt + jb * 8, part[0]);
+                        if (L::KtCols == 128 && !second) tmem_st8(t_kt + 64 + jb * 8, part[2]);
                     } else {
-                        tmem_st8(at, part[0]);
-                        tmem_st8(at + 64, part[1]);
+#pragma unroll
+                        for (int q = 0; q < L::KtCols / 64; ++q) tmem_st8(t_kt + q * 64 + jb * 8, part[q + (L::Late ? 1 : 0)]);
                     }
                 }
             }
@@ -905,16 +939,25 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, EXACT>::Threads, 1) la_ker
             arrive(kt_ready);
             if constexpr (L::Late) {
                 if (more) {
-                    ok = wait(bar_kt, c);
-                    if (!ok) break;
+                    if (!wait(bar_kt, c)) return false;
                     tc_fence_after();
-                    tmem_st16(tbase + row + L::Kt + half * 32, late);
-                    tmem_st16(tbase + row + L::Kt + half * 32 + 16, late + 16);
+#pragma unroll 1
+                    for (int jb = 0; jb < 4; ++jb) {
+                        uint32_t part[3][8];
+                        weighted(jb * 16, part, 1);
+                        tmem_st8(t_kt + jb * 8, part[0]);
+                    }
                     tc_wait_st();
                     tc_fence_before();
                     arrive(late_ready);
                 }
             }
+            return true;
+        };
+        bool ok = true;
+        for (int c = 0; c < nch && ok; ++c) {
+            ok = kAhead ? weigh_keys(c) && carry_on(c) : carry_on(c) && weigh_keys(c);
+            rs_done = rs;
         }
         if (ok && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
             float* dst = (STATE_ONLY ? r.seg + at_seg : r.fin + at_seq) + (int64_t)ch * r.vd;
@@ -1131,7 +1174,7 @@ int sm_count() {
 
 template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
 cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
-    using L = Layout<KP, VP, F16, EXACT>;
+    using L = Layout<KP, VP, F16, STATE_ONLY, EXACT>;
     static std::atomic<uint64_t> ready{0};                    // devices whose kernel has its shared memory size
     auto* kern = la_kernel<KP, VP, F16, STATE_ONLY, EXACT>;
     int dev = 0;
