@@ -36,7 +36,8 @@ using namespace tc;
 
 constexpr int kChunk = 128;                   // tokens of a chunk: the rows of one MMA
 constexpr int kStateWarps = 8;
-constexpr uint32_t kWaitLimit = 1u << 20;
+constexpr uint32_t kWaitLimit = 1u << 16;      // polls of at most kPollNs: a wait gives up after about a second
+constexpr uint32_t kPollNs = 20000;
 constexpr int kMaxRoles = 3;
 
 __device__ int g_status;                      // FFTCONV_ERR_TIMEOUT once a wait gave up
@@ -230,17 +231,22 @@ __device__ __forceinline__ float fp16_scale(float amax) {
     return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    return ok != 0;
+// Wait for the phase with the given parity, suspended rather than polling;
+// false once *abort is set or the limit is reached.
+__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(kPollNs)
+            : "memory");
+        if (ok) return true;
+        if (ld_shared_volatile(abort)) return false;
+    }
+    return false;
 }
 
 // Parts of the weighted keys and how they lie in TMEM: EXACT where the state
@@ -261,21 +267,22 @@ struct Layout {
     // groups of row warps, which take chunks in turn, each with a score tile
     static constexpr int Groups = VP == 64 ? 2 : 1;
     static constexpr int RowWarps = 4 * Groups;
-    static constexpr int LoadWarp = RowWarps + kStateWarps, MmaWarp = LoadWarp + 1, StateMmaWarp = LoadWarp + 2;
-    static constexpr int Threads = (RowWarps + kStateWarps + 3) * 32;
+    static constexpr int LoadWarp = RowWarps + kStateWarps, MmaWarp = LoadWarp + 1, StateMmaWarp = LoadWarp + 2,
+                         ScoreWarp = LoadWarp + 3;
+    static constexpr int Threads = (RowWarps + kStateWarps + 4) * 32;
     static constexpr int XBytes = KP * kChunk * 2, ZBytes = VP * kChunk * 2;
     static constexpr int OffY = STATE_ONLY ? 0 : XBytes, OffZ = OffY + XBytes, StageBytes = OffZ + ZBytes;
     static constexpr int CarryBytes = STATE_ONLY && !Stacked ? 0 : 128 * VP * 2;
     static constexpr int Stages = StageBytes <= 49152 ? 4 : StageBytes <= 65536 ? 3 : 2;
     static constexpr int OffCarry = Stages * StageBytes;
-    static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d|, d = j - i in [-127, 127]
-    static constexpr int OffCol = OffTab + 256 * 4;           // column weights of an unmasked block of P
+    static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d| or 0, d = j - i in [-32, 31]
+    static constexpr int OffCol = OffTab + 64 * 4;            // column weights of an unmasked block of P
     static constexpr int OffPow = OffCol + 32 * 4;            // g^e, e <= 128
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, TMEM base, scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int OffMax = OffBar + 28 * 8;            // (fp16) channel maxima of each half's tokens
-    static constexpr int Bytes = OffMax + (F16 ? KtBufs * 2 * KP * 2 : 0);
+    static constexpr int OffMax = OffBar + 28 * 8;            // (fp16) channel maxima of each warp's tokens
+    static constexpr int Bytes = OffMax + (F16 ? KtBufs * kStateWarps * KP : 0);
     // TMEM columns
     static constexpr int S = 0, O = S + Groups * 128, C = STATE_ONLY ? 0 : O + VP, Kt = C + VP;
     static_assert(Bytes <= 232448, "shared memory");
@@ -286,9 +293,9 @@ struct Layout {
 // that take chunks in turn) own the token rows: P and the output, which
 // leaves through the query tile's shared memory.  Eight state warps keep the
 // state in registers (its decay, its 16-bit copy for the next product) and
-// weigh the keys, transposed into TMEM.  One warp issues the loads, one the
-// MMAs of the rows (scores, carry product, P z), one those of the chunk's own
-// state.  Only the carry product waits for the state, so chunks overlap.
+// weigh the keys, transposed into TMEM.  One warp issues the loads, three the
+// MMAs (scores; carry product and P z; the chunk's own state), so that none
+// waits behind another's operands.  Only the carry product waits for the state, so chunks overlap.
 //
 // Rounding: P and the carry's copy are rounded once to the 16-bit type (their
 // products are the two halves of the output, each with the error of one
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     uint64_t* z_ready = bars + 23;                            // rows behind a packed sequence zeroed
     uint64_t* wgb_bar = bars + 24;
     uint64_t* c_free = bars + 25;                             // the chunk's own state read
-    uint64_t* bar_fin = bars + 26;                            // both MMA warps
+    uint64_t* bar_fin = bars + 26;                            // all MMA warps
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -359,7 +366,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         mbar_init(bar_st, 1);
         mbar_init(bar_kt, 1);
         for (int i = 20; i < 26; ++i) mbar_init(bars + i, kStateWarps);
-        mbar_init(bar_fin, STATE_ONLY ? 1 : 2);
+        mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
         *abort_flag = 0;
         fence_barrier_init();
     } else if (warp == L::MmaWarp) {
@@ -371,9 +378,11 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         const float w = decay_power(ld, (float)i);
         pw[i] = w;
         if (i == 127) pw[128] = decay_power(ld, 128.f);
-        tab[127 + (rev ? i : -i)] = r.a_in * w;
-        if (i) tab[127 - (rev ? i : -i)] = 0.f;
-        if (i < 32) colw[rev ? i : 31 - i] = r.a_in * w;
+        if (i < 32) {
+            tab[32 + (rev ? i : -i)] = r.a_in * w;
+            if (i) tab[32 - (rev ? i : -i)] = 0.f;
+            colw[rev ? i : 31 - i] = r.a_in * w;
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     const bool want_fin = STATE_ONLY || (count == 1 && r.fin != nullptr);
 
     auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
-        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, phase & 1, abort_flag, kWaitLimit));
+        return __all_sync(0xffffffffu, wait_phase(bar, phase & 1, abort_flag));
     };
     auto fail = [&]() {
         *abort_flag = 1;
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             for (int c = 0; c < nch; ++c) {
                 const int st = c % L::Stages;
                 if (c >= L::Stages &&
-                    !mbar_wait_bounded(&empty[st], ((c / L::Stages) - 1) & 1, abort_flag, kWaitLimit)) {
+                    !wait_phase(&empty[st], ((c / L::Stages) - 1) & 1, abort_flag)) {
                     fail();
                     break;
                 }
@@ -445,43 +454,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     } else if (warp == L::MmaWarp) {
         // ------------------------------------------- MMAs of the rows ---
         if constexpr (!STATE_ONLY) {
-            const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
             const uint32_t id_z = idesc_f16_f32(128, VP) | kFmt | kTransB;
-            const uint32_t sb = smem_u32(smem);
+            const uint32_t sb = smem_u32(smem), t_o = tbase + L::O;
             const uint64_t d_carry = make_desc(sb + L::OffCarry, 128 * 128, 1024, 2);
             bool ok = true;
-            int scored = 0;                                   // chunks whose score product is out
-            // scores of chunk `scored`; the score tile's last P is used up
-            auto score = [&]() {
-                const uint32_t base = sb + scored % L::Stages * L::StageBytes;
-                const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::OffY, 16, 1024, 2);
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < KP / 16; ++k) {
-                    const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-                    mma_ss_warp(tbase + L::S + scored % NA * 128, d_x + step, d_y + step, id_s, k > 0);
-                }
-                tc_commit_warp(&bar_s[scored % NA]);
-                ++scored;
-            };
-            // wait for `bar`, and send out the next chunk's scores meanwhile
-            // where a second score tile is free and the loads are there
-            auto wait_busy = [&](uint64_t* bar, uint32_t phase, int c) -> bool {
-                if constexpr (NA == 2) {
-                    for (uint32_t i = 0; scored == c + 1 && scored < nch && i < kWaitLimit; ++i) {
-                        if (__all_sync(0xffffffffu, mbar_test_wait(&full[scored % L::Stages], scored / L::Stages & 1) &&
-                                                        (scored < 2 || mbar_test_wait(&bar_pv[scored % 2],
-                                                                                      scored / 2 - 1 & 1)))) {
-                            score();
-                            break;
-                        }
-                        if (__all_sync(0xffffffffu, mbar_test_wait(bar, phase & 1))) return true;
-                        __nanosleep(40);
-                        if ((i & 31) == 31 && __any_sync(0xffffffffu, ld_shared_volatile(abort_flag))) return false;
-                    }
-                }
-                return wait(bar, phase);
-            };
             for (int c = 0; c < nch; ++c) {
                 const int st = c % L::Stages, ga = c % NA;
                 const int ks = (chunk_n(c) + 15) / 16;
@@ -489,14 +465,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 const uint32_t base = sb + st * L::StageBytes;
                 const uint64_t d_x = make_desc(base, 16, 1024, 2);
                 const uint64_t d_z = make_desc(base + L::OffZ, 16384, 1024, 2);
-                const uint32_t t_o = tbase + L::O;
-                if (scored == c) {
-                    ok = wait(&full[st], c / L::Stages) && (c < NA || wait(&bar_pv[ga], c / NA - 1));
-                    if (!ok) break;
-                    score();
-                }
-                ok = wait_busy(carry_ready, c, c);
-                if (ok && c > 0) ok = wait(&o_free[(c - 1) % NA], (c - 1) / NA);
+                ok = wait(&full[st], c / L::Stages) && wait(carry_ready, c) &&
+                     (c == 0 || wait(&o_free[(c - 1) % NA], (c - 1) / NA));
                 if (!ok) break;
                 tc_fence_after();
                 if (carry) {
@@ -509,13 +479,37 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     }
                 }
                 tc_commit_warp(&bar_o[ga]);
-                ok = wait_busy(&p_ready[ga], c / NA, c);
+                ok = wait(&p_ready[ga], c / NA);
                 if (ok && p.cu && chunk_n(c) < kChunk) ok = wait(z_ready, 0);
                 if (!ok) break;
                 tc_fence_after();
                 token_mma(t_o, tbase + L::S + ga * 128, d_z, id_z, ks, carry ? 1u : 0u);
                 tc_commit_warp(&bar_pv[ga]);
                 tc_commit_warp(&empty[st]);
+            }
+            if (!ok) fail();
+            tc_commit_warp(bar_fin);
+        }
+    } else if (warp == L::ScoreWarp) {
+        // ----------------------------------------- MMAs of the scores ---
+        if constexpr (!STATE_ONLY) {
+            const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
+            const uint32_t sb = smem_u32(smem);
+            bool ok = true;
+            for (int c = 0; c < nch; ++c) {
+                const int st = c % L::Stages, ga = c % NA;
+                const uint32_t base = sb + st * L::StageBytes;
+                const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::OffY, 16, 1024, 2);
+                // the loads are there, and the score tile's last P is used up
+                ok = wait(&full[st], c / L::Stages) && (c < NA || wait(&bar_pv[ga], c / NA - 1));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < KP / 16; ++k) {
+                    const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                    mma_ss_warp(tbase + L::S + ga * 128, d_x + step, d_y + step, id_s, k > 0);
+                }
+                tc_commit_warp(&bar_s[ga]);
             }
             if (!ok) fail();
             tc_commit_warp(bar_fin);
@@ -554,7 +548,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         }
         if (!ok) fail();
         tc_commit_warp(bar_fin);
-        // no MMA of either warp is in flight when TMEM is freed (also after a failed wait)
+        // no MMA of any warp is in flight when TMEM is freed (also after a failed wait)
         for (uint32_t i = 0; i < kWaitLimit; ++i)
             if (__all_sync(0xffffffffu, mbar_try_wait(bar_fin, 0))) break;
     } else if (warp < L::RowWarps) {
@@ -569,14 +563,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 const bool carry = c > 0 || has_init;
                 const int jlo = rev ? i : 0, jhi = rev ? nv - 1 : i;
                 const uint32_t t_o = tbase + row + L::O;
-                // columns 32 blk .. 32 blk + 31: 0 masked, 1 on the border, 2 inside
-                auto kind = [&](int blk) {
-                    if (rev ? blk < wr : blk > wr) return 0;
-                    if (blk == wr || (rev && blk * 32 + 32 > nv)) return blk * 32 < nv ? 1 : 0;
-                    return 2;
-                };
-                auto weigh = [&](uint32_t (&s)[32], int blk, int kd, float scale) {
-                    if (kd == 2) {
+                // columns 32 blk .. 32 blk + 31 have nothing for this warp's rows
+                auto masked = [&](int blk) { return (rev ? blk < wr : blk > wr) || blk * 32 >= nv; };
+                auto weigh = [&](uint32_t (&s)[32], int blk, float scale) {
+                    if (blk != wr) {
                         // g^|i-j| as (row to the block's near edge) x (edge to
                         // column): both at most 1, four columns a load
                         const float f = pw[rev ? blk * 32 - i : i - blk * 32 - 31] * scale;
@@ -587,14 +577,17 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                             scale2(s[j + 2], s[j + 3], mul2(make_float2(f, f), make_float2(w.z, w.w)));
                         }
                     } else {
-                        const float* w = tab + 127 + blk * 32 - i;
+                        // on the diagonal: the table is zero beyond it
+                        const float* w = tab + 32 - lane;
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int col = blk * 32 + j;
-                            float x = __uint_as_float(s[j]) * w[j];
-                            if constexpr (F16) x *= scale;
-                            s[j] = col >= jlo && col <= jhi ? __float_as_uint(x) : 0u;
-                        }
+                        for (int j = 0; j < 32; j += 2)
+                            scale2(s[j], s[j + 1], F16 ? mul2(make_float2(w[j], w[j + 1]), make_float2(scale, scale))
+                                                       : make_float2(w[j], w[j + 1]));
+                    }
+                    if (nv < kChunk) {
+                        // columns behind the end may be another sequence's inf or NaN
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = blk * 32 + j >= jlo && blk * 32 + j <= jhi ? s[j] : 0u;
                     }
                 };
                 if (!wait(&bar_s[ga], c / NA)) { fail(); break; }
@@ -604,29 +597,35 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     float amax = 0.f;
 #pragma unroll 1
                     for (int blk = 0; blk < 4; ++blk) {
-                        const int kd = kind(blk);
-                        if (kd == 0) continue;
+                        if (masked(blk)) continue;
                         uint32_t s[32];
                         tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
-                        weigh(s, blk, kd, 1.f);
+                        // (the weights are at most a; a score far above the
+                        // weighted ones costs nothing within 2^28)
+                        if (nv == kChunk) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
+                            for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (blk * 32 + j >= jlo && blk * 32 + j <= jhi)
+                                    amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
+                        }
                     }
-                    scale = fp16_scale(amax);
+                    scale = fp16_scale(amax * fmaxf(fabsf(r.a_in), fabsf(r.a_in) * pw[127]));
                 }
 #pragma unroll 1
                 for (int blk = 0; blk < 4; ++blk) {
-                    const int kd = kind(blk);
                     uint32_t pk[16];
-                    if (kd == 0) {
+                    if (masked(blk)) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) pk[j] = 0u;
                     } else {
                         uint32_t s[32];
                         tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
-                        weigh(s, blk, kd, scale);
+                        weigh(s, blk, scale);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             pk[j] = pack<F16>(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
@@ -738,13 +737,14 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     } else {
         // -------------------------------------------------- state rows ---
         // Two warps share 32 rows of the MMA: each keeps half of the columns
-        // and weighs half of the tokens.  64 channels: rows 0-63 carry the
-        // sums of the first (and third) part, rows 64-127 of the second.
+        // and weighs half of the tokens.  64 channels: one half of the rows
+        // carries the sums of the first (and third) part, the other, on the
+        // schedulers whose row warps have fewer columns, of the second.
         constexpr int kCols = VP / 2;
         const int ts = tid - L::RowWarps * 32, sw = warp - L::RowWarps, bw = sw & 3, half = sw >> 2;
         const int d = bw * 32 + lane;
         const int ch = L::Stacked ? d & 63 : d;               // key channel
-        const bool second = L::Stacked && bw >= 2;            // (warp-uniform)
+        const bool second = L::Stacked && bw >= 2 == rev;     // (warp-uniform)
         const int col0 = half * kCols;
         const uint32_t row = (uint32_t)(bw * 32) << 16;
         const int64_t mat = (int64_t)r.kd * r.vd;
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         // (fp16) powers of two on this channel's weighted keys: the chunk's at
         // hand, and the one's whose own state is read next
         float rs = 1.f, rs_done = 1.f;
-        uint16_t* kmax_sh = reinterpret_cast<uint16_t*>(smem + L::OffMax);
+        uint8_t* kmax_sh = smem + L::OffMax;
         uint32_t sync_phase = 0;
         auto sync_b = [&]() -> bool {                         // bounded barrier of the state warps
             arrive(wgb_bar);
@@ -767,7 +767,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 #pragma unroll
         for (int j = 0; j < kCols; ++j) state[j] = has_init && nch > 0 ? initial(col0 + j) : 0.f;
         if (L::Stacked && L::KtCols == 128 && second) {
-            // the third part's rows 64-127 stay zero
+            // the third part has no second half
             const uint32_t zero[16] = {};
             for (int buf = 0; buf < L::KtBufs; ++buf) {
                 tmem_st16(tbase + row + L::Kt + buf * L::KtCols + 64 + half * 32, zero);
@@ -868,67 +868,103 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             // one channel of 64 tokens a thread, transposed into TMEM
             const uint8_t* kcol = base + L::OffY + (ch >> 6) * 16384 + (ch & 7) * 2 + half * 64 * 128;
             const int cb = (ch & 63) >> 3;
-            auto keys2 = [&](int j) -> uint32_t {             // tokens j and j + 1 of the half (j even)
-                const uint32_t a = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
-                const uint32_t e = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + 128 + ((cb ^ (j & 7) ^ 1) << 4));
-                return a | e << 16;
+            auto keys2 = [&](int j) -> float2 {               // tokens j and j + 1 of the half (j even)
+                const uint16_t x = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
+                const uint16_t y = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + 128 + ((cb ^ (j & 7) ^ 1) << 4));
+                if constexpr (F16) return make_float2(__half2float(__ushort_as_half(x)), __half2float(__ushort_as_half(y)));
+                return make_float2(__uint_as_float((uint32_t)x << 16), __uint_as_float((uint32_t)y << 16));
             };
-            // the parts of the weighted keys of tokens j0 .. j0 + 15 of the half
-            auto weighted = [&](int j0, uint32_t (&part)[3][8], int parts) {
+            // the first PARTS parts of the weighted keys of tokens j0 .. j0 + 15 of the half
+            auto weighted = [&](int j0, uint32_t (&part)[3][8], auto parts) {
+                constexpr int PARTS = decltype(parts)::value;
 #pragma unroll
                 for (int j4 = 0; j4 < 8; j4 += 2) {
                     const float4 w = *reinterpret_cast<const float4*>(kw + half * 64 + j0 + j4 * 2);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int t = half * 64 + j0 + (j4 + e) * 2;
-                        float2 f = mul2(unpack<F16>(keys2(j0 + (j4 + e) * 2)),
-                                        e ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
-                        if (nv < kChunk) {
-                            // a select, not a product: what lies behind the end may be inf or NaN
-                            if (t >= nv) f.x = 0.f;
-                            if (t + 1 >= nv) f.y = 0.f;
-                        }
+                        float2 f = mul2(keys2(j0 + (j4 + e) * 2), e ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
                         if constexpr (F16) f = mul2(f, make_float2(rs, rs));
 #pragma unroll
-                        for (int q = 0; q < 3; ++q) {
-                            if (q >= parts) break;
+                        for (int q = 0; q < PARTS; ++q) {
                             part[q][j4 + e] = pack<F16>(f.x, f.y);
-                            if (q + 1 < parts) f = fma2(unpack<F16>(part[q][j4 + e]), make_float2(-1.f, -1.f), f);
+                            if (q + 1 < PARTS) f = fma2(unpack<F16>(part[q][j4 + e]), make_float2(-1.f, -1.f), f);
                         }
                     }
                 }
+                if (nv < kChunk) {
+                    // a select, not the weight 0: what lies behind the end may be inf or NaN
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int left = nv - (half * 64 + j0 + 2 * j);
+                        const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+#pragma unroll
+                        for (int q = 0; q < PARTS; ++q) part[q][j] &= keep;
+                    }
+                }
             };
+            using One = std::integral_constant<int, 1>;
+            using Two = std::integral_constant<int, 2>;
+            using All = std::integral_constant<int, L::Parts>;
             const uint32_t t_kt = tbase + row + L::Kt + c % L::KtBufs * L::KtCols + half * 32;
             if (more) {
                 if constexpr (F16) {
-                    // scale the channel so that its largest weighted key is just below 2^15
-                    uint32_t m = 0;                           // magnitudes order like integers
-#pragma unroll 4
-                    for (int j = 0; j < 64; j += 2) {
-                        const uint32_t x = keys2(j);
-                        m = half * 64 + j < nv ? max(m, x & 0x7fffu) : m;
-                        m = half * 64 + j + 1 < nv ? max(m, x >> 16 & 0x7fffu) : m;
+                    // Scale each channel so that its largest weighted key is
+                    // below 2^15, by the exponents of the maxima: a warp takes
+                    // 16 tokens, eight channels a lane at a time.
+                    constexpr int kVecs = KP / 8, kRows = 32 / kVecs;
+                    const int v8 = lane % kVecs;
+                    __half2 m[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.f);
+#pragma unroll
+                    for (int q = 0; q < 16 / kRows; ++q) {
+                        const int j = sw * 16 + q * kRows + lane / kVecs;
+                        if (j < nv) {
+                            const uint4 x = *reinterpret_cast<const uint4*>(base + L::OffY + (v8 >> 3) * 16384 + j * 128 +
+                                                                            (((v8 & 7) ^ (j & 7)) << 4));
+                            const __half2* y = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) m[e] = __hmax2(m[e], __habs2(y[e]));
+                        }
+                    }
+                    uint32_t lo = 0, hi = 0;                  // eight exponents
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                        for (int x = kVecs; x < 32; x *= 2) m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], x));
+                        const uint32_t y = *reinterpret_cast<const uint32_t*>(&m[e]);
+                        const uint32_t two = (y >> 10 & 31u) | (y >> 26 & 31u) << 8;
+                        (e < 2 ? lo : hi) |= two << (e & 1) * 16;
                     }
                     // (the place's last maxima are read: every warp has passed a later barrier)
-                    uint16_t* kmax = kmax_sh + c % L::KtBufs * 2 * KP;
-                    if (!second) kmax[half * KP + ch] = (uint16_t)m;
+                    uint8_t* kmax = kmax_sh + c % L::KtBufs * kStateWarps * KP;
+                    if (lane < kVecs) *reinterpret_cast<uint2*>(kmax + sw * KP + v8 * 8) = make_uint2(lo, hi);
                     if (!sync_b()) return false;
-                    m = max(m, (uint32_t)kmax[(half ^ 1) * KP + ch]);
-                    rs = m < 0x7c00u ? fp16_scale(__half2float(__ushort_as_half((unsigned short)m)) *
-                                                  fabsf(r.key_scale) * fmaxf(1.f, pw[nv]))
-                                     : 1.f;
+                    int top = 0;
+#pragma unroll
+                    for (int w = 0; w < kStateWarps; ++w) top = max(top, (int)kmax[w * KP + ch]);
+                    // keys below 2^(top - 14) (a channel of zeros and subnormals: below 2^-14)
+                    rs = top < 31 ? fp16_scale(__uint_as_float((uint32_t)(max(top, 1) - 15 + 127) << 23) *
+                                               fabsf(r.key_scale) * fmaxf(1.f, pw[nv])) * 0.5f
+                                  : 1.f;
                 }
 #pragma unroll 1
                 for (int jb = 0; jb < 4; ++jb) {
                     uint32_t part[3][8];
-                    weighted(jb * 16, part, L::Parts);
                     if constexpr (L::Stacked) {
-                        if (second)
+                        if (second) {
+                            weighted(jb * 16, part, Two{});
                             tmem_st8(t_kt + jb * 8, part[1]);
-                        else
+                        } else if constexpr (L::KtCols == 128) {
+                            weighted(jb * 16, part, All{});
                             tmem_st8(t_kt + jb * 8, part[0]);
-                        if (L::KtCols == 128 && !second) tmem_st8(t_kt + 64 + jb * 8, part[2]);
+                            tmem_st8(t_kt + 64 + jb * 8, part[2]);
+                        } else {
+                            weighted(jb * 16, part, One{});
+                            tmem_st8(t_kt + jb * 8, part[0]);
+                        }
                     } else {
+                        weighted(jb * 16, part, All{});
 #pragma unroll
                         for (int q = 0; q < L::KtCols / 64; ++q) tmem_st8(t_kt + q * 64 + jb * 8, part[q + (L::Late ? 1 : 0)]);
                     }
@@ -944,7 +980,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 #pragma unroll 1
                     for (int jb = 0; jb < 4; ++jb) {
                         uint32_t part[3][8];
-                        weighted(jb * 16, part, 1);
+                        weighted(jb * 16, part, One{});
                         tmem_st8(t_kt + jb * 8, part[0]);
                     }
                     tc_wait_st();
@@ -967,7 +1003,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) state[j] = initial(col0 + j);
             if constexpr (L::Stacked) {
-                // rows 64-127 hand their half of the sum over, in the carry copy's place
+                // the second half of the rows hands its part of the sum over, in the carry copy's place
                 if (ok && !STATE_ONLY && nch > 0) ok = wait(&bar_o[(nch - 1) % NA], (nch - 1) / NA);
                 float* sum = reinterpret_cast<float*>(smem + L::OffCarry);      // [VP][64]
                 if (ok && second)
