@@ -167,6 +167,23 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // until the issuing thread's stores have read their shared memory
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
+// Four 8 x 8 tiles of 16-bit values, each transposed: a lane gives the address
+// of row lane % 8 of tile lane / 8 and receives column lane / 4, rows
+// 2 (lane % 4) and + 1, of every tile.
+__device__ __forceinline__ void ldmatrix4_trans(const void* row, uint32_t* r) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(row))
+                 : "memory");
+}
+// 16 TMEM lanes x 16 columns: register 2 i + x holds lane 8 x + laneid / 4,
+// column 4 i + laneid % 4.
+__device__ __forceinline__ void tmem_st_16x16(uint32_t a, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
 // 16-bit arithmetic of the two types: packing with round to nearest even, and
 // the two halves as fp32.
 template <bool F16>
@@ -258,12 +275,14 @@ struct Layout {
     // state is kept as the two rows' sum; 128 channels: one MMA a part
     static constexpr bool Stacked = KP == 64;
     static constexpr int Parts = F16 || !EXACT ? 2 : 3;
-    // beside P and the output three parts of 128 channels do not fit: the last
-    // one waits for the first one's columns
-    static constexpr bool Late = !STATE_ONLY && !Stacked && Parts == 3;
-    static constexpr int KtCols = Stacked ? (Parts == 3 ? 128 : 64) : Late ? 128 : Parts * 64;
+    // beside P and the output three parts do not fit: the first one waits for
+    // the others' columns
+    static constexpr bool Late = !STATE_ONLY && Parts == 3;
+    static constexpr int KtCols = Stacked ? (Parts == 3 && !Late ? 128 : 64) : Late ? 128 : Parts * 64;
     // where the columns suffice, a chunk's keys are weighed while the last one's are multiplied
-    static constexpr int KtBufs = STATE_ONLY || KtCols == 64 ? 2 : 1;
+    static constexpr int KtBufs = STATE_ONLY || (KP == 64 && VP == 128 && !Late) ? 2 : 1;
+    // the carry product has columns of its own (else P z is added to it, once it is weighted)
+    static constexpr bool SplitOut = KP == 64 && VP == 64;
     // groups of row warps, which take chunks in turn, each with a score tile
     static constexpr int Groups = VP == 64 ? 2 : 1;
     static constexpr int RowWarps = 4 * Groups;
@@ -284,7 +303,8 @@ struct Layout {
     static constexpr int OffMax = OffBar + 28 * 8;            // (fp16) channel maxima of each warp's tokens
     static constexpr int Bytes = OffMax + (F16 ? KtBufs * kStateWarps * KP : 0);
     // TMEM columns
-    static constexpr int S = 0, O = S + Groups * 128, C = STATE_ONLY ? 0 : O + VP, Kt = C + VP;
+    static constexpr int S = 0, O = S + Groups * 128, Oc = SplitOut ? O + VP : O, C = STATE_ONLY ? 0 : Oc + VP,
+                         Kt = C + VP;
     static_assert(Bytes <= 232448, "shared memory");
     static_assert(Kt + KtBufs * KtCols <= 512, "TMEM columns");
 };
@@ -307,7 +327,7 @@ template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
 __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Threads, 1)
     la_kernel(const __grid_constant__ Params p) {
     using L = Layout<KP, VP, F16, STATE_ONLY, EXACT>;
-    constexpr bool kAhead = L::KtBufs == 2;                   // keys weighed one chunk ahead
+    constexpr bool kAhead = L::KtBufs == 2;                   // keys weighed one chunk ahead (never Late)
     constexpr int NA = L::Groups;
     extern __shared__ __align__(1024) uint8_t smem[];
     float* tab = reinterpret_cast<float*>(smem + L::OffTab);
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         // ------------------------------------------- MMAs of the rows ---
         if constexpr (!STATE_ONLY) {
             const uint32_t id_z = idesc_f16_f32(128, VP) | kFmt | kTransB;
-            const uint32_t sb = smem_u32(smem), t_o = tbase + L::O;
+            const uint32_t sb = smem_u32(smem), t_o = tbase + L::O, t_oc = tbase + L::Oc;
             const uint64_t d_carry = make_desc(sb + L::OffCarry, 128 * 128, 1024, 2);
             bool ok = true;
             for (int c = 0; c < nch; ++c) {
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     for (int k = 0; k < 8; ++k) {
                         const int kx = k % (KP / 16);
                         const uint64_t step = (uint64_t)((kx >> 2) * 16384 + (kx & 3) * 32) >> 4;
-                        mma_ss_warp(t_o, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
+                        mma_ss_warp(t_oc, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
                     }
                 }
                 tc_commit_warp(&bar_o[ga]);
@@ -483,7 +503,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 if (ok && p.cu && chunk_n(c) < kChunk) ok = wait(z_ready, 0);
                 if (!ok) break;
                 tc_fence_after();
-                token_mma(t_o, tbase + L::S + ga * 128, d_z, id_z, ks, carry ? 1u : 0u);
+                token_mma(t_o, tbase + L::S + ga * 128, d_z, id_z, ks, carry && !L::SplitOut ? 1u : 0u);
                 tc_commit_warp(&bar_pv[ga]);
                 tc_commit_warp(&empty[st]);
             }
@@ -558,6 +578,16 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             const int i = wr * 32 + lane;
             const uint32_t row = (uint32_t)(wr * 32) << 16;
             const uint32_t t_s = tbase + row + L::S + ga * 128;
+            // a chunk's stage may be loaded again once its output's stores have
+            // read it; with four stages that can wait until the next chunk's turn
+            constexpr bool kDefer = L::Stages == 4;
+            auto release = [&](int c) {
+                if (lane == 0) {
+                    bulk_wait_read();
+                    mbar_arrive(&empty[c % L::Stages]);
+                }
+                __syncwarp();
+            };
             for (int c = ga; c < nch; c += NA) {
                 const int nv = chunk_n(c);
                 const bool carry = c > 0 || has_init;
@@ -592,6 +622,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 };
                 if (!wait(&bar_s[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
+                if (kDefer && c >= NA) release(c - NA);
                 float scale = 1.f;
                 if constexpr (F16) {
                     float amax = 0.f;
@@ -633,12 +664,20 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     // P (16 bit) lies over score columns that this thread has read
                     tmem_st16(t_s + blk * 16, pk);
                 }
+                const float inv = F16 ? 1.f / scale : 1.f;
+                float f = r.a_carry * pw[min(128, max(0, rev ? nv - 1 - i : i + 1))];
+                if constexpr (L::SplitOut) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    arrive(&p_ready[ga]);
+                }
                 if (!wait(&bar_o[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
-                if (carry) {
-                    const int e = min(128, max(0, rev ? nv - 1 - i : i + 1));
-                    float f = r.a_carry * pw[e];
-                    if constexpr (F16) f *= carry_inv[c & 3] * scale;
+                if constexpr (F16) {
+                    if (carry) f *= carry_inv[c & 3];
+                }
+                if (carry && !L::SplitOut) {
+                    f *= scale;
 #pragma unroll 1
                     for (int blk = 0; blk < VP / 32; ++blk) {
                         uint32_t s[32];
@@ -649,12 +688,13 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                         tmem_st32(t_o + blk * 32, s);
                     }
                 }
-                tc_wait_st();
-                tc_fence_before();
-                arrive(&p_ready[ga]);
+                if constexpr (!L::SplitOut) {
+                    tc_wait_st();
+                    tc_fence_before();
+                    arrive(&p_ready[ga]);
+                }
                 if (!wait(&bar_pv[ga], c / NA)) { fail(); break; }
                 tc_fence_after();
-                const float inv = F16 ? 1.f / scale : 1.f;
                 const int st = c % L::Stages, t = t0 + chunk_at(c);
                 // Through the query tile, which no MMA reads any more: each
                 // warp stages its 32 rows in 4 KB pieces (rows of 128 bytes,
@@ -684,14 +724,34 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 for (int blk = 0; blk < VP / 32; ++blk) {
                     uint32_t s[32];
                     tmem_ld32(t_o + blk * 32, s);
-                    tc_wait_ld();
+                    if constexpr (L::SplitOut) {
+                        uint32_t x[32];
+                        if (carry) tmem_ld32(t_o + VP + blk * 32, x);
+                        tc_wait_ld();
+                        if constexpr (F16) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) scale2(s[j], s[j + 1], make_float2(inv, inv));
+                        }
+                        if (carry) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) {
+                                const float2 y = fma2(make_float2(__uint_as_float(x[j]), __uint_as_float(x[j + 1])),
+                                                      make_float2(f, f),
+                                                      make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+                                s[j] = __float_as_uint(y.x);
+                                s[j + 1] = __float_as_uint(y.y);
+                            }
+                        }
+                    } else {
+                        tc_wait_ld();
+                        if constexpr (F16) {
+#pragma unroll
+                            for (int j = 0; j < 32; j += 2) scale2(s[j], s[j + 1], make_float2(inv, inv));
+                        }
+                    }
                     if (blk == VP / 32 - 1) {
                         tc_fence_before();
                         arrive(&o_free[ga]);
-                    }
-                    if constexpr (F16) {
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) scale2(s[j], s[j + 1], make_float2(inv, inv));
                     }
                     if (direct) {
                         const int64_t at = (int64_t)b * r.out_b + (int64_t)(t + i) * r.out_t + (int64_t)h * r.out_h;
@@ -726,11 +786,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                         if (blk & 1) send(blk * 32 - 32);
                     }
                 }
-                if (lane == 0) {
-                    bulk_wait_read();                         // (the stage may be loaded again)
-                    mbar_arrive(&empty[st]);
-                }
-                __syncwarp();
+                if (!kDefer) release(c);
             }
             if (lane == 0) bulk_wait_read();                  // (also after a failed wait)
         }
@@ -865,40 +921,52 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 fence_proxy_async_smem();
                 arrive(z_ready);
             }
-            // one channel of 64 tokens a thread, transposed into TMEM
-            const uint8_t* kcol = base + L::OffY + (ch >> 6) * 16384 + (ch & 7) * 2 + half * 64 * 128;
-            const int cb = (ch & 63) >> 3;
-            auto keys2 = [&](int j) -> float2 {               // tokens j and j + 1 of the half (j even)
-                const uint16_t x = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + ((cb ^ (j & 7)) << 4));
-                const uint16_t y = *reinterpret_cast<const uint16_t*>(kcol + j * 128 + 128 + ((cb ^ (j & 7) ^ 1) << 4));
-                if constexpr (F16) return make_float2(__half2float(__ushort_as_half(x)), __half2float(__ushort_as_half(y)));
-                return make_float2(__uint_as_float((uint32_t)x << 16), __uint_as_float((uint32_t)y << 16));
-            };
-            // the first PARTS parts of the weighted keys of tokens j0 .. j0 + 15 of the half
-            auto weighted = [&](int j0, uint32_t (&part)[3][8], auto parts) {
+            // Parts of the weighted keys of 32 tokens and 16 channels a time,
+            // transposed into TMEM: a lane has channels lane / 4 and + 8,
+            // tokens 8 i + 2 (lane % 4) and + 1.
+            const uint8_t* krow;
+            {
+                const int tile = lane >> 3, c8 = (L::Stacked ? bw & 1 : bw) * 4 + (tile & 1);
+                krow = base + L::OffY + (c8 >> 3) * 16384 + (half * 64 + (tile >> 1) * 8 + (lane & 7)) * 128;
+            }
+            const int c8 = (L::Stacked ? bw & 1 : bw) * 4 + (lane >> 3 & 1);
+            // the first PARTS parts of channels 16 m.., tokens 32 th.. of the half
+            auto weighted = [&](int m, int th, uint32_t (&part)[3][8], auto parts) {
                 constexpr int PARTS = decltype(parts)::value;
+                uint32_t x[8];
 #pragma unroll
-                for (int j4 = 0; j4 < 8; j4 += 2) {
-                    const float4 w = *reinterpret_cast<const float4*>(kw + half * 64 + j0 + j4 * 2);
+                for (int t = 0; t < 2; ++t)
+                    ldmatrix4_trans(krow + (2 * th + t) * 2048 + ((((c8 + 2 * m) & 7) ^ (lane & 7)) << 4), x + 4 * t);
+                float2 sc[2];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float2 f = mul2(keys2(j0 + (j4 + e) * 2), e ? make_float2(w.z, w.w) : make_float2(w.x, w.y));
-                        if constexpr (F16) f = mul2(f, make_float2(rs, rs));
+                for (int y = 0; y < 2; ++y) {
+                    const float v = F16 ? __shfl_sync(0xffffffffu, rs, m * 16 + y * 8 + (lane >> 2)) : 1.f;
+                    sc[y] = make_float2(v, v);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 w = *reinterpret_cast<const float2*>(kw + half * 64 + 32 * th + 8 * i + 2 * (lane & 3));
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float2 f = mul2(unpack<F16>(x[2 * i + y]), F16 ? mul2(w, sc[y]) : w);
 #pragma unroll
                         for (int q = 0; q < PARTS; ++q) {
-                            part[q][j4 + e] = pack<F16>(f.x, f.y);
-                            if (q + 1 < PARTS) f = fma2(unpack<F16>(part[q][j4 + e]), make_float2(-1.f, -1.f), f);
+                            part[q][2 * i + y] = pack<F16>(f.x, f.y);
+                            if (q + 1 < PARTS) f = fma2(unpack<F16>(part[q][2 * i + y]), make_float2(-1.f, -1.f), f);
                         }
                     }
                 }
                 if (nv < kChunk) {
                     // a select, not the weight 0: what lies behind the end may be inf or NaN
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int left = nv - (half * 64 + j0 + 2 * j);
+                    for (int i = 0; i < 4; ++i) {
+                        const int left = nv - (half * 64 + 32 * th + 8 * i + 2 * (lane & 3));
                         const uint32_t keep = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
 #pragma unroll
-                        for (int q = 0; q < PARTS; ++q) part[q][j] &= keep;
+                        for (int q = 0; q < PARTS; ++q) {
+                            part[q][2 * i] &= keep;
+                            part[q][2 * i + 1] &= keep;
+                        }
                     }
                 }
             };
@@ -949,24 +1017,33 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                                   : 1.f;
                 }
 #pragma unroll 1
-                for (int jb = 0; jb < 4; ++jb) {
+                for (int mt = 0; mt < 4; ++mt) {
+                    const int m = mt >> 1, th = mt & 1;
+                    const uint32_t at = t_kt + th * 16 + ((uint32_t)(m * 16) << 16);
                     uint32_t part[3][8];
-                    if constexpr (L::Stacked) {
-                        if (second) {
-                            weighted(jb * 16, part, Two{});
-                            tmem_st8(t_kt + jb * 8, part[1]);
-                        } else if constexpr (L::KtCols == 128) {
-                            weighted(jb * 16, part, All{});
-                            tmem_st8(t_kt + jb * 8, part[0]);
-                            tmem_st8(t_kt + 64 + jb * 8, part[2]);
-                        } else {
-                            weighted(jb * 16, part, One{});
-                            tmem_st8(t_kt + jb * 8, part[0]);
-                        }
-                    } else {
-                        weighted(jb * 16, part, All{});
+                    if constexpr (!L::Stacked) {
+                        weighted(m, th, part, All{});
 #pragma unroll
-                        for (int q = 0; q < L::KtCols / 64; ++q) tmem_st8(t_kt + q * 64 + jb * 8, part[q + (L::Late ? 1 : 0)]);
+                        for (int q = 0; q < L::KtCols / 64; ++q) tmem_st_16x16(at + q * 64, part[q + (L::Late ? 1 : 0)]);
+                    } else if (L::Late) {
+                        // the third part, and nothing beside it
+                        if (second) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) part[2][j] = 0u;
+                        } else {
+                            weighted(m, th, part, All{});
+                        }
+                        tmem_st_16x16(at, part[2]);
+                    } else if (second) {
+                        weighted(m, th, part, Two{});
+                        tmem_st_16x16(at, part[1]);
+                    } else if constexpr (L::KtCols == 128) {
+                        weighted(m, th, part, All{});
+                        tmem_st_16x16(at, part[0]);
+                        tmem_st_16x16(at + 64, part[2]);
+                    } else {
+                        weighted(m, th, part, One{});
+                        tmem_st_16x16(at, part[0]);
                     }
                 }
             }
@@ -978,10 +1055,17 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     if (!wait(bar_kt, c)) return false;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int jb = 0; jb < 4; ++jb) {
+                    for (int mt = 0; mt < 4; ++mt) {
+                        const int m = mt >> 1, th = mt & 1;
+                    const uint32_t at = t_kt + th * 16 + ((uint32_t)(m * 16) << 16);
                         uint32_t part[3][8];
-                        weighted(jb * 16, part, One{});
-                        tmem_st8(t_kt + jb * 8, part[0]);
+                        if (second) {
+                            weighted(m, th, part, Two{});
+                            tmem_st_16x16(at, part[1]);
+                        } else {
+                            weighted(m, th, part, One{});
+                            tmem_st_16x16(at, part[0]);
+                        }
                     }
                     tc_wait_st();
                     tc_fence_before();
