@@ -758,6 +758,8 @@ int vec_of(int dtype) { return dtype == FFTCONV_F32 ? 4 : 8; }
 size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool bwd) {
     if (N == 0 || S == 0 || C == 0) return 0;
     const int64_t chunks = chunks_of(N, S, C);
+    // (groups of up to 256 channels of one position take the token form whatever their alignment)
+    if (!bwd && S == 1 && C / G <= 256) return 0;
     if (!bwd) {
         // parts of the statistics, and mean and rstd when the caller keeps none
         return (size_t)(pad256(N * G * chunks * ((C + kThreads - 1) / kThreads) * 16) + 2 * pad256(N * G * 4));
@@ -830,7 +832,7 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
     if (overlap(y, bytes, x, ((rows - 1) * ld_x + C) * es) || overlap(y, bytes, gate, ((rows - 1) * ld_gate + C) * es))
         return fail(FFTCONV_ERR_INVALID_ARG, "y overlaps an input");
     const size_t need = workspace_bytes(N, S, C, G, false);
-    if (!workspace || workspace_size < need)
+    if (need && (!workspace || workspace_size < need))
         return fail(FFTCONV_ERR_INVALID_ARG, "workspace of " + std::to_string(workspace_size) + " bytes, " +
                                                  std::to_string(need) + " needed");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)
@@ -903,7 +905,7 @@ int fftconv_group_norm_backward(const void* x, const void* gate, const void* wei
             return fail(FFTCONV_ERR_INVALID_ARG, "a gradient overlaps an input");
     if (overlap(dx, bytes, dgate, bytes)) return fail(FFTCONV_ERR_INVALID_ARG, "dx overlaps dgate");
     const size_t need = workspace_bytes(N, S, C, G, true);
-    if (!workspace || workspace_size < need)
+    if (need && (!workspace || workspace_size < need))
         return fail(FFTCONV_ERR_INVALID_ARG, "workspace of " + std::to_string(workspace_size) + " bytes, " +
                                                  std::to_string(need) + " needed");
     if (reinterpret_cast<uintptr_t>(workspace) & 255u)

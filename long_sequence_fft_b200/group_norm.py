@@ -5,10 +5,21 @@
 """
 from __future__ import annotations
 
-from . import _check, _dtype_code, _lib, _ptr as _p
+from . import BF16, F16, F32, _check, _lib
+from . import _ptr as _p
 from .linear_attention import _on
 
 ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
+_CODES = None
+
+
+def _code(dtype):
+    """The library's code of a torch dtype; None: not one of its types."""
+    global _CODES
+    if _CODES is None:
+        import torch
+        _CODES = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
+    return _CODES.get(dtype)
 
 
 def _rows(t, C):
@@ -20,6 +31,13 @@ def _rows(t, C):
         return t.view(-1, C)
     except RuntimeError:
         return None
+
+
+def _checked_rows(t, C, name):
+    r = _rows(t, C)
+    if t.numel() and (r is None or (r.shape[0] > 1 and r.stride(0) < C) or t.data_ptr() % 16):
+        raise ValueError(f"{name} must be rows of contiguous channels, one stride apart, 16-byte aligned")
+    return t.reshape(-1, C) if r is None else r
 
 
 def _ld(r, C):
@@ -34,10 +52,10 @@ def _forward(x2, gate2, weight, bias, N, S, C, G, act, eps, out, keep, stream, s
         if keep:
             mean, rstd = torch.empty((2, N, G), dtype=torch.float32, device=x2.device).unbind(0)
         n = int(_lib.fftconv_group_norm_workspace_bytes(N, S, C, G, 0))
-        ws = torch.empty(n, dtype=torch.uint8, device=x2.device)
+        ws = torch.empty(n, dtype=torch.uint8, device=x2.device) if n else None
         _check(_lib.fftconv_group_norm(_p(x2), _p(gate2), _p(weight), _p(bias), _p(y), _p(mean), _p(rstd), N, S, C, G,
-                                       _ld(x2, C), 0 if gate2 is None else _ld(gate2, C), _dtype_code(x2.dtype),
-                                       _dtype_code(x2.dtype if weight is None else weight.dtype), act, eps, _p(ws), n,
+                                       _ld(x2, C), 0 if gate2 is None else _ld(gate2, C), _code(x2.dtype),
+                                       _code(x2.dtype if weight is None else weight.dtype), act, eps, _p(ws), n,
                                        handle))
     return y, mean, rstd
 
@@ -77,11 +95,11 @@ def _autograd_function():
                 if weight is not None and (need[2] or need[3]):
                     dw, db = torch.empty((2, C), dtype=torch.float32, device=x.device).unbind(0)
                 n = int(_lib.fftconv_group_norm_workspace_bytes(N, S, C, G, 1))
-                ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+                ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
                 _check(_lib.fftconv_group_norm_backward(
                     _p(x2), _p(gate2), _p(weight), _p(bias), _p(dy2), _p(mean), _p(rstd), _p(dx), _p(dgate), _p(dw),
                     _p(db), N, S, C, G, _ld(x2, C), 0 if gate is None else _ld(gate2, C), _ld(dy2, C),
-                    _dtype_code(x.dtype), _dtype_code(x.dtype if weight is None else weight.dtype), act, _p(ws), n,
+                    _code(x.dtype), _code(x.dtype if weight is None else weight.dtype), act, _p(ws), n,
                     handle))
             return (dx if need[0] else None, dgate if need[1] else None, dw.to(weight.dtype) if need[2] else None,
                     db.to(bias.dtype) if need[3] else None, None, None, None, None, None, None)
@@ -106,7 +124,7 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
         raise ValueError("x must have at least 2 dimensions: sample, ..., channel")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dtype not in (torch.float32, torch.float16, torch.bfloat16):
+    if _code(x.dtype) is None:
         raise ValueError(f"x has dtype {x.dtype}; group norm takes float32, float16 or bfloat16")
     act = ACTIVATIONS.get(activation)
     if act is None:
@@ -119,33 +137,26 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
         S *= n
     if (weight is None) != (bias is None):
         raise ValueError("weight and bias: both or neither")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        if t.device != x.device or tuple(t.shape) != (C,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous vector of {C} on {x.device}")
-        if t.dtype not in (x.dtype, torch.float32):
-            raise ValueError(f"{name} must be {x.dtype} or float32")
-    if weight is not None and weight.dtype != bias.dtype:
-        raise ValueError("weight and bias must have the same dtype")
+    if weight is not None:
+        for t, name in ((weight, "weight"), (bias, "bias")):
+            if t.device != x.device or t.shape != (C,) or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous vector of {C} on {x.device}")
+            if t.dtype != x.dtype and t.dtype != torch.float32:
+                raise ValueError(f"{name} must be {x.dtype} or float32")
+        if weight.dtype != bias.dtype:
+            raise ValueError("weight and bias must have the same dtype")
     if gate is not None and (gate.device != x.device or gate.dtype != x.dtype or gate.shape != x.shape):
         raise ValueError("gate must have x's shape, dtype and device")
-    rows = {}
-    for t, name in ((x, "x"), (gate, "gate"), (out, "out")):
-        if t is None or not t.numel():
-            rows[name] = t
-            continue
-        rows[name] = r = _rows(t, C)
-        if r is None or (r.shape[0] > 1 and r.stride(0) < C) or t.data_ptr() % 16:
-            raise ValueError(f"{name} must be rows of contiguous channels, one stride apart, 16-byte aligned")
-    grad = torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, gate, weight, bias))
-    if not x.numel():
-        rows = {n: None if t is None else t.reshape(0, C) for n, t in (("x", x), ("gate", gate))}
+    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or
+                            not out.is_contiguous() or (out.numel() and out.data_ptr() % 16)):
+        raise ValueError("out must be contiguous, 16-byte aligned, and have x's shape, dtype and device")
+    x2 = _checked_rows(x, C, "x")
+    gate2 = None if gate is None else _checked_rows(gate, C, "gate")
+    grad = torch.is_grad_enabled() and (
+        x.requires_grad or (gate is not None and gate.requires_grad) or
+        (weight is not None and (weight.requires_grad or bias.requires_grad)))
     if grad:
         if out is not None or stream is not None:
             raise NotImplementedError("group_norm: no gradients with out= or stream=")
         return _autograd_function().apply(x, gate, weight, bias, N, S, C, G, act, float(eps))
-    if out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or
-                            not out.is_contiguous()):
-        raise ValueError("out must be contiguous and have x's shape, dtype and device")
-    return _forward(rows["x"], rows["gate"], weight, bias, N, S, C, G, act, float(eps), out, False, stream, x.shape)[0]
+    return _forward(x2, gate2, weight, bias, N, S, C, G, act, float(eps), out, False, stream, x.shape)[0]

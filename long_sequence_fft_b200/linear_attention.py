@@ -6,13 +6,13 @@
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 from . import BF16, F16, _check, _i64, _lib, _vp
 from . import _ptr as _p
 
 _CODES = None
+_Pair = _i64 * 2
 
 
 class _Shape(ctypes.Structure):
@@ -33,29 +33,50 @@ def _dtype_of(t, name):
     return code
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _On:
     """Make `device` and `stream` (None: the device's current one; a
-    torch.cuda.Stream or a raw handle) current, so that what is allocated here
-    belongs to the stream that uses it; yields the raw handle."""
-    import torch
-    with torch.cuda.device(device):
+    torch.cuda.Stream or a raw handle) current, so that what is allocated
+    inside belongs to the stream that uses it; enters with the raw handle.
+    Nothing is switched, or asked of torch's slower interfaces, for a call on
+    the current device and stream: small calls are all overhead."""
+    __slots__ = ("device", "stream", "outer")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.outer = device, stream, ()
+
+    def __enter__(self):
+        import torch
+        stream = self.stream
+        if stream is None and torch._C._cuda_getDevice() == self.device.index:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        device = torch.cuda.device(self.device)
+        device.__enter__()
+        self.outer = (device,)
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-            return
+            return torch.cuda.current_stream().cuda_stream
         if isinstance(stream, int):
             # 0 is the legacy default stream, which has no external handle
             stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+        inside = torch.cuda.stream(stream)
+        inside.__enter__()
+        self.outer = (inside, device)
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        for o in self.outer:
+            o.__exit__(*exc)
+        return False
+
+
+_on = _On
 
 
 def _need(t, name, dtype, shape, device):
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -65,7 +86,7 @@ def _need_contiguous(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_heads(log_decay, device, **heads):
+def _check_heads(log_decay, device, *heads):
     import torch
     if log_decay.dim() != 1 or log_decay.shape[0] == 0:
         raise ValueError("log_decay must be a vector of one value for each head")
@@ -73,17 +94,23 @@ def _check_heads(log_decay, device, **heads):
     _need_contiguous(log_decay, "log_decay", torch.float32, (H,), device)
     if log_decay.requires_grad and torch.is_grad_enabled():
         raise NotImplementedError("linear attention has no gradient for log_decay: detach it")
-    for name, h in heads.items():
+    for name, h in zip("qkv", heads):
         if h < 1 or H % h:
             raise ValueError(f"{name} has {h} heads, which do not divide the {H} heads of log_decay")
     return H
 
 
+def _check_readable(*tensors):
+    for t, name in zip(tensors, "qkv"):
+        if not ((t.is_contiguous() and t.data_ptr() % 16 == 0) or not t.numel() or _usable(t)):
+            raise ValueError(f"{name}: the last index must be contiguous, and the other strides and the data's "
+                             "address multiples of 16 bytes (not expanded)")
+
+
 def _shape_of(q, k, v, o_shape_stride, log_decay, nseq, scale, zero_rest):
     (B, T, Hq, K), Hk, (Hv, V) = q.shape, k.shape[2], v.shape[2:]
     return _Shape(B, T, nseq, log_decay.shape[0], Hq, Hk, Hv, K, V, _dtype_of(q, "q"), scale, zero_rest,
-                  (_i64 * 3)(*q.stride()[:3]), (_i64 * 3)(*k.stride()[:3]), (_i64 * 3)(*v.stride()[:3]),
-                  (_i64 * 3)(*o_shape_stride[:3]))
+                  q.stride()[:3], k.stride()[:3], v.stride()[:3], o_shape_stride[:3])
 
 
 def _workspace(shape, backward, device):
@@ -203,11 +230,8 @@ def linear_attention(q, k, v, log_decay, *, scale=None, initial_state=None, cu_s
     _dtype_of(q, "q")
     _need(k, "k", q.dtype, (B, T, k.shape[2], K), device)
     _need(v, "v", q.dtype, (B, T, v.shape[2], V), device)
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.numel() and not _usable(t):
-            raise ValueError(f"{name}: the last index must be contiguous, and the other strides and the data's "
-                             "address multiples of 16 bytes (not expanded)")
-    H = _check_heads(log_decay, device, q=Hq, k=k.shape[2], v=v.shape[2])
+    _check_readable(q, k, v)
+    H = _check_heads(log_decay, device, Hq, k.shape[2], v.shape[2])
     n = B
     if cu_seqlens is not None:
         if B != 1:
@@ -255,18 +279,15 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     code = _dtype_of(q, "q")
     _need(k, "k", q.dtype, (B, k.shape[1], K), device)
     _need(v, "v", q.dtype, (B, v.shape[1], V), device)
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.numel() and not _usable(t):
-            raise ValueError(f"{name}: the last index must be contiguous, and the other strides and the data's "
-                             "address multiples of 16 bytes (not expanded)")
-    H = _check_heads(log_decay, device, q=Hq, k=k.shape[1], v=v.shape[1])
+    _check_readable(q, k, v)
+    H = _check_heads(log_decay, device, Hq, k.shape[1], v.shape[1])
     if state.dim() != 4:
         raise ValueError("state must have 4 dimensions: sequence, head, K, V")
     pool = state.shape[0]
     _need_contiguous(state, "state", torch.float32, (B if slots is None else pool, H, K, V), device)
     if slots is not None:
         _need_contiguous(slots, "slots", torch.int32, (B,), device)
-    if torch.is_grad_enabled() and any(t.requires_grad for t in (q, k, v, state)):
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or state.requires_grad):
         raise NotImplementedError("linear_attention_step has no gradients: use linear_attention, or torch.no_grad()")
     scale = K ** -0.5 if scale is None else float(scale)
     with _on(device, stream) as handle:
@@ -276,8 +297,8 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
             _need_contiguous(out, "out", q.dtype, (B, H, V), device)
         _check(_lib.fftconv_linear_attention_step(
             _p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(slots), _p(out), B, pool, H, Hq, k.shape[1],
-            v.shape[1], K, V, code, scale, (_i64 * 2)(*q.stride()[:2]), (_i64 * 2)(*k.stride()[:2]),
-            (_i64 * 2)(*v.stride()[:2]), handle))
+            v.shape[1], K, V, code, scale, _Pair(*q.stride()[:2]), _Pair(*k.stride()[:2]), _Pair(*v.stride()[:2]),
+            handle))
     return out
 
 
