@@ -7,14 +7,16 @@
 //     dx = rstd (dn w - mean(dn w) - xh mean(dn w xh))
 //
 // All bandwidth: each value is touched by a few dozen instructions, so the
-// layouts serve wide loads and few passes.
-//   Token form (S = 1, group widths up to 8 vectors a lane): a sub-warp of 1
-//   to 32 lanes holds one row's group in registers, so x, gate and dy are
-//   read once; mean and variance in two passes over the registers.
-//   Sample form (S > 1, or wider groups): a pass for the statistics
-//   (or the sums of the backward pass), a small join, a second pass that
-//   applies them, in the opposite order of blocks so that it starts with what
-//   the first pass left in L2.
+// layouts serve wide loads, few passes and few instructions.
+//   Token form (S = 1, groups of up to 512 channels): a sub-warp of 1 to 32
+//   lanes keeps its group, with the group's weights (and sums of dw and db) in
+//   registers, and walks down the rows; x, gate and dy are read once, mean and
+//   variance take two passes over the registers.
+//   Sample form (S > 1, or wider groups): a pass for the statistics (or the
+//   sums of the backward pass), a small join, a second pass that applies them,
+//   in the opposite order of blocks so that it starts with what the first pass
+//   left in L2.  A thread keeps its channels, so groups need not be whole
+//   vectors.
 // Partial results are joined in a fixed order: runs repeat bit for bit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -46,19 +48,16 @@ template <typename T>
 struct Type;
 template <>
 struct Type<float> {
-    static constexpr int Vec = 4;
     static __device__ __forceinline__ float get(float x) { return x; }
     static __device__ __forceinline__ float put(float x) { return x; }
 };
 template <>
 struct Type<__half> {
-    static constexpr int Vec = 8;
     static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
     static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
 };
 template <>
 struct Type<__nv_bfloat16> {
-    static constexpr int Vec = 8;
     static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
     static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
 };
@@ -100,34 +99,81 @@ __device__ __forceinline__ void load_w(const void* w, int f32, int c, float none
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = none;
     } else if (f32) {
+        const float* p = reinterpret_cast<const float*>(w) + c;
+        if constexpr (V == 1) {
+            f[0] = p[0];
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = reinterpret_cast<const float*>(w)[c + i];
+            for (int i = 0; i < V; i += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p + i);
+                f[i] = v.x;
+                f[i + 1] = v.y;
+                f[i + 2] = v.z;
+                f[i + 3] = v.w;
+            }
+        }
     } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = Type<T>::get(reinterpret_cast<const T*>(w)[c + i]);
+        const Pack<T, V> v = load<T, V>(w, c);
+        unpack<T, V>(v, f);
     }
 }
 
 // exp and the reciprocal of the fast units: both within a few 2^-22 of the
 // value for the arguments where the sigmoid is not 0 or 1, below fp32's own
-// error of a sum of this kind.
+// error of a sum of this kind.  (Beyond 2^126 __fdividef gives 0, the limit.)
 __device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-// act(x) and its slope
-__device__ __forceinline__ float activate(float x, int act) {
-    if (act == FFTCONV_ACT_NONE) return x;
-    const float s = x < -87.f ? 0.f : sigmoid(x);             // (1 + exp would leave __fdividef's range)
-    return act == FFTCONV_ACT_SILU ? x * s : s;
-}
-__device__ __forceinline__ float activate(float x, int act, float& slope) {
-    slope = 1.f;
-    if (act == FFTCONV_ACT_NONE) return x;
-    const float s = x < -87.f ? 0.f : sigmoid(x);
-    if (act == FFTCONV_ACT_SIGMOID) {
-        slope = s * (1.f - s);
-        return s;
+
+// f <- act(f); slope (if wanted): act'.  One uniform branch a vector.
+template <int V, bool SLOPE>
+__device__ __forceinline__ void activate(float (&f)[V], float (&slope)[V], int act) {
+    if (act == FFTCONV_ACT_NONE) {
+        if (SLOPE)
+#pragma unroll
+            for (int j = 0; j < V; ++j) slope[j] = 1.f;
+    } else if (act == FFTCONV_ACT_SILU) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float s = sigmoid(f[j]);
+            if (SLOPE) slope[j] = s * fmaf(f[j], 1.f - s, 1.f);
+            f[j] *= s;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            f[j] = sigmoid(f[j]);
+            if (SLOPE) slope[j] = f[j] * (1.f - f[j]);
+        }
     }
-    slope = s * fmaf(x, 1.f - s, 1.f);
-    return x * s;
+}
+// y of n (in place): act(n), or n act(gate)
+template <int V>
+__device__ __forceinline__ void finish(float (&n)[V], float (&gate)[V], bool gated, int act) {
+    float none[V];
+    if (gated) {
+        activate<V, false>(gate, none, act);
+#pragma unroll
+        for (int j = 0; j < V; ++j) n[j] *= gate[j];
+    } else {
+        activate<V, false>(n, none, act);
+    }
+}
+// dn of dy (in place), and dgate of the gate (in place)
+template <int V>
+__device__ __forceinline__ void start(float (&n)[V], float (&dy)[V], float (&gate)[V], bool gated, int act) {
+    float slope[V];
+    if (gated) {
+        activate<V, true>(gate, slope, act);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = dy[j];
+            dy[j] = d * gate[j];
+            gate[j] = d * n[j] * slope[j];
+        }
+    } else {
+        activate<V, true>(n, slope, act);
+#pragma unroll
+        for (int j = 0; j < V; ++j) dy[j] *= slope[j];
+    }
 }
 
 template <int LANES>
@@ -138,162 +184,170 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // ------------------------------------------------------------ token form ---
+//
+// I vectors of V elements a lane, LANES lanes a group.  Blocks of
+// gsubs x rsubs sub-warps (groups x rows), grid (row blocks, group blocks); U
+// rows of a sub-warp are in flight together.
 
-// I vectors of V elements a lane, LANES lanes a (row, group) pair, U pairs in
-// flight a sub-warp.
 template <typename T, int V, int I, int LANES>
-__global__ void __launch_bounds__(kThreads) gn_token_forward(const Args a) {
-    constexpr int U = I >= 4 ? 1 : 4 / I;
+__global__ void __launch_bounds__(kThreads) gn_token_forward(const Args a, int gsubs, int rsubs) {
+    constexpr int U = I == 1 ? 4 : I == 2 ? 2 : 1;
+    constexpr bool kKeep = I * V <= 16;                       // weights stay in registers
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    constexpr int kSubs = kThreads / LANES;
-    const int nvec = a.D / V;
-    const int64_t pairs = a.N * a.G;
+    const int g = blockIdx.y * gsubs + sub % gsubs, rs = sub / gsubs;
+    const bool on = g < a.G && rs < rsubs;
+    const int nvec = a.D / V, c = g * a.D + lane * V;
     const float inv = 1.f / (float)a.D;
-    const int64_t p0 = (int64_t)blockIdx.x * (kSubs * U) + sub;
-    Pack<T, V> x[U][I], gt[U][I];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t p = p0 + u * kSubs;
-        if (p >= pairs) continue;
-        const int64_t r = p / a.G;
-        const int c = (int)(p % a.G) * a.D;
+    const bool gated = a.gate != nullptr;
+    float w[kKeep ? I : 1][V], b[kKeep ? I : 1][V];
+    if constexpr (kKeep) {
 #pragma unroll
         for (int i = 0; i < I; ++i)
-            if (lane + i * LANES < nvec) {
-                const int at = c + (lane + i * LANES) * V;
-                x[u][i] = load<T, V>(a.x, r * a.ldx + at);
-                if (a.gate) gt[u][i] = load<T, V>(a.gate, r * a.ldg + at);
+            if (on && lane + i * LANES < nvec) {
+                load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, w[i]);
+                load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, b[i]);
             }
     }
+    // (the same trip count for a whole block: all lanes take part in the sums)
+    for (int64_t base = (int64_t)blockIdx.x * rsubs * U; base < a.N; base += (int64_t)gridDim.x * rsubs * U) {
+        Pack<T, V> x[U][I], gt[U][I];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t p = p0 + u * kSubs;
-        const bool in = p < pairs;                            // (all lanes take part in the shuffles)
-        const int64_t r = p / a.G;
-        const int c = (int)(p % a.G) * a.D;
-        float f[I][V], sum = 0.f, sq = 0.f;
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = base + u * rsubs + rs;
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if (in && lane + i * LANES < nvec) {
-                unpack<T, V>(x[u][i], f[i]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) sum += f[i][j];
-            }
-        }
-        const float mean = lanes_sum<LANES>(sum) * inv;
-#pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if (in && lane + i * LANES < nvec) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    f[i][j] -= mean;
-                    sq = fmaf(f[i][j], f[i][j], sq);
+            for (int i = 0; i < I; ++i)
+                if (on && r < a.N && lane + i * LANES < nvec) {
+                    x[u][i] = load<T, V>(a.x, r * a.ldx + c + i * LANES * V);
+                    if (gated) gt[u][i] = load<T, V>(a.gate, r * a.ldg + c + i * LANES * V);
                 }
-            }
-        }
-        const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(sq), inv, a.eps));
-        if (!in) continue;
-        if (lane == 0 && a.mean) {
-            a.mean[p] = mean;
-            a.rstd[p] = rstd;
         }
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if (lane + i * LANES >= nvec) continue;
-            const int at = c + (lane + i * LANES) * V;
-            float w[V], b[V], g[V];
-            load_w<T, V>(a.w, a.w_f32, at, 1.f, w);
-            load_w<T, V>(a.b, a.w_f32, at, 0.f, b);
-            if (a.gate) unpack<T, V>(gt[u][i], g);
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = base + u * rsubs + rs;
+            const bool in = on && r < a.N;
+            float f[I][V], sum = 0.f, sq = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float n = fmaf(f[i][j] * rstd, w[j], b[j]);
-                f[i][j] = a.gate ? n * activate(g[j], a.act) : activate(n, a.act);
+            for (int i = 0; i < I; ++i)
+                if (in && lane + i * LANES < nvec) {
+                    unpack<T, V>(x[u][i], f[i]);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) sum += f[i][j];
+                }
+            const float mean = lanes_sum<LANES>(sum) * inv;
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+                if (in && lane + i * LANES < nvec) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        f[i][j] -= mean;
+                        sq = fmaf(f[i][j], f[i][j], sq);
+                    }
+                }
+            const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(sq), inv, a.eps));
+            if (!in) continue;
+            if (lane == 0 && a.mean) {
+                a.mean[r * a.G + g] = mean;
+                a.rstd[r * a.G + g] = rstd;
             }
-            store<T, V>(a.y, r * a.C + at, f[i]);
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                if (lane + i * LANES >= nvec) continue;
+                float gate[V];
+                if (gated) unpack<T, V>(gt[u][i], gate);
+                if constexpr (kKeep) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
+                } else {
+                    float wi[V], bi[V];
+                    load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, wi);
+                    load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, bi);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * rstd, wi[j], bi[j]);
+                }
+                finish<V>(f[i], gate, gated, a.act);
+                store<T, V>(a.y, r * a.C + c + i * LANES * V, f[i]);
+            }
         }
     }
 }
 
-// Blocks of (groups x rows) sub-warps: a sub-warp keeps its group and walks
-// down the rows, so that its channels' dw and db stay in registers.
-// blockDim = LANES * subs, subs = gsubs * rsubs; grid (row blocks, group blocks).
 template <typename T, int V, int I, int LANES>
 __global__ void __launch_bounds__(kThreads) gn_token_backward(const Args a, int gsubs, int rsubs) {
+    constexpr int U = I * V <= 8 ? 2 : 1;
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     const int g = blockIdx.y * gsubs + sub % gsubs, rs = sub / gsubs;
     const bool on = g < a.G && rs < rsubs;
-    const int nvec = a.D / V;
+    const int nvec = a.D / V, c = g * a.D + lane * V;
     const float inv = 1.f / (float)a.D;
-    const int c = g * a.D;
-    const int64_t stride = (int64_t)gridDim.x * rsubs;
-    const int64_t row0 = (int64_t)blockIdx.x * rsubs;
+    const bool gated = a.gate != nullptr;
     float dw[I][V], db[I][V], w[I][V], b[I][V];
 #pragma unroll
     for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = w[i][j] = b[i][j] = 0.f;
-    if (on)
 #pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (lane + i * LANES < nvec) {
-                load_w<T, V>(a.w, a.w_f32, c + (lane + i * LANES) * V, 1.f, w[i]);
-                load_w<T, V>(a.b, a.w_f32, c + (lane + i * LANES) * V, 0.f, b[i]);
-            }
-    for (int64_t base = row0; base < a.N; base += stride) {   // the same trip count for a whole block
-        const int64_t r = base + rs;
-        const bool in = on && r < a.N;
-        float mean = 0.f, rstd = 0.f;
-        Pack<T, V> px[I], pd[I], pg[I];
-        if (in) {
-            mean = a.mean[r * a.G + g];
-            rstd = a.rstd[r * a.G + g];
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-                if (lane + i * LANES < nvec) {
-                    const int at = c + (lane + i * LANES) * V;
-                    px[i] = load<T, V>(a.x, r * a.ldx + at);
-                    pd[i] = load<T, V>(a.dy, r * a.ldy + at);
-                    if (a.gate) pg[i] = load<T, V>(a.gate, r * a.ldg + at);
-                }
+    for (int i = 0; i < I; ++i)
+        if (on && lane + i * LANES < nvec) {
+            load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, w[i]);
+            load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, b[i]);
         }
-        float xh[I][V], dn[I][V], s1 = 0.f, s2 = 0.f;
+    for (int64_t base = (int64_t)blockIdx.x * rsubs * U; base < a.N; base += (int64_t)gridDim.x * rsubs * U) {
+        float mean[U], rstd[U];
+        Pack<T, V> px[U][I], pd[U][I], pg[U][I];
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if (!in || lane + i * LANES >= nvec) continue;
-            float dy[V], gt[V];
-            unpack<T, V>(px[i], xh[i]);
-            unpack<T, V>(pd[i], dy);
-            if (a.gate) unpack<T, V>(pg[i], gt);
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = base + u * rsubs + rs;
+            if (on && r < a.N) {
+                mean[u] = a.mean[r * a.G + g];
+                rstd[u] = a.rstd[r * a.G + g];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                xh[i][j] = (xh[i][j] - mean) * rstd;
-                const float n = fmaf(xh[i][j], w[i][j], b[i][j]);
-                float slope;
-                if (a.gate) {
-                    dn[i][j] = dy[j] * activate(gt[j], a.act, slope);
-                    gt[j] = dy[j] * n * slope;
-                } else {
-                    activate(n, a.act, slope);
-                    dn[i][j] = dy[j] * slope;
-                }
-                dw[i][j] = fmaf(dn[i][j], xh[i][j], dw[i][j]);
-                db[i][j] += dn[i][j];
-                dn[i][j] *= w[i][j];
-                s1 += dn[i][j];
-                s2 = fmaf(dn[i][j], xh[i][j], s2);
+                for (int i = 0; i < I; ++i)
+                    if (lane + i * LANES < nvec) {
+                        const int at = c + i * LANES * V;
+                        px[u][i] = load<T, V>(a.x, r * a.ldx + at);
+                        pd[u][i] = load<T, V>(a.dy, r * a.ldy + at);
+                        if (gated) pg[u][i] = load<T, V>(a.gate, r * a.ldg + at);
+                    }
             }
-            if (a.gate) store<T, V>(a.dgate, r * a.C + c + (lane + i * LANES) * V, gt);
         }
-        s1 = lanes_sum<LANES>(s1) * inv;
-        s2 = lanes_sum<LANES>(s2) * inv;
-        if (!in) continue;
 #pragma unroll
-        for (int i = 0; i < I; ++i) {
-            if (lane + i * LANES >= nvec) continue;
+        for (int u = 0; u < U; ++u) {
+            const int64_t r = base + u * rsubs + rs;
+            const bool in = on && r < a.N;
+            float xh[I][V], dn[I][V], s1 = 0.f, s2 = 0.f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) dn[i][j] = rstd * (dn[i][j] - s1 - xh[i][j] * s2);
-            store<T, V>(a.dx, r * a.C + c + (lane + i * LANES) * V, dn[i]);
+            for (int i = 0; i < I; ++i) {
+                if (!in || lane + i * LANES >= nvec) continue;
+                float gt[V], n[V];
+                unpack<T, V>(px[u][i], xh[i]);
+                unpack<T, V>(pd[u][i], dn[i]);
+                if (gated) unpack<T, V>(pg[u][i], gt);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    xh[i][j] = (xh[i][j] - mean[u]) * rstd[u];
+                    n[j] = fmaf(xh[i][j], w[i][j], b[i][j]);
+                }
+                start<V>(n, dn[i], gt, gated, a.act);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dw[i][j] = fmaf(dn[i][j], xh[i][j], dw[i][j]);
+                    db[i][j] += dn[i][j];
+                    dn[i][j] *= w[i][j];
+                    s1 += dn[i][j];
+                    s2 = fmaf(dn[i][j], xh[i][j], s2);
+                }
+                if (gated) store<T, V>(a.dgate, r * a.C + c + i * LANES * V, gt);
+            }
+            s1 = lanes_sum<LANES>(s1) * inv;
+            s2 = lanes_sum<LANES>(s2) * inv;
+            if (!in) continue;
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                if (lane + i * LANES >= nvec) continue;
+#pragma unroll
+                for (int j = 0; j < V; ++j) dn[i][j] = rstd[u] * (dn[i][j] - s1 - xh[i][j] * s2);
+                store<T, V>(a.dx, r * a.C + c + i * LANES * V, dn[i]);
+            }
         }
     }
     if (!on || !a.dw) return;
@@ -303,8 +357,8 @@ __global__ void __launch_bounds__(kThreads) gn_token_backward(const Args a, int 
         if (lane + i * LANES < nvec)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                out[(lane + i * LANES) * V + j] = dw[i][j];
-                out[a.C + (lane + i * LANES) * V + j] = db[i][j];
+                out[i * LANES * V + j] = dw[i][j];
+                out[a.C + i * LANES * V + j] = db[i][j];
             }
 }
 
@@ -361,52 +415,69 @@ __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, flo
     n = t;
 }
 
+// Statistics of a block's part of every group: per channel first, from sums
+// over a few positions at a time.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) gn_stats(const Args a) {
-    __shared__ float sh[3][kThreads];
+    __shared__ float sh_m[V * kThreads], sh_q[V * kThreads], sh_n[kThreads];      // [row lane][channel of the block]
     const Tile t = tile_of<V>(a, blockIdx.x);
-    float n = 0.f, m = 0.f, q = 0.f;
+    const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
+    float n = 0.f, m[V], q[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) m[j] = q[j] = 0.f;
     if (t.on) {
         const int64_t row0 = (int64_t)t.n * a.S;
         constexpr int kAhead = V == 1 ? 8 : 4;
         for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
             Pack<T, V> p[kAhead];
-            float f[kAhead][V], sum = 0.f, sq = 0.f, cnt = 0.f;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1) p[k] = load<T, V>(a.x, (row0 + s + k * t.rows) * a.ldx + (int64_t)t.colv * V);
+            float cnt = 0.f;
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (s + k * t.rows < t.s1) {
-                    unpack<T, V>(p[k], f[k]);
-                    cnt += V;
-#pragma unroll
-                    for (int j = 0; j < V; ++j) sum += f[k][j];
+                    p[k] = load<T, V>(a.x, (row0 + s + k * t.rows) * a.ldx + (int64_t)t.colv * V);
+                    cnt += 1.f;
                 }
-            const float mean = sum / cnt;
+            const float inv = 1.f / cnt, f = cnt / (n + cnt);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1)
+            for (int j = 0; j < V; ++j) {
+                float x[kAhead], sum = 0.f, sq = 0.f;
 #pragma unroll
-                    for (int j = 0; j < V; ++j) sq = fmaf(f[k][j] - mean, f[k][j] - mean, sq);
-            join(n, m, q, cnt, mean, sq);
+                for (int k = 0; k < kAhead; ++k)
+                    if (s + k * t.rows < t.s1) {
+                        x[k] = Type<T>::get(p[k].e[j]);
+                        sum += x[k];
+                    }
+                const float mean = sum * inv;
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    if (s + k * t.rows < t.s1) sq = fmaf(x[k] - mean, x[k] - mean, sq);
+                const float d = mean - m[j];
+                m[j] = fmaf(d, f, m[j]);
+                q[j] += fmaf(d * d, n * f, sq);
+            }
+            n += cnt;
         }
     }
-    sh[0][threadIdx.x] = n;
-    sh[1][threadIdx.x] = m;
-    sh[2][threadIdx.x] = q;
+    if (t.on) {
+        const int at = t.rl * width + (t.colv - (int)blockIdx.y * kThreads);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            sh_m[at * V + j] = m[j];
+            sh_q[at * V + j] = q[j];
+        }
+        if (at % width == 0) sh_n[t.rl] = n;
+    }
     __syncthreads();
-    // one warp a group: the entries of the group's columns in every row lane
-    const int gv = a.D / V, width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
-    const int v0 = blockIdx.y * kThreads, g0 = v0 / gv, g1 = (v0 + width - 1) / gv;
+    // one warp a group: its channels in every row lane
+    const int c0 = (int)blockIdx.y * kThreads * V, c1 = c0 + width * V;
     const int lane = threadIdx.x % 32;
     for (int g = threadIdx.x / 32; g < a.G; g += kThreads / 32) {
         float gn = 0.f, gm = 0.f, gq = 0.f;
-        if (g >= g0 && g <= g1) {
-            const int lo = max(g * gv, v0) - v0, hi = min((g + 1) * gv, v0 + width) - v0;
+        const int lo = max(g * a.D, c0) - c0, hi = min((g + 1) * a.D, c1) - c0;
+        if (hi > lo) {
             for (int e = lane; e < (hi - lo) * t.rows; e += 32) {
-                const int at = e / (hi - lo) * width + lo + e % (hi - lo);
-                join(gn, gm, gq, sh[0][at], sh[1][at], sh[2][at]);
+                const int row = e / (hi - lo), at = row * width * V + lo + e % (hi - lo);
+                join(gn, gm, gq, sh_n[row], sh_m[at], sh_q[at]);
             }
             for (int d = 16; d > 0; d >>= 1) {
                 const float n2 = __shfl_down_sync(0xffffffffu, gn, d), m2 = __shfl_down_sync(0xffffffffu, gm, d),
@@ -427,6 +498,7 @@ __global__ void __launch_bounds__(kThreads) gn_join_stats(const Args a) {
     if (p >= a.N * a.G) return;
     const int lane = threadIdx.x % 32;
     float n = 0.f, m = 0.f, q = 0.f;
+#pragma unroll 4
     for (int e = lane; e < a.parts; e += 32) {
         const float4 v = reinterpret_cast<const float4*>(a.part)[p * a.parts + e];
         join(n, m, q, v.x, v.y, v.z);
@@ -442,17 +514,32 @@ __global__ void __launch_bounds__(kThreads) gn_join_stats(const Args a) {
     }
 }
 
+// mean, rstd, weight and bias of a thread's channels
+template <typename T, int V>
+__device__ __forceinline__ void channel_of(const Args& a, int n, int c, float (&mean)[V], float (&rstd)[V],
+                                           float (&w)[V], float (&b)[V]) {
+    load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
+    load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t p = (int64_t)n * a.G + (c + j) / a.D;
+        mean[j] = a.mean[p];
+        rstd[j] = a.rstd[p];
+    }
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) gn_apply(const Args a) {
     const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!t.on) return;
     const int c = t.colv * V;
-    const int64_t p = (int64_t)t.n * a.G + c / a.D, row0 = (int64_t)t.n * a.S;
-    const float mean = a.mean[p], rstd = a.rstd[p];
-    float w[V], b[V];
-    load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
-    load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+    const int64_t row0 = (int64_t)t.n * a.S;
+    float mean[V], rstd[V], w[V], b[V];
+    channel_of<T, V>(a, t.n, c, mean, rstd, w, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[j] *= rstd[j];
     constexpr int kAhead = 4;
+    const bool gated = a.gate != nullptr;
     for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
         Pack<T, V> px[kAhead], pg[kAhead];
 #pragma unroll
@@ -460,64 +547,56 @@ __global__ void __launch_bounds__(kThreads) gn_apply(const Args a) {
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
                 px[k] = load<T, V>(a.x, r * a.ldx + c);
-                if (a.gate) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                if (gated) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
                 float f[V], g[V];
                 unpack<T, V>(px[k], f);
-                if (a.gate) unpack<T, V>(pg[k], g);
+                if (gated) unpack<T, V>(pg[k], g);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float n = fmaf((f[j] - mean) * rstd, w[j], b[j]);
-                    f[j] = a.gate ? n * activate(g[j], a.act) : activate(n, a.act);
-                }
+                for (int j = 0; j < V; ++j) f[j] = fmaf(f[j] - mean[j], w[j], b[j]);
+                finish<V>(f, g, gated, a.act);
                 store<T, V>(a.y, (row0 + s + k * t.rows) * a.C + c, f);
             }
     }
 }
 
-// dn (and dgate) of one vector
+// xh, dn and dgate of one vector
 template <typename T, int V>
-__device__ __forceinline__ void grad_of(const Args& a, const Pack<T, V>& px, const Pack<T, V>& pd, const Pack<T, V>& pg,
-                                        float mean, float rstd, const float (&w)[V], const float (&b)[V],
-                                        float (&xh)[V], float (&dn)[V], float (&dg)[V]) {
-    float dy[V];
+__device__ __forceinline__ void grad_of(const Args& a, bool gated, const Pack<T, V>& px, const Pack<T, V>& pd,
+                                        const Pack<T, V>& pg, const float (&mean)[V], const float (&rstd)[V],
+                                        const float (&w)[V], const float (&b)[V], float (&xh)[V], float (&dn)[V],
+                                        float (&dg)[V]) {
+    float n[V];
     unpack<T, V>(px, xh);
-    unpack<T, V>(pd, dy);
-    if (a.gate) unpack<T, V>(pg, dg);
+    unpack<T, V>(pd, dn);
+    if (gated) unpack<T, V>(pg, dg);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        xh[j] = (xh[j] - mean) * rstd;
-        const float n = fmaf(xh[j], w[j], b[j]);
-        float slope;
-        if (a.gate) {
-            dn[j] = dy[j] * activate(dg[j], a.act, slope);
-            dg[j] = dy[j] * n * slope;
-        } else {
-            activate(n, a.act, slope);
-            dn[j] = dy[j] * slope;
-        }
+        xh[j] = (xh[j] - mean[j]) * rstd[j];
+        n[j] = fmaf(xh[j], w[j], b[j]);
     }
+    start<V>(n, dn, dg, gated, a.act);
 }
 
 // First backward pass: the sums of dn xh and dn over the chunk's positions,
 // by channel: part[(sample, chunk)][2][C].
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) gn_grad_sums(const Args a) {
-    __shared__ float sh[2][kThreads][V];
+    __shared__ float sh[2][kThreads * V];
     const Tile t = tile_of<V>(a, blockIdx.x);
+    const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
     float s1[V], s2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
     const int c = t.colv * V;
     if (t.on) {
-        const int64_t p = (int64_t)t.n * a.G + c / a.D, row0 = (int64_t)t.n * a.S;
-        const float mean = a.mean[p], rstd = a.rstd[p];
-        float w[V], b[V];
-        load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
-        load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+        const int64_t row0 = (int64_t)t.n * a.S;
+        const bool gated = a.gate != nullptr;
+        float mean[V], rstd[V], w[V], b[V];
+        channel_of<T, V>(a, t.n, c, mean, rstd, w, b);
         constexpr int kAhead = 2;
         for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
             Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
@@ -527,13 +606,13 @@ __global__ void __launch_bounds__(kThreads) gn_grad_sums(const Args a) {
                     const int64_t r = row0 + s + k * t.rows;
                     px[k] = load<T, V>(a.x, r * a.ldx + c);
                     pd[k] = load<T, V>(a.dy, r * a.ldy + c);
-                    if (a.gate) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                    if (gated) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
                 }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (s + k * t.rows < t.s1) {
                     float xh[V], dn[V], dg[V];
-                    grad_of<T, V>(a, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
+                    grad_of<T, V>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         s1[j] = fmaf(dn[j], xh[j], s1[j]);
@@ -541,53 +620,55 @@ __global__ void __launch_bounds__(kThreads) gn_grad_sums(const Args a) {
                     }
                 }
         }
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        sh[0][threadIdx.x][j] = s1[j];
-        sh[1][threadIdx.x][j] = s2[j];
-    }
-    __syncthreads();
-    if (t.on && t.rl == 0) {
-        const int width = kThreads / t.rows == 0 ? 1 : min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
-        float* out = a.part + (int64_t)blockIdx.x * 2 * a.C + c;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            float x = 0.f, y = 0.f;
-            for (int r = 0; r < t.rows; ++r) {
-                x += sh[0][threadIdx.x + r * width][j];
-                y += sh[1][threadIdx.x + r * width][j];
-            }
-            out[j] = x;
-            out[a.C + j] = y;
+            sh[0][(t.rl * width + t.colv - (int)blockIdx.y * kThreads) * V + j] = s1[j];
+            sh[1][(t.rl * width + t.colv - (int)blockIdx.y * kThreads) * V + j] = s2[j];
         }
+    }
+    __syncthreads();
+    float* out = a.part + (int64_t)blockIdx.x * 2 * a.C + (int64_t)blockIdx.y * kThreads * V;
+    for (int e = threadIdx.x; e < width * V; e += kThreads) {
+        float x = 0.f, y = 0.f;
+        for (int r = 0; r < t.rows; ++r) {
+            x += sh[0][r * width * V + e];
+            y += sh[1][r * width * V + e];
+        }
+        out[e] = x;
+        out[a.C + e] = y;
     }
 }
 
-// One warp a (sample, group): mean(dn w) and mean(dn w xh).
+// One block a (sample, group): mean(dn w) and mean(dn w xh).
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gn_join_sums(const Args a) {
-    const int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-    if (p >= a.N * a.G) return;
-    const int64_t n = p / a.G;
-    const int c0 = (int)(p % a.G) * a.D, lane = threadIdx.x % 32;
+    __shared__ float sh[2][kThreads / 32];
+    const int64_t p = blockIdx.x, n = p / a.G;
+    const int c0 = (int)(p % a.G) * a.D;
     float s1 = 0.f, s2 = 0.f;
-    for (int c = c0 + lane % a.D; c < c0 + a.D && lane < 32 / min(32, a.D) * a.D; c += 32) {
-        // narrow groups: the lanes beyond the first a.D take further chunks
-        const int step = a.D >= 32 ? 1 : 32 / a.D;
-        float w[1], x = 0.f, y = 0.f;
+    // (chunk, channel) in order of memory
+#pragma unroll 4
+    for (int e = threadIdx.x; e < a.D * a.chunks; e += kThreads) {
+        const int k = e / a.D, c = c0 + e % a.D;
+        float w[1];
         load_w<T, 1>(a.w, a.w_f32, c, 1.f, w);
-        for (int k = a.D >= 32 ? 0 : lane / a.D; k < a.chunks; k += step) {
-            const float* src = a.part + (n * a.chunks + k) * 2 * a.C;
-            x += src[c];
-            y += src[a.C + c];
-        }
-        s1 = fmaf(x, w[0], s1);
-        s2 = fmaf(y, w[0], s2);
+        const float* src = a.part + (n * a.chunks + k) * 2 * a.C + c;
+        s1 = fmaf(src[0], w[0], s1);
+        s2 = fmaf(src[a.C], w[0], s2);
     }
     s1 = lanes_sum<32>(s1);
     s2 = lanes_sum<32>(s2);
-    if (lane == 0) {
+    if (threadIdx.x % 32 == 0) {
+        sh[0][threadIdx.x / 32] = s1;
+        sh[1][threadIdx.x / 32] = s2;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s1 = s2 = 0.f;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            s1 += sh[0][i];
+            s2 += sh[1][i];
+        }
         const float inv = 1.f / ((float)a.S * (float)a.D);
         a.sums[2 * p] = s2 * inv;
         a.sums[2 * p + 1] = s1 * inv;
@@ -599,11 +680,16 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply(const Args a) {
     const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!t.on) return;
     const int c = t.colv * V;
-    const int64_t p = (int64_t)t.n * a.G + c / a.D, row0 = (int64_t)t.n * a.S;
-    const float mean = a.mean[p], rstd = a.rstd[p], m1 = a.sums[2 * p], m2 = a.sums[2 * p + 1];
-    float w[V], b[V];
-    load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
-    load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+    const int64_t row0 = (int64_t)t.n * a.S;
+    const bool gated = a.gate != nullptr;
+    float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
+    channel_of<T, V>(a, t.n, c, mean, rstd, w, b);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t p = (int64_t)t.n * a.G + (c + j) / a.D;
+        m1[j] = a.sums[2 * p];
+        m2[j] = a.sums[2 * p + 1];
+    }
     constexpr int kAhead = 2;
     for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
         Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
@@ -613,17 +699,17 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply(const Args a) {
                 const int64_t r = row0 + s + k * t.rows;
                 px[k] = load<T, V>(a.x, r * a.ldx + c);
                 pd[k] = load<T, V>(a.dy, r * a.ldy + c);
-                if (a.gate) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                if (gated) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
                 float xh[V], dn[V], dg[V];
-                grad_of<T, V>(a, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
-                if (a.gate) store<T, V>(a.dgate, r * a.C + c, dg);
+                grad_of<T, V>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
+                if (gated) store<T, V>(a.dgate, r * a.C + c, dg);
 #pragma unroll
-                for (int j = 0; j < V; ++j) dn[j] = rstd * (dn[j] * w[j] - m1 - xh[j] * m2);
+                for (int j = 0; j < V; ++j) dn[j] = rstd[j] * (dn[j] * w[j] - m1[j] - xh[j] * m2[j]);
                 store<T, V>(a.dx, r * a.C + c, dn);
             }
     }
@@ -636,10 +722,10 @@ int fail(int status, const std::string& msg) {
     return status;
 }
 
-constexpr int64_t kTokenBlocks = 148 * 8;     // row blocks of the token form's backward pass at most
+constexpr int64_t kTokenBlocks = 148 * 4;     // row blocks of the token form at most: they walk
 
 // Samples are cut so that the blocks fill the GPU a few times over, but no
-// finer than 16 positions for each row lane.
+// finer than 16384 values.
 int64_t chunks_of(int64_t N, int64_t S, int64_t C) {
     int64_t want = (148 * 8 + N - 1) / N;
     const int64_t most = S * C / 16384 > 1 ? S * C / 16384 : 1;
@@ -647,105 +733,112 @@ int64_t chunks_of(int64_t N, int64_t S, int64_t C) {
     return want > S ? S : want;
 }
 
-// Lanes and vectors a lane of the token form for groups of nvec vectors; 0
-// lanes: too wide for it.
-void token_shape(int64_t nvec, int& lanes, int& per) {
+// Lanes and vectors a lane of the token form for groups of nvec vectors of V
+// elements; 0 lanes: too wide for it (over 512 channels, or 256 one by one).
+void token_shape(int64_t nvec, int V, int& lanes, int& per) {
     lanes = 1;
     while (lanes < 32 && lanes < nvec) lanes *= 2;
     per = 1;
     while (per * lanes < nvec) per *= 2;
-    if (per > 8) lanes = 0;
-}
-
-template <typename T, int V, int I>
-void token_forward(const Args& a, int lanes, cudaStream_t s) {
-    constexpr int U = I >= 4 ? 1 : 4 / I;
-    const int64_t pairs = a.N * a.G, per = (int64_t)kThreads / lanes * U;
-    const unsigned grid = (unsigned)((pairs + per - 1) / per);
-    if constexpr (I == 1) {
-        switch (lanes) {
-            case 1: gn_token_forward<T, V, I, 1><<<grid, kThreads, 0, s>>>(a); return;
-            case 2: gn_token_forward<T, V, I, 2><<<grid, kThreads, 0, s>>>(a); return;
-            case 4: gn_token_forward<T, V, I, 4><<<grid, kThreads, 0, s>>>(a); return;
-            case 8: gn_token_forward<T, V, I, 8><<<grid, kThreads, 0, s>>>(a); return;
-            case 16: gn_token_forward<T, V, I, 16><<<grid, kThreads, 0, s>>>(a); return;
-            default: break;
-        }
-    }
-    gn_token_forward<T, V, I, 32><<<grid, kThreads, 0, s>>>(a);
+    if (per > (V == 8 ? 2 : V == 4 ? 4 : 8)) lanes = 0;
 }
 
 struct TokenGrid {
     int gsubs, rsubs, threads;
     unsigned gx, gy;
 };
-TokenGrid token_grid(int64_t N, int64_t G, int lanes) {
+// Blocks of whole rows where the groups of one fit, so that a block's loads
+// are contiguous; as many as fill the GPU, or fewer where rows run out.
+TokenGrid token_grid(int64_t N, int64_t G, int lanes, int rows_at_once) {
     TokenGrid t;
     const int subs = kThreads / lanes;
     t.gsubs = (int)(G < subs ? G : subs);
     t.rsubs = subs / t.gsubs;
+    if (t.rsubs > N) t.rsubs = (int)N;
     t.threads = (t.gsubs * t.rsubs * lanes + 31) / 32 * 32;
     t.gy = (unsigned)((G + t.gsubs - 1) / t.gsubs);
-    int64_t most = kTokenBlocks / t.gy > 1 ? kTokenBlocks / t.gy : 1;
-    const int64_t rows = (N + t.rsubs - 1) / t.rsubs;
+    const int64_t most = kTokenBlocks / t.gy > 1 ? kTokenBlocks / t.gy : 1;
+    const int64_t rows = (N + t.rsubs * rows_at_once - 1) / (t.rsubs * rows_at_once);
     t.gx = (unsigned)(rows < most ? rows : most);
     return t;
 }
 
-template <typename T, int V, int I>
-void token_backward(const Args& a, int lanes, const TokenGrid& t, cudaStream_t s) {
+template <typename T, int V, int I, int LANES>
+void token_launch(const Args& a, const TokenGrid& t, bool back, cudaStream_t s) {
     const dim3 grid(t.gx, t.gy);
-    if constexpr (I == 1) {
+    if (back)
+        gn_token_backward<T, V, I, LANES><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
+    else
+        gn_token_forward<T, V, I, LANES><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
+}
+
+// (the rows that a sub-warp has in flight, as the kernels choose them)
+int rows_at_once(int per, int V, bool back) { return back ? (per * V <= 8 ? 2 : 1) : per == 1 ? 4 : per == 2 ? 2 : 1; }
+
+template <typename T, int V>
+void token(Args a, int lanes, int per, bool back, cudaStream_t s) {
+    const TokenGrid t = token_grid(a.N, a.G, lanes, rows_at_once(per, V, back));
+    a.parts = (int)t.gx * t.rsubs;
+    if (per == 1) {
         switch (lanes) {
-            case 1: gn_token_backward<T, V, I, 1><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs); return;
-            case 2: gn_token_backward<T, V, I, 2><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs); return;
-            case 4: gn_token_backward<T, V, I, 4><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs); return;
-            case 8: gn_token_backward<T, V, I, 8><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs); return;
-            case 16: gn_token_backward<T, V, I, 16><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs); return;
-            default: break;
+            case 1: token_launch<T, V, 1, 1>(a, t, back, s); break;
+            case 2: token_launch<T, V, 1, 2>(a, t, back, s); break;
+            case 4: token_launch<T, V, 1, 4>(a, t, back, s); break;
+            case 8: token_launch<T, V, 1, 8>(a, t, back, s); break;
+            case 16: token_launch<T, V, 1, 16>(a, t, back, s); break;
+            default: token_launch<T, V, 1, 32>(a, t, back, s); break;
+        }
+    } else if (per == 2) {
+        token_launch<T, V, 2, 32>(a, t, back, s);
+    } else if constexpr (V < 8) {
+        if (per == 4) {
+            token_launch<T, V, 4, 32>(a, t, back, s);
+        } else if constexpr (V == 1) {
+            token_launch<T, V, 8, 32>(a, t, back, s);
         }
     }
-    gn_token_backward<T, V, I, 32><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
+    if (back && a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
 }
 
 template <typename T, int V>
-void forward(Args a, bool token, int lanes, int per, cudaStream_t s) {
-    if (token) {
-        switch (per) {
-            case 1: return token_forward<T, V, 1>(a, lanes, s);
-            case 2: return token_forward<T, V, 2>(a, lanes, s);
-            case 4: return token_forward<T, V, 4>(a, lanes, s);
-            default: return token_forward<T, V, 8>(a, lanes, s);
-        }
-    }
+void sample(Args a, bool back, cudaStream_t s) {
     const unsigned cols = (unsigned)((a.C / V + kThreads - 1) / kThreads);
     const dim3 grid((unsigned)(a.N * a.chunks), cols);
-    a.parts = (int)cols * a.chunks;
-    gn_stats<T, V><<<grid, kThreads, 0, s>>>(a);
-    gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
-    gn_apply<T, V><<<grid, kThreads, 0, s>>>(a);
+    if (!back) {
+        a.parts = (int)cols * a.chunks;
+        gn_stats<T, V><<<grid, kThreads, 0, s>>>(a);
+        gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
+        gn_apply<T, V><<<grid, kThreads, 0, s>>>(a);
+    } else {
+        a.parts = (int)(a.N * a.chunks);
+        gn_grad_sums<T, V><<<grid, kThreads, 0, s>>>(a);
+        gn_join_sums<T><<<(unsigned)(a.N * a.G), kThreads, 0, s>>>(a);
+        gn_grad_apply<T, V><<<grid, kThreads, 0, s>>>(a);
+        if (a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
+    }
 }
 
 template <typename T, int V>
-void backward(Args a, bool token, int lanes, int per, cudaStream_t s) {
-    if (token) {
-        const TokenGrid t = token_grid(a.N, a.G, lanes);
-        a.parts = (int)t.gx * t.rsubs;
-        switch (per) {
-            case 1: token_backward<T, V, 1>(a, lanes, t, s); break;
-            case 2: token_backward<T, V, 2>(a, lanes, t, s); break;
-            case 4: token_backward<T, V, 4>(a, lanes, t, s); break;
-            default: token_backward<T, V, 8>(a, lanes, t, s); break;
-        }
-    } else {
-        const unsigned cols = (unsigned)((a.C / V + kThreads - 1) / kThreads);
-        const dim3 grid((unsigned)(a.N * a.chunks), cols);
-        a.parts = (int)(a.N * a.chunks);
-        gn_grad_sums<T, V><<<grid, kThreads, 0, s>>>(a);
-        gn_join_sums<T><<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
-        gn_grad_apply<T, V><<<grid, kThreads, 0, s>>>(a);
+void run(const Args& a, bool back, cudaStream_t s) {
+    int lanes = 0, per = 0;
+    if (a.S == 1 && a.D % V == 0) token_shape(a.D / V, V, lanes, per);
+    if (lanes > 0)
+        token<T, V>(a, lanes, per, back, s);
+    else
+        sample<T, V>(a, back, s);
+}
+
+// Vectors need rows that are whole vectors; the token form whole groups too.
+bool use_vectors(const Args& a, int V, bool rows_aligned) {
+    if (!rows_aligned || a.C % V) return false;
+    if (a.S == 1 && a.D % V) {
+        // groups that are no whole vectors: element by element in the token
+        // form (one pass) unless they are too wide for it
+        int lanes, per;
+        token_shape(a.D, 1, lanes, per);
+        return lanes == 0;
     }
-    if (a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
+    return true;
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -753,22 +846,25 @@ int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
 
 int vec_of(int dtype) { return dtype == FFTCONV_F32 ? 4 : 8; }
 
-// The token form serves both vector widths by the same rule; its width
-// depends on alignment, so the workspace is sized for either form.
+// Sized for either vector width (which depends on strides): the token form's
+// partial sums are at most kTokenBlocks x kThreads rows, and kThreads more than x has.
 size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool bwd) {
     if (N == 0 || S == 0 || C == 0) return 0;
+    const bool token = S == 1 && C / G <= 256;                // whatever the width
     const int64_t chunks = chunks_of(N, S, C);
-    // (groups of up to 256 channels of one position take the token form whatever their alignment)
-    if (!bwd && S == 1 && C / G <= 256) return 0;
     if (!bwd) {
+        if (token) return 0;
         // parts of the statistics, and mean and rstd when the caller keeps none
         return (size_t)(pad256(N * G * chunks * ((C + kThreads - 1) / kThreads) * 16) + 2 * pad256(N * G * 4));
     }
-    int64_t parts = N * chunks;
-    if (S == 1 && parts > kTokenBlocks * kThreads) parts = N;
-    const int64_t token = S == 1 ? (N < kTokenBlocks * kThreads ? N + kThreads : kTokenBlocks * kThreads) : 0;
-    if (token > parts) parts = token;
-    return (size_t)(pad256(parts * 2 * C * 4) + pad256(N * G * 8));
+    int64_t parts = 0;
+    if (!token) parts = N * chunks;
+    if (S == 1) {
+        // (row blocks x row sub-warps, the last of them beyond the rows)
+        const int64_t most = N + kThreads < kTokenBlocks * kThreads ? N + kThreads : kTokenBlocks * kThreads;
+        if (most > parts) parts = most;
+    }
+    return (size_t)(pad256(parts * 2 * C * 4) + (token ? 0 : pad256(N * G * 8)));
 }
 
 int check(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int wdtype, int act, bool affine) {
@@ -846,13 +942,10 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
     a.eps = eps;
     a.chunks = (int)chunks_of(N, S, C);
     const int V = vec_of(dtype);
-    const bool vec = a.D % V == 0 && (rows == 1 || ld_x % V == 0) && (!gate || rows == 1 || ld_gate % V == 0);
-    int lanes = 0, per = 0;
-    token_shape(a.D / (vec ? V : 1), lanes, per);
-    const bool token = S == 1 && lanes > 0;
+    const bool vec = use_vectors(a, V, rows == 1 || (ld_x % V == 0 && (!gate || ld_gate % V == 0)));
     a.mean = mean;
     a.rstd = rstd;
-    if (!token) {
+    if (need) {
         const int64_t parts = pad256(N * G * (int64_t)a.chunks * ((C + kThreads - 1) / kThreads) * 16);
         a.part = (float*)workspace;
         if (!mean) {
@@ -862,7 +955,7 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
     }
     dispatch(dtype, vec, [&](auto* t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
-        forward<T, decltype(v)::value>(a, token, lanes, per, (cudaStream_t)stream);
+        run<T, decltype(v)::value>(a, false, (cudaStream_t)stream);
     });
     const cudaError_t e = cudaPeekAtLastError();
     return e == cudaSuccess ? FFTCONV_OK
@@ -921,15 +1014,14 @@ int fftconv_group_norm_backward(const void* x, const void* gate, const void* wei
     a.act = act;
     a.chunks = (int)chunks_of(N, S, C);
     const int V = vec_of(dtype);
-    const bool vec = a.D % V == 0 && (rows == 1 || (ld_x % V == 0 && ld_dy % V == 0 && (!gate || ld_gate % V == 0)));
-    int lanes = 0, per = 0;
-    token_shape(a.D / (vec ? V : 1), lanes, per);
-    const bool token = S == 1 && lanes > 0;
+    const bool vec =
+        use_vectors(a, V, rows == 1 || (ld_x % V == 0 && ld_dy % V == 0 && (!gate || ld_gate % V == 0)));
+    const int64_t sums = S == 1 && C / G <= 256 ? 0 : pad256(N * G * 8);
     a.sums = (float*)workspace;
-    a.part = (float*)((uint8_t*)workspace + pad256(N * G * 8));
+    a.part = (float*)((uint8_t*)workspace + sums);
     dispatch(dtype, vec, [&](auto* t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
-        backward<T, decltype(v)::value>(a, token, lanes, per, s);
+        run<T, decltype(v)::value>(a, true, s);
     });
     const cudaError_t e = cudaPeekAtLastError();
     return e == cudaSuccess ? FFTCONV_OK
