@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <string>
+#include <type_traits>
 
 #include "../../include/fftconv.h"
 #include "internal.h"
@@ -45,52 +46,82 @@ struct Args {
 };
 
 template <typename T>
-struct Type;
-template <>
-struct Type<float> {
-    static __device__ __forceinline__ float get(float x) { return x; }
-    static __device__ __forceinline__ float put(float x) { return x; }
-};
-template <>
-struct Type<__half> {
-    static __device__ __forceinline__ float get(__half x) { return __half2float(x); }
-    static __device__ __forceinline__ __half put(float x) { return __float2half_rn(x); }
-};
-template <>
-struct Type<__nv_bfloat16> {
-    static __device__ __forceinline__ float get(__nv_bfloat16 x) { return __bfloat162float(x); }
-    static __device__ __forceinline__ __nv_bfloat16 put(float x) { return __float2bfloat16_rn(x); }
-};
+__device__ __forceinline__ float get(T x) {
+    if constexpr (std::is_same_v<T, float>) return x;
+    else if constexpr (std::is_same_v<T, __half>) return __half2float(x);
+    else return __bfloat162float(x);
+}
+template <typename T>
+__device__ __forceinline__ T put(float x) {
+    if constexpr (std::is_same_v<T, float>) return x;
+    else if constexpr (std::is_same_v<T, __half>) return __float2half_rn(x);
+    else return __float2bfloat16_rn(x);
+}
 
-// V elements: one 16-byte vector, or one element.
+// V elements: one 16-byte vector, as the words it is loaded in, or one element.
 template <typename T, int V>
-struct alignas(V * sizeof(T)) Pack {
-    T e[V];
+struct Pack {
+    uint32_t w[V == 1 ? 1 : 4];
 };
 template <typename T, int V>
 __device__ __forceinline__ Pack<T, V> load(const void* p, int64_t at) {
     Pack<T, V> r;
-    if constexpr (V == 1) {
-        r.e[0] = reinterpret_cast<const T*>(p)[at];
+    if constexpr (V > 1) {
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p) + at);
+        r.w[0] = v.x;
+        r.w[1] = v.y;
+        r.w[2] = v.z;
+        r.w[3] = v.w;
+    } else if constexpr (sizeof(T) == 4) {
+        r.w[0] = reinterpret_cast<const uint32_t*>(p)[at];
     } else {
-        *reinterpret_cast<uint4*>(&r) = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p) + at);
+        r.w[0] = reinterpret_cast<const uint16_t*>(p)[at];
     }
     return r;
 }
-template <typename T, int V>
-__device__ __forceinline__ void store(void* p, int64_t at, const float (&f)[V]) {
-    Pack<T, V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.e[i] = Type<T>::put(f[i]);
-    if constexpr (V == 1)
-        reinterpret_cast<T*>(p)[at] = r.e[0];
-    else
-        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p) + at) = *reinterpret_cast<const uint4*>(&r);
+template <typename T>
+__device__ __forceinline__ float2 two_of(uint32_t w) {
+    if constexpr (std::is_same_v<T, __half>) {
+        __half2 h;
+        *reinterpret_cast<uint32_t*>(&h) = w;
+        return __half22float2(h);
+    } else {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
 }
 template <typename T, int V>
 __device__ __forceinline__ void unpack(const Pack<T, V>& p, float (&f)[V]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = Type<T>::get(p.e[i]);
+        for (int i = 0; i < V; ++i) f[i] = __uint_as_float(p.w[i]);
+    } else if constexpr (V == 1) {
+        f[0] = two_of<T>(p.w[0]).x;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 v = two_of<T>(p.w[i]);
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+        }
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store(void* p, int64_t at, const float (&f)[V]) {
+    if constexpr (V == 1) {
+        reinterpret_cast<T*>(p)[at] = put<T>(f[0]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4)
+                w[i] = __float_as_uint(f[i]);
+            else if constexpr (std::is_same_v<T, __half>)
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+            else
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
+        }
+        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 // weight or bias of channels c .. c + V (in x's type or fp32)
 template <typename T, int V>
@@ -190,8 +221,8 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // rows of a sub-warp are in flight together.
 
 template <typename T, int V, int I, int LANES>
-__global__ void __launch_bounds__(kThreads) gn_token_forward(const Args a, int gsubs, int rsubs) {
-    constexpr int U = I == 1 ? 4 : I == 2 ? 2 : 1;
+__global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(const Args a, int gsubs, int rsubs) {
+    constexpr int U = I == 1 ? 2 : 1;
     constexpr bool kKeep = I * V <= 16;                       // weights stay in registers
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     const int g = blockIdx.y * gsubs + sub % gsubs, rs = sub / gsubs;
@@ -208,19 +239,31 @@ __global__ void __launch_bounds__(kThreads) gn_token_forward(const Args a, int g
                 load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, b[i]);
             }
     }
-    // (the same trip count for a whole block: all lanes take part in the sums)
-    for (int64_t base = (int64_t)blockIdx.x * rsubs * U; base < a.N; base += (int64_t)gridDim.x * rsubs * U) {
-        Pack<T, V> x[U][I], gt[U][I];
+    Pack<T, V> x[U][I], gt[U][I], nx[U][I], ng[U][I];
+    auto fetch = [&](int64_t base) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = base + u * rsubs + rs;
 #pragma unroll
             for (int i = 0; i < I; ++i)
                 if (on && r < a.N && lane + i * LANES < nvec) {
-                    x[u][i] = load<T, V>(a.x, r * a.ldx + c + i * LANES * V);
-                    if (gated) gt[u][i] = load<T, V>(a.gate, r * a.ldg + c + i * LANES * V);
+                    nx[u][i] = load<T, V>(a.x, r * a.ldx + c + i * LANES * V);
+                    if (gated) ng[u][i] = load<T, V>(a.gate, r * a.ldg + c + i * LANES * V);
                 }
         }
+    };
+    const int64_t stride = (int64_t)gridDim.x * rsubs * U;
+    fetch((int64_t)blockIdx.x * rsubs * U);
+    // (the same trip count for a whole block: all lanes take part in the sums)
+    for (int64_t base = (int64_t)blockIdx.x * rsubs * U; base < a.N; base += stride) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                x[u][i] = nx[u][i];
+                gt[u][i] = ng[u][i];
+            }
+        fetch(base + stride);                                 // the next rows' loads are out during this one's work
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = base + u * rsubs + rs;
@@ -272,8 +315,7 @@ __global__ void __launch_bounds__(kThreads) gn_token_forward(const Args a, int g
 }
 
 template <typename T, int V, int I, int LANES>
-__global__ void __launch_bounds__(kThreads) gn_token_backward(const Args a, int gsubs, int rsubs) {
-    constexpr int U = I * V <= 8 ? 2 : 1;
+__global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward(const Args a, int gsubs, int rsubs) {
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     const int g = blockIdx.y * gsubs + sub % gsubs, rs = sub / gsubs;
     const bool on = g < a.G && rs < rsubs;
@@ -291,63 +333,65 @@ __global__ void __launch_bounds__(kThreads) gn_token_backward(const Args a, int 
             load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, w[i]);
             load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, b[i]);
         }
-    for (int64_t base = (int64_t)blockIdx.x * rsubs * U; base < a.N; base += (int64_t)gridDim.x * rsubs * U) {
-        float mean[U], rstd[U];
-        Pack<T, V> px[U][I], pd[U][I], pg[U][I];
+    float mean = 0.f, rstd = 0.f;
+    Pack<T, V> px[I], pd[I], pg[I];
+    auto fetch = [&](int64_t r) {
+        if (on && r < a.N) {
+            mean = a.mean[r * a.G + g];
+            rstd = a.rstd[r * a.G + g];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = base + u * rsubs + rs;
-            if (on && r < a.N) {
-                mean[u] = a.mean[r * a.G + g];
-                rstd[u] = a.rstd[r * a.G + g];
-#pragma unroll
-                for (int i = 0; i < I; ++i)
-                    if (lane + i * LANES < nvec) {
-                        const int at = c + i * LANES * V;
-                        px[u][i] = load<T, V>(a.x, r * a.ldx + at);
-                        pd[u][i] = load<T, V>(a.dy, r * a.ldy + at);
-                        if (gated) pg[u][i] = load<T, V>(a.gate, r * a.ldg + at);
-                    }
-            }
+            for (int i = 0; i < I; ++i)
+                if (lane + i * LANES < nvec) {
+                    const int at = c + i * LANES * V;
+                    px[i] = load<T, V>(a.x, r * a.ldx + at);
+                    pd[i] = load<T, V>(a.dy, r * a.ldy + at);
+                    if (gated) pg[i] = load<T, V>(a.gate, r * a.ldg + at);
+                }
         }
+    };
+    const int64_t stride = (int64_t)gridDim.x * rsubs;
+    fetch((int64_t)blockIdx.x * rsubs + rs);
+    for (int64_t base = (int64_t)blockIdx.x * rsubs; base < a.N; base += stride) {
+        const int64_t r = base + rs;
+        const bool in = on && r < a.N;
+        const float scale = rstd;
+        float xh[I][V], dn[I][V], gt[I][V], s1 = 0.f, s2 = 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t r = base + u * rsubs + rs;
-            const bool in = on && r < a.N;
-            float xh[I][V], dn[I][V], s1 = 0.f, s2 = 0.f;
+        for (int i = 0; i < I; ++i)
+            if (in && lane + i * LANES < nvec) {
+                unpack<T, V>(px[i], xh[i]);
+                unpack<T, V>(pd[i], dn[i]);
+                if (gated) unpack<T, V>(pg[i], gt[i]);
 #pragma unroll
-            for (int i = 0; i < I; ++i) {
-                if (!in || lane + i * LANES >= nvec) continue;
-                float gt[V], n[V];
-                unpack<T, V>(px[u][i], xh[i]);
-                unpack<T, V>(pd[u][i], dn[i]);
-                if (gated) unpack<T, V>(pg[u][i], gt);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    xh[i][j] = (xh[i][j] - mean[u]) * rstd[u];
-                    n[j] = fmaf(xh[i][j], w[i][j], b[i][j]);
-                }
-                start<V>(n, dn[i], gt, gated, a.act);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    dw[i][j] = fmaf(dn[i][j], xh[i][j], dw[i][j]);
-                    db[i][j] += dn[i][j];
-                    dn[i][j] *= w[i][j];
-                    s1 += dn[i][j];
-                    s2 = fmaf(dn[i][j], xh[i][j], s2);
-                }
-                if (gated) store<T, V>(a.dgate, r * a.C + c + i * LANES * V, gt);
+                for (int j = 0; j < V; ++j) xh[i][j] = (xh[i][j] - mean) * rstd;
             }
-            s1 = lanes_sum<LANES>(s1) * inv;
-            s2 = lanes_sum<LANES>(s2) * inv;
-            if (!in) continue;
+        fetch(r + stride);                                    // the next row's loads are out during this one's work
 #pragma unroll
-            for (int i = 0; i < I; ++i) {
-                if (lane + i * LANES >= nvec) continue;
+        for (int i = 0; i < I; ++i) {
+            if (!in || lane + i * LANES >= nvec) continue;
+            float n[V];
 #pragma unroll
-                for (int j = 0; j < V; ++j) dn[i][j] = rstd[u] * (dn[i][j] - s1 - xh[i][j] * s2);
-                store<T, V>(a.dx, r * a.C + c + i * LANES * V, dn[i]);
+            for (int j = 0; j < V; ++j) n[j] = fmaf(xh[i][j], w[i][j], b[i][j]);
+            start<V>(n, dn[i], gt[i], gated, a.act);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                dw[i][j] = fmaf(dn[i][j], xh[i][j], dw[i][j]);
+                db[i][j] += dn[i][j];
+                dn[i][j] *= w[i][j];
+                s1 += dn[i][j];
+                s2 = fmaf(dn[i][j], xh[i][j], s2);
             }
+            if (gated) store<T, V>(a.dgate, r * a.C + c + i * LANES * V, gt[i]);
+        }
+        s1 = lanes_sum<LANES>(s1) * inv;
+        s2 = lanes_sum<LANES>(s2) * inv;
+        if (!in) continue;
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            if (lane + i * LANES >= nvec) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) dn[i][j] = scale * (dn[i][j] - s1 - xh[i][j] * s2);
+            store<T, V>(a.dx, r * a.C + c + i * LANES * V, dn[i]);
         }
     }
     if (!on || !a.dw) return;
@@ -418,7 +462,7 @@ __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, flo
 // Statistics of a block's part of every group: per channel first, from sums
 // over a few positions at a time.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_stats(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) gn_stats(const Args a) {
     __shared__ float sh_m[V * kThreads], sh_q[V * kThreads], sh_n[kThreads];      // [row lane][channel of the block]
     const Tile t = tile_of<V>(a, blockIdx.x);
     const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
@@ -437,23 +481,33 @@ __global__ void __launch_bounds__(kThreads) gn_stats(const Args a) {
                     p[k] = load<T, V>(a.x, (row0 + s + k * t.rows) * a.ldx + (int64_t)t.colv * V);
                     cnt += 1.f;
                 }
-            const float inv = 1.f / cnt, f = cnt / (n + cnt);
+            const float inv = 1.f / cnt, f = cnt / (n + cnt), nf = n * f;
+            float sum[V], sq[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] = sq[j] = 0.f;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (s + k * t.rows < t.s1) {
+                    float x[V];
+                    unpack<T, V>(p[k], x);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) sum[j] += x[j];
+                }
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] *= inv;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (s + k * t.rows < t.s1) {
+                    float x[V];
+                    unpack<T, V>(p[k], x);
+#pragma unroll
+                    for (int j = 0; j < V; ++j) sq[j] = fmaf(x[j] - sum[j], x[j] - sum[j], sq[j]);
+                }
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float x[kAhead], sum = 0.f, sq = 0.f;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (s + k * t.rows < t.s1) {
-                        x[k] = Type<T>::get(p[k].e[j]);
-                        sum += x[k];
-                    }
-                const float mean = sum * inv;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (s + k * t.rows < t.s1) sq = fmaf(x[k] - mean, x[k] - mean, sq);
-                const float d = mean - m[j];
+                const float d = sum[j] - m[j];
                 m[j] = fmaf(d, f, m[j]);
-                q[j] += fmaf(d * d, n * f, sq);
+                q[j] += fmaf(d * d, nf, sq[j]);
             }
             n += cnt;
         }
@@ -514,28 +568,30 @@ __global__ void __launch_bounds__(kThreads) gn_join_stats(const Args a) {
     }
 }
 
-// mean, rstd, weight and bias of a thread's channels
-template <typename T, int V>
-__device__ __forceinline__ void channel_of(const Args& a, int n, int c, float (&mean)[V], float (&rstd)[V],
-                                           float (&w)[V], float (&b)[V]) {
-    load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
-    load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+// A statistic of a thread's channels: one value where the vector lies in one
+// group (WHOLE), else one a channel.
+template <int V, bool WHOLE>
+struct Stat {
+    float v[WHOLE ? 1 : V];
+    __device__ __forceinline__ float operator[](int j) const { return v[WHOLE ? 0 : j]; }
+    __device__ __forceinline__ void read(const float* p, int64_t row, int c, int D, int step) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int64_t p = (int64_t)n * a.G + (c + j) / a.D;
-        mean[j] = a.mean[p];
-        rstd[j] = a.rstd[p];
+        for (int j = 0; j < (WHOLE ? 1 : V); ++j) v[j] = p[(row + (c + j) / D) * step];
     }
-}
+};
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_apply(const Args a) {
+template <typename T, int V, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, 4) gn_apply(const Args a) {
     const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!t.on) return;
     const int c = t.colv * V;
     const int64_t row0 = (int64_t)t.n * a.S;
-    float mean[V], rstd[V], w[V], b[V];
-    channel_of<T, V>(a, t.n, c, mean, rstd, w, b);
+    float w[V], b[V];
+    load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
+    load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+    Stat<V, WHOLE> mean, rstd;
+    mean.read(a.mean, (int64_t)t.n * a.G, c, a.D, 1);
+    rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] *= rstd[j];
     constexpr int kAhead = 4;
@@ -564,9 +620,9 @@ __global__ void __launch_bounds__(kThreads) gn_apply(const Args a) {
 }
 
 // xh, dn and dgate of one vector
-template <typename T, int V>
+template <typename T, int V, bool WHOLE>
 __device__ __forceinline__ void grad_of(const Args& a, bool gated, const Pack<T, V>& px, const Pack<T, V>& pd,
-                                        const Pack<T, V>& pg, const float (&mean)[V], const float (&rstd)[V],
+                                        const Pack<T, V>& pg, const Stat<V, WHOLE>& mean, const Stat<V, WHOLE>& rstd,
                                         const float (&w)[V], const float (&b)[V], float (&xh)[V], float (&dn)[V],
                                         float (&dg)[V]) {
     float n[V];
@@ -583,8 +639,8 @@ __device__ __forceinline__ void grad_of(const Args& a, bool gated, const Pack<T,
 
 // First backward pass: the sums of dn xh and dn over the chunk's positions,
 // by channel: part[(sample, chunk)][2][C].
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_grad_sums(const Args a) {
+template <typename T, int V, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, 3) gn_grad_sums(const Args a) {
     __shared__ float sh[2][kThreads * V];
     const Tile t = tile_of<V>(a, blockIdx.x);
     const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
@@ -595,8 +651,12 @@ __global__ void __launch_bounds__(kThreads) gn_grad_sums(const Args a) {
     if (t.on) {
         const int64_t row0 = (int64_t)t.n * a.S;
         const bool gated = a.gate != nullptr;
-        float mean[V], rstd[V], w[V], b[V];
-        channel_of<T, V>(a, t.n, c, mean, rstd, w, b);
+        float w[V], b[V];
+        load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
+        load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+        Stat<V, WHOLE> mean, rstd;
+        mean.read(a.mean, (int64_t)t.n * a.G, c, a.D, 1);
+        rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
         constexpr int kAhead = 2;
         for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
             Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
@@ -612,7 +672,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_sums(const Args a) {
             for (int k = 0; k < kAhead; ++k)
                 if (s + k * t.rows < t.s1) {
                     float xh[V], dn[V], dg[V];
-                    grad_of<T, V>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
+                    grad_of<T, V, WHOLE>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         s1[j] = fmaf(dn[j], xh[j], s1[j]);
@@ -675,21 +735,21 @@ __global__ void __launch_bounds__(kThreads) gn_join_sums(const Args a) {
     }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gn_grad_apply(const Args a) {
+template <typename T, int V, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, 3) gn_grad_apply(const Args a) {
     const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!t.on) return;
     const int c = t.colv * V;
     const int64_t row0 = (int64_t)t.n * a.S;
     const bool gated = a.gate != nullptr;
-    float mean[V], rstd[V], w[V], b[V], m1[V], m2[V];
-    channel_of<T, V>(a, t.n, c, mean, rstd, w, b);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int64_t p = (int64_t)t.n * a.G + (c + j) / a.D;
-        m1[j] = a.sums[2 * p];
-        m2[j] = a.sums[2 * p + 1];
-    }
+    float w[V], b[V];
+    load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
+    load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
+    Stat<V, WHOLE> mean, rstd, m1, m2;
+    mean.read(a.mean, (int64_t)t.n * a.G, c, a.D, 1);
+    rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
+    m1.read(a.sums, (int64_t)t.n * a.G, c, a.D, 2);
+    m2.read(a.sums + 1, (int64_t)t.n * a.G, c, a.D, 2);
     constexpr int kAhead = 2;
     for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
         Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
@@ -706,7 +766,7 @@ __global__ void __launch_bounds__(kThreads) gn_grad_apply(const Args a) {
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
                 float xh[V], dn[V], dg[V];
-                grad_of<T, V>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
+                grad_of<T, V, WHOLE>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
                 if (gated) store<T, V>(a.dgate, r * a.C + c, dg);
 #pragma unroll
                 for (int j = 0; j < V; ++j) dn[j] = rstd[j] * (dn[j] * w[j] - m1[j] - xh[j] * m2[j]);
@@ -722,12 +782,12 @@ int fail(int status, const std::string& msg) {
     return status;
 }
 
-constexpr int64_t kTokenBlocks = 148 * 4;     // row blocks of the token form at most: they walk
+constexpr int64_t kTokenBlocks = 148 * 3;     // blocks of the token form at most, all resident: they walk down the rows
 
-// Samples are cut so that the blocks fill the GPU a few times over, but no
-// finer than 16384 values.
+// Samples are cut so that all blocks are resident at once where there are few
+// samples (3 blocks an SM at least), but no finer than 16384 values.
 int64_t chunks_of(int64_t N, int64_t S, int64_t C) {
-    int64_t want = (148 * 8 + N - 1) / N;
+    int64_t want = N > 0 && N < 148 * 3 ? 148 * 3 / N : 1;
     const int64_t most = S * C / 16384 > 1 ? S * C / 16384 : 1;
     if (want > most) want = most;
     return want > S ? S : want;
@@ -773,11 +833,11 @@ void token_launch(const Args& a, const TokenGrid& t, bool back, cudaStream_t s) 
 }
 
 // (the rows that a sub-warp has in flight, as the kernels choose them)
-int rows_at_once(int per, int V, bool back) { return back ? (per * V <= 8 ? 2 : 1) : per == 1 ? 4 : per == 2 ? 2 : 1; }
+int rows_at_once(int per, bool back) { return !back && per == 1 ? 2 : 1; }
 
 template <typename T, int V>
 void token(Args a, int lanes, int per, bool back, cudaStream_t s) {
-    const TokenGrid t = token_grid(a.N, a.G, lanes, rows_at_once(per, V, back));
+    const TokenGrid t = token_grid(a.N, a.G, lanes, rows_at_once(per, back));
     a.parts = (int)t.gx * t.rsubs;
     if (per == 1) {
         switch (lanes) {
@@ -800,22 +860,30 @@ void token(Args a, int lanes, int per, bool back, cudaStream_t s) {
     if (back && a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
 }
 
-template <typename T, int V>
-void sample(Args a, bool back, cudaStream_t s) {
+template <typename T, int V, bool WHOLE>
+void sample_of(Args a, bool back, cudaStream_t s) {
     const unsigned cols = (unsigned)((a.C / V + kThreads - 1) / kThreads);
     const dim3 grid((unsigned)(a.N * a.chunks), cols);
     if (!back) {
         a.parts = (int)cols * a.chunks;
         gn_stats<T, V><<<grid, kThreads, 0, s>>>(a);
         gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
-        gn_apply<T, V><<<grid, kThreads, 0, s>>>(a);
+        gn_apply<T, V, WHOLE><<<grid, kThreads, 0, s>>>(a);
     } else {
         a.parts = (int)(a.N * a.chunks);
-        gn_grad_sums<T, V><<<grid, kThreads, 0, s>>>(a);
+        gn_grad_sums<T, V, WHOLE><<<grid, kThreads, 0, s>>>(a);
         gn_join_sums<T><<<(unsigned)(a.N * a.G), kThreads, 0, s>>>(a);
-        gn_grad_apply<T, V><<<grid, kThreads, 0, s>>>(a);
+        gn_grad_apply<T, V, WHOLE><<<grid, kThreads, 0, s>>>(a);
         if (a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
     }
+}
+
+template <typename T, int V>
+void sample(const Args& a, bool back, cudaStream_t s) {
+    if constexpr (V > 1) {
+        if (a.D % V) return sample_of<T, V, false>(a, back, s);
+    }
+    sample_of<T, V, true>(a, back, s);
 }
 
 template <typename T, int V>
