@@ -177,10 +177,10 @@ __device__ __forceinline__ void activate(float (&f)[V], float (&slope)[V], int a
     }
 }
 // y of n (in place): act(n), or n act(gate)
-template <int V>
-__device__ __forceinline__ void finish(float (&n)[V], float (&gate)[V], bool gated, int act) {
+template <int V, bool GATED>
+__device__ __forceinline__ void finish(float (&n)[V], float (&gate)[V], int act) {
     float none[V];
-    if (gated) {
+    if constexpr (GATED) {
         activate<V, false>(gate, none, act);
 #pragma unroll
         for (int j = 0; j < V; ++j) n[j] *= gate[j];
@@ -189,10 +189,10 @@ __device__ __forceinline__ void finish(float (&n)[V], float (&gate)[V], bool gat
     }
 }
 // dn of dy (in place), and dgate of the gate (in place)
-template <int V>
-__device__ __forceinline__ void start(float (&n)[V], float (&dy)[V], float (&gate)[V], bool gated, int act) {
+template <int V, bool GATED>
+__device__ __forceinline__ void start(float (&n)[V], float (&dy)[V], float (&gate)[V], int act) {
     float slope[V];
-    if (gated) {
+    if constexpr (GATED) {
         activate<V, true>(gate, slope, act);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -220,7 +220,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // gsubs x rsubs sub-warps (groups x rows), grid (row blocks, group blocks); U
 // rows of a sub-warp are in flight together.
 
-template <typename T, int V, int I, int LANES>
+template <typename T, int V, int I, int LANES, bool GATED>
 __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(const Args a, int gsubs, int rsubs) {
     constexpr int U = I == 1 ? 2 : 1;
     constexpr bool kKeep = I * V <= 16;                       // weights stay in registers
@@ -229,7 +229,6 @@ __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(con
     const bool on = g < a.G && rs < rsubs;
     const int nvec = a.D / V, c = g * a.D + lane * V;
     const float inv = 1.f / (float)a.D;
-    const bool gated = a.gate != nullptr;
     float w[kKeep ? I : 1][V], b[kKeep ? I : 1][V];
     if constexpr (kKeep) {
 #pragma unroll
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(con
             for (int i = 0; i < I; ++i)
                 if (on && r < a.N && lane + i * LANES < nvec) {
                     nx[u][i] = load<T, V>(a.x, r * a.ldx + c + i * LANES * V);
-                    if (gated) ng[u][i] = load<T, V>(a.gate, r * a.ldg + c + i * LANES * V);
+                    if constexpr (GATED) ng[u][i] = load<T, V>(a.gate, r * a.ldg + c + i * LANES * V);
                 }
         }
     };
@@ -296,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(con
             for (int i = 0; i < I; ++i) {
                 if (lane + i * LANES >= nvec) continue;
                 float gate[V];
-                if (gated) unpack<T, V>(gt[u][i], gate);
+                if constexpr (GATED) unpack<T, V>(gt[u][i], gate);
                 if constexpr (kKeep) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
@@ -307,32 +306,61 @@ __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(con
 #pragma unroll
                     for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * rstd, wi[j], bi[j]);
                 }
-                finish<V>(f[i], gate, gated, a.act);
+                finish<V, GATED>(f[i], gate, a.act);
                 store<T, V>(a.y, r * a.C + c + i * LANES * V, f[i]);
             }
         }
     }
 }
 
-template <typename T, int V, int I, int LANES>
+template <typename T, int V, int I, int LANES, bool GATED>
 __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward(const Args a, int gsubs, int rsubs) {
     const int sub = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     const int g = blockIdx.y * gsubs + sub % gsubs, rs = sub / gsubs;
     const bool on = g < a.G && rs < rsubs;
     const int nvec = a.D / V, c = g * a.D + lane * V;
     const float inv = 1.f / (float)a.D;
-    const bool gated = a.gate != nullptr;
-    float dw[I][V], db[I][V], w[I][V], b[I][V];
+    // a lane's own weights: in shared memory where they would crowd out the
+    // registers of a third block (vectors of 8)
+    constexpr bool kShared = I * V >= 8;
+    __shared__ float4 shw[kShared ? I * V / 4 : 1][kThreads], shb[kShared ? I * V / 4 : 1][kThreads];
+    float dw[I][V], db[I][V], w[kShared ? 1 : I][V], b[kShared ? 1 : I][V];
 #pragma unroll
-    for (int i = 0; i < I; ++i)
+    for (int i = 0; i < I; ++i) {
+        float wi[V], bi[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = w[i][j] = b[i][j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < I; ++i)
+        for (int j = 0; j < V; ++j) dw[i][j] = db[i][j] = wi[j] = bi[j] = 0.f;
         if (on && lane + i * LANES < nvec) {
-            load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, w[i]);
-            load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, b[i]);
+            load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, wi);
+            load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, bi);
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if constexpr (kShared) {
+                reinterpret_cast<float*>(&shw[(i * V + j) / 4][threadIdx.x])[(i * V + j) % 4] = wi[j];
+                reinterpret_cast<float*>(&shb[(i * V + j) / 4][threadIdx.x])[(i * V + j) % 4] = bi[j];
+            } else {
+                w[i][j] = wi[j];
+                b[i][j] = bi[j];
+            }
+        }
+    }
+    auto own = [&](const float4 (*sh)[kThreads], int i, float (&f)[V]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if constexpr (V % 4 == 0) {
+                if (j % 4 == 0) {
+                    const float4 v = sh[(i * V + j) / 4][threadIdx.x];
+                    f[j] = v.x;
+                    f[j + 1] = v.y;
+                    f[j + 2] = v.z;
+                    f[j + 3] = v.w;
+                }
+            } else {
+                f[j] = reinterpret_cast<const float*>(&sh[(i * V + j) / 4][threadIdx.x])[(i * V + j) % 4];
+            }
+        }
+    };
     float mean = 0.f, rstd = 0.f;
     Pack<T, V> px[I], pd[I], pg[I];
     auto fetch = [&](int64_t r) {
@@ -345,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
                     const int at = c + i * LANES * V;
                     px[i] = load<T, V>(a.x, r * a.ldx + at);
                     pd[i] = load<T, V>(a.dy, r * a.ldy + at);
-                    if (gated) pg[i] = load<T, V>(a.gate, r * a.ldg + at);
+                    if constexpr (GATED) pg[i] = load<T, V>(a.gate, r * a.ldg + at);
                 }
         }
     };
@@ -361,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
             if (in && lane + i * LANES < nvec) {
                 unpack<T, V>(px[i], xh[i]);
                 unpack<T, V>(pd[i], dn[i]);
-                if (gated) unpack<T, V>(pg[i], gt[i]);
+                if constexpr (GATED) unpack<T, V>(pg[i], gt[i]);
 #pragma unroll
                 for (int j = 0; j < V; ++j) xh[i][j] = (xh[i][j] - mean) * rstd;
             }
@@ -369,19 +397,29 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             if (!in || lane + i * LANES >= nvec) continue;
-            float n[V];
+            float n[V], wi[V], bi[V];
+            if constexpr (kShared) {
+                own(shw, i, wi);
+                own(shb, i, bi);
+            } else {
 #pragma unroll
-            for (int j = 0; j < V; ++j) n[j] = fmaf(xh[i][j], w[i][j], b[i][j]);
-            start<V>(n, dn[i], gt[i], gated, a.act);
+                for (int j = 0; j < V; ++j) {
+                    wi[j] = w[i][j];
+                    bi[j] = b[i][j];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) n[j] = fmaf(xh[i][j], wi[j], bi[j]);
+            start<V, GATED>(n, dn[i], gt[i], a.act);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 dw[i][j] = fmaf(dn[i][j], xh[i][j], dw[i][j]);
                 db[i][j] += dn[i][j];
-                dn[i][j] *= w[i][j];
+                dn[i][j] *= wi[j];
                 s1 += dn[i][j];
                 s2 = fmaf(dn[i][j], xh[i][j], s2);
             }
-            if (gated) store<T, V>(a.dgate, r * a.C + c + i * LANES * V, gt[i]);
+            if constexpr (GATED) store<T, V>(a.dgate, r * a.C + c + i * LANES * V, gt[i]);
         }
         s1 = lanes_sum<LANES>(s1) * inv;
         s2 = lanes_sum<LANES>(s2) * inv;
@@ -580,8 +618,8 @@ struct Stat {
     }
 };
 
-template <typename T, int V, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 4) gn_apply(const Args a) {
+template <typename T, int V, bool WHOLE, bool GATED>
+__global__ void __launch_bounds__(kThreads, 3) gn_apply(const Args a) {
     const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!t.on) return;
     const int c = t.colv * V;
@@ -594,8 +632,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_apply(const Args a) {
     rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] *= rstd[j];
-    constexpr int kAhead = 4;
-    const bool gated = a.gate != nullptr;
+    constexpr int kAhead = GATED ? 2 : 4;
     for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
         Pack<T, V> px[kAhead], pg[kAhead];
 #pragma unroll
@@ -603,44 +640,44 @@ __global__ void __launch_bounds__(kThreads, 4) gn_apply(const Args a) {
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
                 px[k] = load<T, V>(a.x, r * a.ldx + c);
-                if (gated) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                if constexpr (GATED) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
                 float f[V], g[V];
                 unpack<T, V>(px[k], f);
-                if (gated) unpack<T, V>(pg[k], g);
+                if constexpr (GATED) unpack<T, V>(pg[k], g);
 #pragma unroll
                 for (int j = 0; j < V; ++j) f[j] = fmaf(f[j] - mean[j], w[j], b[j]);
-                finish<V>(f, g, gated, a.act);
+                finish<V, GATED>(f, g, a.act);
                 store<T, V>(a.y, (row0 + s + k * t.rows) * a.C + c, f);
             }
     }
 }
 
 // xh, dn and dgate of one vector
-template <typename T, int V, bool WHOLE>
-__device__ __forceinline__ void grad_of(const Args& a, bool gated, const Pack<T, V>& px, const Pack<T, V>& pd,
+template <typename T, int V, bool WHOLE, bool GATED>
+__device__ __forceinline__ void grad_of(const Args& a, const Pack<T, V>& px, const Pack<T, V>& pd,
                                         const Pack<T, V>& pg, const Stat<V, WHOLE>& mean, const Stat<V, WHOLE>& rstd,
                                         const float (&w)[V], const float (&b)[V], float (&xh)[V], float (&dn)[V],
                                         float (&dg)[V]) {
     float n[V];
     unpack<T, V>(px, xh);
     unpack<T, V>(pd, dn);
-    if (gated) unpack<T, V>(pg, dg);
+    if constexpr (GATED) unpack<T, V>(pg, dg);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         xh[j] = (xh[j] - mean[j]) * rstd[j];
         n[j] = fmaf(xh[j], w[j], b[j]);
     }
-    start<V>(n, dn, dg, gated, a.act);
+    start<V, GATED>(n, dn, dg, a.act);
 }
 
 // First backward pass: the sums of dn xh and dn over the chunk's positions,
 // by channel: part[(sample, chunk)][2][C].
-template <typename T, int V, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 3) gn_grad_sums(const Args a) {
+template <typename T, int V, bool WHOLE, bool GATED>
+__global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_sums(const Args a) {
     __shared__ float sh[2][kThreads * V];
     const Tile t = tile_of<V>(a, blockIdx.x);
     const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
@@ -650,8 +687,7 @@ __global__ void __launch_bounds__(kThreads, 3) gn_grad_sums(const Args a) {
     const int c = t.colv * V;
     if (t.on) {
         const int64_t row0 = (int64_t)t.n * a.S;
-        const bool gated = a.gate != nullptr;
-        float w[V], b[V];
+            float w[V], b[V];
         load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
         load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
         Stat<V, WHOLE> mean, rstd;
@@ -666,13 +702,13 @@ __global__ void __launch_bounds__(kThreads, 3) gn_grad_sums(const Args a) {
                     const int64_t r = row0 + s + k * t.rows;
                     px[k] = load<T, V>(a.x, r * a.ldx + c);
                     pd[k] = load<T, V>(a.dy, r * a.ldy + c);
-                    if (gated) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                    if constexpr (GATED) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
                 }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (s + k * t.rows < t.s1) {
                     float xh[V], dn[V], dg[V];
-                    grad_of<T, V, WHOLE>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
+                    grad_of<T, V, WHOLE, GATED>(a, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         s1[j] = fmaf(dn[j], xh[j], s1[j]);
@@ -735,13 +771,12 @@ __global__ void __launch_bounds__(kThreads) gn_join_sums(const Args a) {
     }
 }
 
-template <typename T, int V, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, 3) gn_grad_apply(const Args a) {
+template <typename T, int V, bool WHOLE, bool GATED>
+__global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_apply(const Args a) {
     const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
     if (!t.on) return;
     const int c = t.colv * V;
     const int64_t row0 = (int64_t)t.n * a.S;
-    const bool gated = a.gate != nullptr;
     float w[V], b[V];
     load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
     load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
@@ -759,15 +794,15 @@ __global__ void __launch_bounds__(kThreads, 3) gn_grad_apply(const Args a) {
                 const int64_t r = row0 + s + k * t.rows;
                 px[k] = load<T, V>(a.x, r * a.ldx + c);
                 pd[k] = load<T, V>(a.dy, r * a.ldy + c);
-                if (gated) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                if constexpr (GATED) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
                 float xh[V], dn[V], dg[V];
-                grad_of<T, V, WHOLE>(a, gated, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
-                if (gated) store<T, V>(a.dgate, r * a.C + c, dg);
+                grad_of<T, V, WHOLE, GATED>(a, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
+                if constexpr (GATED) store<T, V>(a.dgate, r * a.C + c, dg);
 #pragma unroll
                 for (int j = 0; j < V; ++j) dn[j] = rstd[j] * (dn[j] * w[j] - m1[j] - xh[j] * m2[j]);
                 store<T, V>(a.dx, r * a.C + c, dn);
@@ -827,9 +862,11 @@ template <typename T, int V, int I, int LANES>
 void token_launch(const Args& a, const TokenGrid& t, bool back, cudaStream_t s) {
     const dim3 grid(t.gx, t.gy);
     if (back)
-        gn_token_backward<T, V, I, LANES><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
+        a.gate ? gn_token_backward<T, V, I, LANES, true><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs)
+               : gn_token_backward<T, V, I, LANES, false><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
     else
-        gn_token_forward<T, V, I, LANES><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
+        a.gate ? gn_token_forward<T, V, I, LANES, true><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs)
+               : gn_token_forward<T, V, I, LANES, false><<<grid, t.threads, 0, s>>>(a, t.gsubs, t.rsubs);
 }
 
 // (the rows that a sub-warp has in flight, as the kernels choose them)
@@ -860,7 +897,7 @@ void token(Args a, int lanes, int per, bool back, cudaStream_t s) {
     if (back && a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
 }
 
-template <typename T, int V, bool WHOLE>
+template <typename T, int V, bool WHOLE, bool GATED>
 void sample_of(Args a, bool back, cudaStream_t s) {
     const unsigned cols = (unsigned)((a.C / V + kThreads - 1) / kThreads);
     const dim3 grid((unsigned)(a.N * a.chunks), cols);
@@ -868,12 +905,12 @@ void sample_of(Args a, bool back, cudaStream_t s) {
         a.parts = (int)cols * a.chunks;
         gn_stats<T, V><<<grid, kThreads, 0, s>>>(a);
         gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
-        gn_apply<T, V, WHOLE><<<grid, kThreads, 0, s>>>(a);
+        gn_apply<T, V, WHOLE, GATED><<<grid, kThreads, 0, s>>>(a);
     } else {
         a.parts = (int)(a.N * a.chunks);
-        gn_grad_sums<T, V, WHOLE><<<grid, kThreads, 0, s>>>(a);
+        gn_grad_sums<T, V, WHOLE, GATED><<<grid, kThreads, 0, s>>>(a);
         gn_join_sums<T><<<(unsigned)(a.N * a.G), kThreads, 0, s>>>(a);
-        gn_grad_apply<T, V, WHOLE><<<grid, kThreads, 0, s>>>(a);
+        gn_grad_apply<T, V, WHOLE, GATED><<<grid, kThreads, 0, s>>>(a);
         if (a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
     }
 }
@@ -881,9 +918,9 @@ void sample_of(Args a, bool back, cudaStream_t s) {
 template <typename T, int V>
 void sample(const Args& a, bool back, cudaStream_t s) {
     if constexpr (V > 1) {
-        if (a.D % V) return sample_of<T, V, false>(a, back, s);
+        if (a.D % V) return a.gate ? sample_of<T, V, false, true>(a, back, s) : sample_of<T, V, false, false>(a, back, s);
     }
-    sample_of<T, V, true>(a, back, s);
+    a.gate ? sample_of<T, V, true, true>(a, back, s) : sample_of<T, V, true, false>(a, back, s);
 }
 
 template <typename T, int V>
