@@ -444,22 +444,24 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
             }
 }
 
-// dw and db: the sum of `parts` rows of (dw[C], db[C]), in a fixed order.
-__global__ void __launch_bounds__(1024) gn_sum_parts(const Args a) {
+// dw and db: the sum of `parts` rows of (dw[C], db[C]) for 32 of the 2 C
+// columns, in a fixed order, by 1024 threads.
+__device__ __forceinline__ void sum_parts(const Args& a, int block) {
     __shared__ float sh[32][33];
-    const int col = blockIdx.x * 32 + threadIdx.x % 32, r0 = threadIdx.x / 32;
+    const int col = block * 32 + threadIdx.x % 32, r0 = threadIdx.x / 32;
     float s = 0.f;
     if (col < 2 * a.C) {
         const float* p = a.part + col;
-#pragma unroll 4
+#pragma unroll 8
         for (int r = r0; r < a.parts; r += 32) s += p[(int64_t)r * 2 * a.C];
     }
     sh[r0][threadIdx.x % 32] = s;
     __syncthreads();
     s = lanes_sum<32>(sh[threadIdx.x % 32][r0]);
-    const int c = blockIdx.x * 32 + r0;
+    const int c = block * 32 + r0;
     if (threadIdx.x % 32 == 0 && c < 2 * a.C) (c < a.C ? a.dw[c] : a.db[c - a.C]) = s;
 }
+__global__ void __launch_bounds__(1024) gn_sum_parts(const Args a) { sum_parts(a, blockIdx.x); }
 
 // ----------------------------------------------------------- sample form ---
 //
@@ -477,7 +479,7 @@ __device__ __forceinline__ Tile tile_of(const Args& a, int bx) {
     t.n = bx / a.chunks;
     t.chunk = bx % a.chunks;
     const int cv = a.C / V, width = min(cv - (int)blockIdx.y * kThreads, kThreads);
-    t.rows = kThreads / width;
+    t.rows = (int)blockDim.x / width;
     t.rl = threadIdx.x / width;
     t.colv = blockIdx.y * kThreads + threadIdx.x % width;
     t.on = t.rl < t.rows;
@@ -509,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats(const Args a) {
     for (int j = 0; j < V; ++j) m[j] = q[j] = 0.f;
     if (t.on) {
         const int64_t row0 = (int64_t)t.n * a.S;
-        constexpr int kAhead = V == 1 ? 8 : 4;
+        constexpr int kAhead = V == 8 ? 4 : 8;
         for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
             Pack<T, V> p[kAhead];
             float cnt = 0.f;
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats(const Args a) {
     // one warp a group: its channels in every row lane
     const int c0 = (int)blockIdx.y * kThreads * V, c1 = c0 + width * V;
     const int lane = threadIdx.x % 32;
-    for (int g = threadIdx.x / 32; g < a.G; g += kThreads / 32) {
+    for (int g = threadIdx.x / 32; g < a.G; g += (int)blockDim.x / 32) {
         float gn = 0.f, gm = 0.f, gq = 0.f;
         const int lo = max(g * a.D, c0) - c0, hi = min((g + 1) * a.D, c1) - c0;
         if (hi > lo) {
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_sums
     }
     __syncthreads();
     float* out = a.part + (int64_t)blockIdx.x * 2 * a.C + (int64_t)blockIdx.y * kThreads * V;
-    for (int e = threadIdx.x; e < width * V; e += kThreads) {
+    for (int e = threadIdx.x; e < width * V; e += (int)blockDim.x) {
         float x = 0.f, y = 0.f;
         for (int r = 0; r < t.rows; ++r) {
             x += sh[0][r * width * V + e];
@@ -735,16 +737,18 @@ __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_sums
     }
 }
 
-// One block a (sample, group): mean(dn w) and mean(dn w xh).
+// One block a (sample, group): mean(dn w) and mean(dn w xh); the blocks behind
+// them sum dw and db.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) gn_join_sums(const Args a) {
-    __shared__ float sh[2][kThreads / 32];
+__global__ void __launch_bounds__(1024) gn_join_sums(const Args a) {
+    if (blockIdx.x >= a.N * a.G) return sum_parts(a, (int)(blockIdx.x - a.N * a.G));
+    __shared__ float sh[2][32];
     const int64_t p = blockIdx.x, n = p / a.G;
     const int c0 = (int)(p % a.G) * a.D;
     float s1 = 0.f, s2 = 0.f;
     // (chunk, channel) in order of memory
 #pragma unroll 4
-    for (int e = threadIdx.x; e < a.D * a.chunks; e += kThreads) {
+    for (int e = threadIdx.x; e < a.D * a.chunks; e += (int)blockDim.x) {
         const int k = e / a.D, c = c0 + e % a.D;
         float w[1];
         load_w<T, 1>(a.w, a.w_f32, c, 1.f, w);
@@ -759,15 +763,15 @@ __global__ void __launch_bounds__(kThreads) gn_join_sums(const Args a) {
         sh[1][threadIdx.x / 32] = s2;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        s1 = s2 = 0.f;
-        for (int i = 0; i < kThreads / 32; ++i) {
-            s1 += sh[0][i];
-            s2 += sh[1][i];
+    if (threadIdx.x < 32) {
+        const bool in = threadIdx.x < blockDim.x / 32;
+        s1 = lanes_sum<32>(in ? sh[0][threadIdx.x] : 0.f);
+        s2 = lanes_sum<32>(in ? sh[1][threadIdx.x] : 0.f);
+        if (threadIdx.x == 0) {
+            const float inv = 1.f / ((float)a.S * (float)a.D);
+            a.sums[2 * p] = s2 * inv;
+            a.sums[2 * p + 1] = s1 * inv;
         }
-        const float inv = 1.f / ((float)a.S * (float)a.D);
-        a.sums[2 * p] = s2 * inv;
-        a.sums[2 * p + 1] = s1 * inv;
     }
 }
 
@@ -819,13 +823,30 @@ int fail(int status, const std::string& msg) {
 
 constexpr int64_t kTokenBlocks = 148 * 3;     // blocks of the token form at most, all resident: they walk down the rows
 
+// Threads of the sample form's blocks: whole rows of vector columns.
+int sample_threads(int64_t S, int64_t C, int V) {
+    const int64_t cv = C / V > 0 ? C / V : 1, width = cv < kThreads ? cv : kThreads;
+    int64_t rows = kThreads / width;
+    if (rows > S) rows = S;
+    return (int)((width * rows + 31) / 32 * 32);
+}
 // Samples are cut so that all blocks are resident at once where there are few
-// samples (3 blocks an SM at least), but no finer than 16384 values.
-int64_t chunks_of(int64_t N, int64_t S, int64_t C) {
-    int64_t want = N > 0 && N < 148 * 3 ? 148 * 3 / N : 1;
-    const int64_t most = S * C / 16384 > 1 ? S * C / 16384 : 1;
+// samples (768 threads an SM), but no finer than 16384 values.
+int64_t chunks_of(int64_t N, int64_t S, int64_t C, int V) {
+    const int64_t cols = (C / V + kThreads - 1) / kThreads > 0 ? (C / V + kThreads - 1) / kThreads : 1;
+    int64_t want = 148 * (768 / sample_threads(S, C, V)) / ((N > 0 ? N : 1) * cols);
+    const int64_t most = S * C / 16384;
     if (want > most) want = most;
-    return want > S ? S : want;
+    if (want > S) want = S;
+    return want > 1 ? want : 1;
+}
+int64_t most_chunks(int64_t N, int64_t S, int64_t C) {
+    int64_t m = 1;
+    for (int V : {1, 4, 8}) {
+        const int64_t k = chunks_of(N, S, C, V);
+        if (k > m) m = k;
+    }
+    return m;
 }
 
 // Lanes and vectors a lane of the token form for groups of nvec vectors of V
@@ -900,18 +921,23 @@ void token(Args a, int lanes, int per, bool back, cudaStream_t s) {
 template <typename T, int V, bool WHOLE, bool GATED>
 void sample_of(Args a, bool back, cudaStream_t s) {
     const unsigned cols = (unsigned)((a.C / V + kThreads - 1) / kThreads);
+    a.chunks = (int)chunks_of(a.N, a.S, a.C, V);
     const dim3 grid((unsigned)(a.N * a.chunks), cols);
+    const int threads = sample_threads(a.S, a.C, V);
     if (!back) {
         a.parts = (int)cols * a.chunks;
-        gn_stats<T, V><<<grid, kThreads, 0, s>>>(a);
+        gn_stats<T, V><<<grid, threads, 0, s>>>(a);
         gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
-        gn_apply<T, V, WHOLE, GATED><<<grid, kThreads, 0, s>>>(a);
+        gn_apply<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
     } else {
         a.parts = (int)(a.N * a.chunks);
-        gn_grad_sums<T, V, WHOLE, GATED><<<grid, kThreads, 0, s>>>(a);
-        gn_join_sums<T><<<(unsigned)(a.N * a.G), kThreads, 0, s>>>(a);
-        gn_grad_apply<T, V, WHOLE, GATED><<<grid, kThreads, 0, s>>>(a);
-        if (a.dw) gn_sum_parts<<<(unsigned)((2 * a.C + 31) / 32), 1024, 0, s>>>(a);
+        gn_grad_sums<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
+        const int64_t values = (int64_t)a.D * a.chunks;
+        if (a.dw)
+            gn_join_sums<T><<<(unsigned)(a.N * a.G + (2 * a.C + 31) / 32), 1024, 0, s>>>(a);
+        else
+            gn_join_sums<T><<<(unsigned)(a.N * a.G), values > 256 ? 1024 : 256, 0, s>>>(a);
+        gn_grad_apply<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
     }
 }
 
@@ -956,7 +982,7 @@ int vec_of(int dtype) { return dtype == FFTCONV_F32 ? 4 : 8; }
 size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool bwd) {
     if (N == 0 || S == 0 || C == 0) return 0;
     const bool token = S == 1 && C / G <= 256;                // whatever the width
-    const int64_t chunks = chunks_of(N, S, C);
+    const int64_t chunks = most_chunks(N, S, C);
     if (!bwd) {
         if (token) return 0;
         // parts of the statistics, and mean and rstd when the caller keeps none
@@ -981,7 +1007,7 @@ int check(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int wdtype, int
         return fail(FFTCONV_ERR_INVALID_ARG, "weight and bias must have x's type or fp32");
     if (act < FFTCONV_ACT_NONE || act > FFTCONV_ACT_SIGMOID) return fail(FFTCONV_ERR_INVALID_ARG, "unknown activation");
     if (C >= (int64_t(1) << 24) || (double)N * (double)G >= 2147483647.0 ||
-        (double)N * (double)chunks_of(N ? N : 1, S ? S : 1, C) >= 2147483647.0)
+        (double)N * (double)most_chunks(N, S ? S : 1, C) + (double)C >= 2147483647.0)
         return fail(FFTCONV_ERR_UNSUPPORTED, "too many channels, samples or groups");
     return FFTCONV_OK;
 }
@@ -1045,13 +1071,12 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
     a.w_f32 = weight_dtype == FFTCONV_F32;
     a.act = act;
     a.eps = eps;
-    a.chunks = (int)chunks_of(N, S, C);
     const int V = vec_of(dtype);
     const bool vec = use_vectors(a, V, rows == 1 || (ld_x % V == 0 && (!gate || ld_gate % V == 0)));
     a.mean = mean;
     a.rstd = rstd;
     if (need) {
-        const int64_t parts = pad256(N * G * (int64_t)a.chunks * ((C + kThreads - 1) / kThreads) * 16);
+        const int64_t parts = pad256(N * G * most_chunks(N, S, C) * ((C + kThreads - 1) / kThreads) * 16);
         a.part = (float*)workspace;
         if (!mean) {
             a.mean = (float*)((uint8_t*)workspace + parts);
@@ -1117,7 +1142,6 @@ int fftconv_group_norm_backward(const void* x, const void* gate, const void* wei
     a.ldx = ld_x; a.ldg = ld_gate; a.ldy = ld_dy;
     a.w_f32 = weight_dtype == FFTCONV_F32;
     a.act = act;
-    a.chunks = (int)chunks_of(N, S, C);
     const int V = vec_of(dtype);
     const bool vec =
         use_vectors(a, V, rows == 1 || (ld_x % V == 0 && ld_dy % V == 0 && (!gate || ld_gate % V == 0)));
