@@ -22,42 +22,39 @@ def _code(dtype):
     return _CODES.get(dtype)
 
 
-def _rows(t, C):
-    """t as rows of C channels one stride apart (None: it does not lie so), and
-    whether the kernels can read it as it lies."""
-    if t.stride(-1) != 1 and C > 1:
-        return None
+def _ld(t, C):
+    """The row stride of t as rows of C channels one stride apart; None where
+    it does not lie so, or where the kernels cannot read it as it lies."""
+    if t.is_contiguous():
+        return C if t.data_ptr() % 16 == 0 else None
+    if not t.numel():
+        return C
     try:
-        return t.view(-1, C)
+        rows = t.view(-1, C)
     except RuntimeError:
         return None
+    if t.data_ptr() % 16 or (C > 1 and t.stride(-1) != 1):
+        return None
+    if rows.shape[0] == 1:
+        return C
+    return rows.stride(0) if rows.stride(0) >= C else None
 
 
-def _checked_rows(t, C, name):
-    r = _rows(t, C)
-    if t.numel() and (r is None or (r.shape[0] > 1 and r.stride(0) < C) or t.data_ptr() % 16):
-        raise ValueError(f"{name} must be rows of contiguous channels, one stride apart, 16-byte aligned")
-    return t.reshape(-1, C) if r is None else r
-
-
-def _ld(r, C):
-    return r.stride(0) if r.shape[0] > 1 else C
-
-
-def _forward(x2, gate2, weight, bias, N, S, C, G, act, eps, out, keep, stream, shape):
+def _forward(x, ld, gate, ld_gate, weight, bias, N, S, C, G, act, eps, out, keep, stream):
     import torch
-    with _on(x2.device, stream) as handle:
-        y = torch.empty(shape, dtype=x2.dtype, device=x2.device) if out is None else out
-        mean = rstd = None
-        if keep:
-            mean, rstd = torch.empty((2, N, G), dtype=torch.float32, device=x2.device).unbind(0)
+    device = x.device
+    with _on(device, stream) as handle:
+        y = torch.empty(x.shape, dtype=x.dtype, device=device) if out is None else out
+        # mean and rstd, one after the other
+        stats = torch.empty((2, N, G), dtype=torch.float32, device=device) if keep else None
+        mean = stats.data_ptr() if keep else None
         n = int(_lib.fftconv_group_norm_workspace_bytes(N, S, C, G, 0))
-        ws = torch.empty(n, dtype=torch.uint8, device=x2.device) if n else None
-        _check(_lib.fftconv_group_norm(_p(x2), _p(gate2), _p(weight), _p(bias), _p(y), _p(mean), _p(rstd), N, S, C, G,
-                                       _ld(x2, C), 0 if gate2 is None else _ld(gate2, C), _code(x2.dtype),
-                                       _code(x2.dtype if weight is None else weight.dtype), act, eps, _p(ws), n,
-                                       handle))
-    return y, mean, rstd
+        ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        code = _code(x.dtype)
+        _check(_lib.fftconv_group_norm(_p(x), _p(gate), _p(weight), _p(bias), _p(y), mean,
+                                       mean + 4 * N * G if keep else None, N, S, C, G, ld, ld_gate, code,
+                                       code if weight is None else _code(weight.dtype), act, eps, _p(ws), n, handle))
+    return y, stats
 
 
 _AUTOGRAD_FN = None
@@ -71,38 +68,39 @@ def _autograd_function():
 
     class GroupNormFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, gate, weight, bias, N, S, C, G, act, eps):
-            y, mean, rstd = _forward(_rows(x, C), None if gate is None else _rows(gate, C), weight, bias, N, S, C, G,
-                                     act, eps, None, True, None, x.shape)
-            ctx.save_for_backward(x, gate, weight, bias, mean, rstd)
-            ctx.args = (N, S, C, G, act)
+        def forward(ctx, x, gate, weight, bias, ld, ld_gate, N, S, C, G, act, eps):
+            y, stats = _forward(x, ld, gate, ld_gate, weight, bias, N, S, C, G, act, eps, None, True, None)
+            ctx.save_for_backward(x, gate, weight, bias, stats)
+            ctx.args = (ld, ld_gate, N, S, C, G, act)
             return y
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dy):
-            x, gate, weight, bias, mean, rstd = ctx.saved_tensors
-            N, S, C, G, act = ctx.args
-            x2, gate2, dy2 = _rows(x, C), None if gate is None else _rows(gate, C), _rows(dy, C)
-            # a gradient comes in whatever layout autograd has
-            if dy2 is None or dy2.data_ptr() % 16 or _ld(dy2, C) < C:
-                dy2 = dy.contiguous().view(-1, C)
+            x, gate, weight, bias, stats = ctx.saved_tensors
+            ld, ld_gate, N, S, C, G, act = ctx.args
             need = ctx.needs_input_grad
-            with _on(x.device, None) as handle:
-                dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-                dgate = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-                dw = db = None
+            ld_dy = _ld(dy, C)
+            if ld_dy is None:
+                # a gradient comes in whatever layout autograd has
+                dy, ld_dy = dy.contiguous(), C
+            device = x.device
+            with _on(device, None) as handle:
+                dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+                dgate = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=device)
+                sums = None
                 if weight is not None and (need[2] or need[3]):
-                    dw, db = torch.empty((2, C), dtype=torch.float32, device=x.device).unbind(0)
+                    sums = torch.empty((2, C), dtype=torch.float32, device=device)
                 n = int(_lib.fftconv_group_norm_workspace_bytes(N, S, C, G, 1))
-                ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+                ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+                code, mean = _code(x.dtype), stats.data_ptr()
+                dw = None if sums is None else sums.data_ptr()
                 _check(_lib.fftconv_group_norm_backward(
-                    _p(x2), _p(gate2), _p(weight), _p(bias), _p(dy2), _p(mean), _p(rstd), _p(dx), _p(dgate), _p(dw),
-                    _p(db), N, S, C, G, _ld(x2, C), 0 if gate is None else _ld(gate2, C), _ld(dy2, C),
-                    _code(x.dtype), _code(x.dtype if weight is None else weight.dtype), act, _p(ws), n,
-                    handle))
-            return (dx if need[0] else None, dgate if need[1] else None, dw.to(weight.dtype) if need[2] else None,
-                    db.to(bias.dtype) if need[3] else None, None, None, None, None, None, None)
+                    _p(x), _p(gate), _p(weight), _p(bias), _p(dy), mean, mean + 4 * N * G, _p(dx), _p(dgate), dw,
+                    None if dw is None else dw + 4 * C, N, S, C, G, ld, ld_gate, ld_dy, code,
+                    code if weight is None else _code(weight.dtype), act, _p(ws), n, handle))
+            return (dx if need[0] else None, dgate if need[1] else None, sums[0].to(weight.dtype) if need[2] else None,
+                    sums[1].to(bias.dtype) if need[3] else None) + (None,) * 8
 
     _AUTOGRAD_FN = GroupNormFunction
     return _AUTOGRAD_FN
@@ -150,13 +148,15 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
     if out is not None and (out.shape != x.shape or out.dtype != x.dtype or out.device != x.device or
                             not out.is_contiguous() or (out.numel() and out.data_ptr() % 16)):
         raise ValueError("out must be contiguous, 16-byte aligned, and have x's shape, dtype and device")
-    x2 = _checked_rows(x, C, "x")
-    gate2 = None if gate is None else _checked_rows(gate, C, "gate")
+    ld, ld_gate = _ld(x, C), 0 if gate is None else _ld(gate, C)
+    if ld is None or ld_gate is None:
+        raise ValueError(f"{'x' if ld is None else 'gate'} must be rows of contiguous channels, one stride apart, "
+                         "16-byte aligned")
     grad = torch.is_grad_enabled() and (
         x.requires_grad or (gate is not None and gate.requires_grad) or
         (weight is not None and (weight.requires_grad or bias.requires_grad)))
     if grad:
         if out is not None or stream is not None:
             raise NotImplementedError("group_norm: no gradients with out= or stream=")
-        return _autograd_function().apply(x, gate, weight, bias, N, S, C, G, act, float(eps))
-    return _forward(x2, gate2, weight, bias, N, S, C, G, act, float(eps), out, False, stream, x.shape)[0]
+        return _autograd_function().apply(x, gate, weight, bias, ld, ld_gate, N, S, C, G, act, float(eps))
+    return _forward(x, ld, gate, ld_gate, weight, bias, N, S, C, G, act, float(eps), out, False, stream)[0]
