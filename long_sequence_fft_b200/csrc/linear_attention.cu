@@ -1144,24 +1144,29 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
     }
     if (count < 2 || sid0 + count > p.max_seg) return;
     const int64_t mat = (int64_t)r.kd * r.vd;
-    const int e = blockIdx.y * 256 + threadIdx.x;
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;       // four elements of a row
     if (e >= mat) return;
     const float ld = p.log_decay[h];
     const float whole = decay_power(ld, (float)p.seg_len);
     const float tail = decay_power(ld, (float)(len - (count - 1) * p.seg_len));
-    float run = 0.f;
+    const int64_t at_seq = ((int64_t)seq * p.H + h) * mat;
+    float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r.init) {
-        const int row = e / r.vd, col = e % r.vd;
-        run = r.init[((int64_t)seq * p.H + h) * mat + (r.init_t ? col * r.kd + row : e)];
+        if (r.init_t) {
+            const float* src = r.init + at_seq + (int64_t)(e % r.vd) * r.kd + e / r.vd;
+            run = make_float4(src[0], src[r.kd], src[2 * r.kd], src[3 * r.kd]);
+        } else {
+            run = *reinterpret_cast<const float4*>(r.init + at_seq + e);
+        }
     }
-    const int64_t step = (int64_t)p.H * mat;
-    float* at = r.seg + ((int64_t)sid0 * p.H + h) * mat + e;
+    const int64_t step = (int64_t)p.H * mat / 4;
+    float4* at = reinterpret_cast<float4*>(r.seg + ((int64_t)sid0 * p.H + h) * mat + e);
     // the last segment's own state is there where the final state is wanted
     const int have = r.fin ? count : count - 1;
     // the loads of four segments go out together: their addresses do not
     // depend on the running state
     for (int s = 0; s < count; s += 4) {
-        float local[4];
+        float4 local[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
             if (s + q < have) local[q] = at[(int64_t)(r.rev ? count - 1 - s - q : s + q) * step];
@@ -1170,10 +1175,16 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
             if (s + q >= count) break;
             const int i = r.rev ? count - 1 - s - q : s + q;
             at[(int64_t)i * step] = run;
-            if (s + q < have) run = fmaf(i == count - 1 ? tail : whole, run, local[q]);
+            if (s + q < have) {
+                const float g = i == count - 1 ? tail : whole;
+                run.x = fmaf(g, run.x, local[q].x);
+                run.y = fmaf(g, run.y, local[q].y);
+                run.z = fmaf(g, run.z, local[q].z);
+                run.w = fmaf(g, run.w, local[q].w);
+            }
         }
     }
-    if (r.fin) r.fin[((int64_t)seq * p.H + h) * mat + e] = run;
+    if (r.fin) *reinterpret_cast<float4*>(r.fin + at_seq + e) = run;
 }
 
 __device__ __forceinline__ void used_tokens(const int32_t* cu, int nseq, int64_t T, int64_t& lo, int64_t& hi) {
@@ -1345,9 +1356,9 @@ Split split_of(const fftconv_linear_attention_t& d, int nroles) {
     Split s{up(d.T), 1, seqs, false};
     int64_t len;
     if (d.nseq > 0) {
-        // lengths are known on the device only
-        const int64_t share = (d.T * d.H * nroles + sms - 1) / sms;
-        len = up(share + share * 3 / 5);
+        // lengths are known on the device only: half an even share a piece
+        // evens the SMs' work out whatever they are
+        len = up((d.T * d.H * nroles + 2 * sms - 1) / (2 * sms));
     } else {
         const int64_t share = (d.B * d.T * d.H * nroles + sms - 1) / sms;
         if (d.T * ((tasks + sms - 1) / sms) <= share + share * 3 / 5 + 4 * kChunk) return s;
@@ -1431,10 +1442,10 @@ void fill(Params& p, const fftconv_linear_attention_t& d, const Split& s, const 
     p.max_seg = (int)s.max_seg;
 }
 
-// The launches of up to three roles of one padded shape.
-cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, const Split& s, cudaStream_t stream) {
-    const Role& r = p.role[0];
-    const int kp = r.kd > 64 ? 128 : 64, vp = r.vd > 64 ? 128 : 64;
+// The launches of up to three roles, all with key and value dims within
+// (kp, vp).
+cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, const Split& s, int kp, int vp,
+                      cudaStream_t stream) {
     const bool f16 = d.dtype == FFTCONV_F16;
     const int64_t ctas = s.max_seg * d.H * p.nroles;
     bool exact = false;                       // a state is a result
@@ -1445,7 +1456,7 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
         const int64_t seqs = d.nseq > 0 ? d.nseq : d.B;
         void* args[] = {const_cast<Params*>(&p)};
         e = cudaLaunchKernel(reinterpret_cast<const void*>(la_combine),
-                             dim3((unsigned)(seqs * d.H), (unsigned)((d.K * d.V + 255) / 256), (unsigned)p.nroles),
+                             dim3((unsigned)(seqs * d.H), (unsigned)((d.K * d.V + 1023) / 1024), (unsigned)p.nroles),
                              dim3(256), args, 0, stream);
         if (e != cudaSuccess) return e;
     }
@@ -1540,7 +1551,7 @@ int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void
     r.seg = (float*)workspace;
     cudaError_t e = cudaSuccess;
     if (d.nseq > 0 && d.zero_rest) e = zero_rest(o, d, d.H, d.V, d.o_stride, cu_seqlens, s);
-    if (e == cudaSuccess) e = run_roles(p, d, sp, s);
+    if (e == cudaSuccess) e = run_roles(p, d, sp, d.K > 64 ? 128 : 64, d.V > 64 ? 128 : 64, s);
     return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "linear attention launch");
 }
 
@@ -1656,17 +1667,21 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
             if (!part[i]) e = zero_rest(out[i], d, heads[i], dims[i], st, cu_seqlens, s);
         }
     if (e == cudaSuccess) {
-        if ((d.K > 64) == (d.V > 64)) {
-            e = run_roles(p, d, sp, s);
+        const int kp = d.K > 64 ? 128 : 64, vp = d.V > 64 ? 128 : 64;
+        if (kp == vp || sp.max_seg * d.H * 3 <= sm_count()) {
+            // (mixed widths that leave SMs idle: one launch at the larger one
+            // instead of two in a row)
+            const int w = kp > vp ? kp : vp;
+            e = run_roles(p, d, sp, w, w, s);
         } else {
-            // dq and dk have the dims (V, K), dv has (K, V): two padded shapes
+            // dq and dk have the dims (V, K), dv has (K, V)
             Params a = p;
             a.nroles = 2;
-            e = run_roles(a, d, sp, s);
+            e = run_roles(a, d, sp, vp, kp, s);
             if (e == cudaSuccess) {
                 a.nroles = 1;
                 a.role[0] = p.role[2];
-                e = run_roles(a, d, sp, s);
+                e = run_roles(a, d, sp, kp, vp, s);
             }
         }
     }
