@@ -55,7 +55,7 @@ struct Role {
     int64_t out_b, out_t, out_h;
     const float* init;                        // [seq][H][kd][vd], or null: zeros
     float* fin;                               // carry behind the last token, or null
-    float* seg;                               // segment states [segment][H][kd][vd]
+    float* seg;                               // segment states [segment][H][vd][kd]: a lane's row, so that loads coalesce
 };
 
 struct Params {
@@ -814,14 +814,31 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             arrive(wgb_bar);
             return wait(wgb_bar, sync_phase++);
         };
-        auto initial = [&](int col) -> float {
-            if (second || ch >= r.kd || col >= r.vd) return 0.f;
-            if (!first) return r.seg[at_seg + (int64_t)ch * r.vd + col];
-            return r.init ? r.init[at_seq + (r.init_t ? (int64_t)col * r.kd + ch : (int64_t)ch * r.vd + col)] : 0.f;
-        };
         float state[kCols];
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) state[j] = has_init && nch > 0 ? initial(col0 + j) : 0.f;
+        for (int j = 0; j < kCols; ++j) state[j] = 0.f;
+        // the state in front of the first chunk
+        auto initial = [&]() {
+            if (second || ch >= r.kd || (first && !r.init)) return;
+            if (!first || r.init_t) {
+                const float* src = (first ? r.init + at_seq : r.seg + at_seg) + ch;
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    if (col0 + j < r.vd) state[j] = src[(int64_t)(col0 + j) * r.kd];
+            } else {
+                const float* src = r.init + at_seq + (int64_t)ch * r.vd + col0;
+#pragma unroll
+                for (int j = 0; j < kCols; j += 4)
+                    if (col0 + j < r.vd) {
+                        const float4 v = *reinterpret_cast<const float4*>(src + j);
+                        state[j] = v.x;
+                        state[j + 1] = v.y;
+                        state[j + 2] = v.z;
+                        state[j + 3] = v.w;
+                    }
+            }
+        };
+        if (has_init && nch > 0) initial();
         if (L::Stacked && L::KtCols == 128 && second) {
             // the third part has no second half
             const uint32_t zero[16] = {};
@@ -1080,12 +1097,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             rs_done = rs;
         }
         if (ok && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
-            float* dst = (STATE_ONLY ? r.seg + at_seg : r.fin + at_seq) + (int64_t)ch * r.vd;
             if (nch > 0)
                 ok = advance(nch - 1);
             else
-#pragma unroll
-                for (int j = 0; j < kCols; ++j) state[j] = initial(col0 + j);
+                initial();
             if constexpr (L::Stacked) {
                 // the second half of the rows hands its part of the sum over, in the carry copy's place
                 if (ok && !STATE_ONLY && nch > 0) ok = wait(&bar_o[(nch - 1) % NA], (nch - 1) / NA);
@@ -1099,11 +1114,19 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     for (int j = 0; j < kCols; ++j) state[j] += sum[(col0 + j) * 64 + ch];
             }
             if (ok && ch < r.kd && !second) {
+                if constexpr (STATE_ONLY) {
+                    float* dst = r.seg + at_seg + ch;
 #pragma unroll
-                for (int j = 0; j < kCols; j += 4)
-                    if (col0 + j < r.vd)
-                        *reinterpret_cast<float4*>(dst + col0 + j) =
-                            make_float4(state[j], state[j + 1], state[j + 2], state[j + 3]);
+                    for (int j = 0; j < kCols; ++j)
+                        if (col0 + j < r.vd) dst[(int64_t)(col0 + j) * r.kd] = state[j];
+                } else {
+                    float* dst = r.fin + at_seq + (int64_t)ch * r.vd + col0;
+#pragma unroll
+                    for (int j = 0; j < kCols; j += 4)
+                        if (col0 + j < r.vd)
+                            *reinterpret_cast<float4*>(dst + j) =
+                                make_float4(state[j], state[j + 1], state[j + 2], state[j + 3]);
+                }
             }
         }
         if (!ok) fail();
@@ -1144,8 +1167,9 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
     }
     if (count < 2 || sid0 + count > p.max_seg) return;
     const int64_t mat = (int64_t)r.kd * r.vd;
-    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;       // four elements of a row
+    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;       // four rows of a column
     if (e >= mat) return;
+    const int row = e % r.kd, col = e / r.kd;
     const float ld = p.log_decay[h];
     const float whole = decay_power(ld, (float)p.seg_len);
     const float tail = decay_power(ld, (float)(len - (count - 1) * p.seg_len));
@@ -1153,10 +1177,10 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r.init) {
         if (r.init_t) {
-            const float* src = r.init + at_seq + (int64_t)(e % r.vd) * r.kd + e / r.vd;
-            run = make_float4(src[0], src[r.kd], src[2 * r.kd], src[3 * r.kd]);
-        } else {
             run = *reinterpret_cast<const float4*>(r.init + at_seq + e);
+        } else {
+            const float* src = r.init + at_seq + (int64_t)row * r.vd + col;
+            run = make_float4(src[0], src[r.vd], src[2 * r.vd], src[3 * r.vd]);
         }
     }
     const int64_t step = (int64_t)p.H * mat / 4;
@@ -1184,7 +1208,13 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
             }
         }
     }
-    if (r.fin) *reinterpret_cast<float4*>(r.fin + at_seq + e) = run;
+    if (r.fin) {
+        float* dst = r.fin + at_seq + (int64_t)row * r.vd + col;
+        dst[0] = run.x;
+        dst[r.vd] = run.y;
+        dst[2 * r.vd] = run.z;
+        dst[3 * r.vd] = run.w;
+    }
 }
 
 __device__ __forceinline__ void used_tokens(const int32_t* cu, int nseq, int64_t T, int64_t& lo, int64_t& hi) {
