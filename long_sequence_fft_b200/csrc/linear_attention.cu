@@ -1166,30 +1166,42 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
         count = cnt(seq, len);
     }
     if (count < 2 || sid0 + count > p.max_seg) return;
-    const int64_t mat = (int64_t)r.kd * r.vd;
-    const int e = (blockIdx.y * 256 + threadIdx.x) * 4;       // four rows of a column
-    if (e >= mat) return;
-    const int row = e % r.kd, col = e / r.kd;
+    // a tile of 32 x 32: a thread has four rows of a column of the segments'
+    // states; where the first and the last state lie the other way, they go
+    // through shared memory
+    const int64_t mat = (int64_t)r.kd * r.vd, at_seq = ((int64_t)seq * p.H + h) * mat;
+    const int tiles = (r.kd + 31) / 32, row0 = (int)blockIdx.y % tiles * 32, col0 = (int)blockIdx.y / tiles * 32;
+    if (col0 >= r.vd) return;
+    __shared__ float turn[32][33];
+    const int x4 = threadIdx.x % 8 * 4, y = threadIdx.x / 8;
+    const int row = row0 + x4, col = col0 + y;                // of the segments' states
+    const int nrow = row0 + y, ncol = col0 + x4;              // of a state in rows
+    const bool in = row < r.kd && col < r.vd, nin = nrow < r.kd && ncol < r.vd;
     const float ld = p.log_decay[h];
     const float whole = decay_power(ld, (float)p.seg_len);
     const float tail = decay_power(ld, (float)(len - (count - 1) * p.seg_len));
-    const int64_t at_seq = ((int64_t)seq * p.H + h) * mat;
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r.init) {
-        if (r.init_t) {
-            run = *reinterpret_cast<const float4*>(r.init + at_seq + e);
-        } else {
-            const float* src = r.init + at_seq + (int64_t)row * r.vd + col;
-            run = make_float4(src[0], src[r.vd], src[2 * r.vd], src[3 * r.vd]);
+    if (r.init && r.init_t) {
+        if (in) run = *reinterpret_cast<const float4*>(r.init + at_seq + (int64_t)col * r.kd + row);
+    } else if (r.init) {
+        if (nin) {
+            const float4 v = *reinterpret_cast<const float4*>(r.init + at_seq + (int64_t)nrow * r.vd + ncol);
+            turn[y][x4] = v.x;
+            turn[y][x4 + 1] = v.y;
+            turn[y][x4 + 2] = v.z;
+            turn[y][x4 + 3] = v.w;
         }
+        __syncthreads();
+        run = make_float4(turn[x4][y], turn[x4 + 1][y], turn[x4 + 2][y], turn[x4 + 3][y]);
+        __syncthreads();
     }
     const int64_t step = (int64_t)p.H * mat / 4;
-    float4* at = reinterpret_cast<float4*>(r.seg + ((int64_t)sid0 * p.H + h) * mat + e);
+    float4* at = reinterpret_cast<float4*>(r.seg + ((int64_t)sid0 * p.H + h) * mat + (int64_t)col * r.kd + row);
     // the last segment's own state is there where the final state is wanted
-    const int have = r.fin ? count : count - 1;
+    const int have = r.fin ? count : count - 1, todo = in ? count : 0;
     // the loads of four segments go out together: their addresses do not
     // depend on the running state
-    for (int s = 0; s < count; s += 4) {
+    for (int s = 0; s < todo; s += 4) {
         float4 local[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -1209,11 +1221,14 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
         }
     }
     if (r.fin) {
-        float* dst = r.fin + at_seq + (int64_t)row * r.vd + col;
-        dst[0] = run.x;
-        dst[r.vd] = run.y;
-        dst[2 * r.vd] = run.z;
-        dst[3 * r.vd] = run.w;
+        turn[x4][y] = run.x;
+        turn[x4 + 1][y] = run.y;
+        turn[x4 + 2][y] = run.z;
+        turn[x4 + 3][y] = run.w;
+        __syncthreads();
+        if (nin)
+            *reinterpret_cast<float4*>(r.fin + at_seq + (int64_t)nrow * r.vd + ncol) =
+                make_float4(turn[y][x4], turn[y][x4 + 1], turn[y][x4 + 2], turn[y][x4 + 3]);
     }
 }
 
@@ -1486,7 +1501,7 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
         const int64_t seqs = d.nseq > 0 ? d.nseq : d.B;
         void* args[] = {const_cast<Params*>(&p)};
         e = cudaLaunchKernel(reinterpret_cast<const void*>(la_combine),
-                             dim3((unsigned)(seqs * d.H), (unsigned)((d.K * d.V + 1023) / 1024), (unsigned)p.nroles),
+                             dim3((unsigned)(seqs * d.H), (unsigned)((d.K + 31) / 32 * ((d.V + 31) / 32)), (unsigned)p.nroles),
                              dim3(256), args, 0, stream);
         if (e != cudaSuccess) return e;
     }
