@@ -300,8 +300,9 @@ struct Layout {
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, TMEM base, scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int OffMax = OffBar + 28 * 8;            // (fp16) channel maxima of each warp's tokens
-    static constexpr int Bytes = OffMax + (F16 ? KtBufs * kStateWarps * KP : 0);
+    static constexpr int Bars = 27 + (F16 ? Stages : 0);
+    static constexpr int OffMax = OffBar + (Bars + 1) / 2 * 16;   // (fp16) channel scales of each stage's keys
+    static constexpr int Bytes = OffMax + (F16 ? Stages * KP * 4 : 0);
     // TMEM columns
     static constexpr int S = 0, O = S + Groups * 128, Oc = SplitOut ? O + VP : O, C = STATE_ONLY ? 0 : Oc + VP,
                          Kt = C + VP;
@@ -356,6 +357,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     uint64_t* wgb_bar = bars + 24;
     uint64_t* c_free = bars + 25;                             // the chunk's own state read
     uint64_t* bar_fin = bars + 26;                            // all MMA warps
+    uint64_t* scale_ready = bars + 27;                        // [Stages] (fp16) scales of a stage's keys
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -366,29 +368,54 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     const Role& r = p.role[role_i];
     const bool rev = r.rev != 0;
 
-    if (warp == 0) {
+    // a segment's chunks, and whether it is the first or last in the role's
+    // direction of time; a split sequence's last own state only matters where
+    // it is a result
+    auto first_of = [&](int idx, int count) { return rev ? idx == count - 1 : idx == 0; };
+    auto chunks_of = [&](const Segment& s) {
+        if (s.seq < 0 || (STATE_ONLY && first_of(s.count - 1 - s.idx, s.count) && (s.count == 1 || r.fin == nullptr)))
+            return 0;
+        return (s.n + kChunk - 1) / kChunk;
+    };
+    auto load_chunk = [&](int c, int nch, int t0, int b) {    // by one thread
+        const int st = c % L::Stages, t = t0 + (rev ? nch - 1 - c : c) * kChunk;
+        const int hx = h / r.x_div, hy = h / r.y_div, hz = h / r.z_div;
+        uint8_t* base = smem + st * L::StageBytes;
+        mbar_expect_tx(&full[st], L::StageBytes);
+        for (int d = 0; d < KP; d += 64) tma_load(base + L::OffY + d * 256, &p.maps[r.y], d, hy, t, b, &full[st]);
+        if (!STATE_ONLY)
+            for (int d = 0; d < KP; d += 64) tma_load(base + d * 256, &p.maps[r.x], d, hx, t, b, &full[st]);
+        for (int d = 0; d < VP; d += 64) tma_load(base + L::OffZ + d * 256, &p.maps[r.z], d, hz, t, b, &full[st]);
+    };
+
+    if (warp == L::LoadWarp) {
         const Segment s = find_segment(p, sid);
         if (lane == 0) {
+            for (int i = 0; i < 4; ++i) {
+                mbar_init(&full[i], 1);
+                mbar_init(&empty[i], STATE_ONLY ? 1 : 6);     // two MMA warps, four row warps
+            }
+            for (int i = 8; i < 14; ++i) mbar_init(bars + i, 1);
+            for (int i = 14; i < 18; ++i) mbar_init(bars + i, 4);
+            mbar_init(bar_st, 1);
+            mbar_init(bar_kt, 1);
+            for (int i = 20; i < 26; ++i) mbar_init(bars + i, kStateWarps);
+            mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
+            if constexpr (F16)
+                for (int i = 0; i < L::Stages; ++i) mbar_init(&scale_ready[i], 1);
+            *abort_flag = 0;
+            fence_barrier_init();
+            fence_proxy_async_smem();                         // the loads' engine sees the barriers
             misc[0] = s.seq;
             misc[1] = s.idx;
             misc[2] = s.count;
             misc[3] = s.n;
             misc[4] = s.t0;
             misc[5] = s.b;
+            // the first loads go out while the other warps set up
+            const int nch = chunks_of(s);
+            for (int c = 0; c < min(nch, L::Stages); ++c) load_chunk(c, nch, s.t0, s.b);
         }
-    } else if (warp == L::LoadWarp && lane == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], STATE_ONLY ? 1 : 6);         // two MMA warps, four row warps
-        }
-        for (int i = 8; i < 14; ++i) mbar_init(bars + i, 1);
-        for (int i = 14; i < 18; ++i) mbar_init(bars + i, 4);
-        mbar_init(bar_st, 1);
-        mbar_init(bar_kt, 1);
-        for (int i = 20; i < 26; ++i) mbar_init(bars + i, kStateWarps);
-        mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
-        *abort_flag = 0;
-        fence_barrier_init();
     } else if (warp == L::MmaWarp) {
         tmem_alloc(tmem_sh, 512);
         tmem_relinquish();
@@ -409,12 +436,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_sh, 0);
     const int seq = misc[0], idx = misc[1], count = misc[2], n = misc[3], t0 = misc[4], b = misc[5];
-    const bool first = rev ? idx == count - 1 : idx == 0;     // in the direction of time of the role
-    const bool last = rev ? idx == 0 : idx == count - 1;
-    // a split sequence's last state only matters where it is a result
-    const int nch = (seq < 0 || (STATE_ONLY && last && (count == 1 || r.fin == nullptr)))
-                        ? 0
-                        : (n + kChunk - 1) / kChunk;
+    const bool first = first_of(idx, count);
+    const int nch = chunks_of(Segment{seq, idx, count, n, t0, b});
     const bool has_init = !STATE_ONLY && (first ? r.init != nullptr : true);
     const bool want_fin = STATE_ONLY || (count == 1 && r.fin != nullptr);
 
@@ -446,24 +469,14 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 
     if (warp == L::LoadWarp) {
         // ------------------------------------------------------- loads ---
-        if (lane == 0 && nch > 0) {
-            const CUtensorMap *mx = &p.maps[r.x], *my = &p.maps[r.y], *mz = &p.maps[r.z];
-            const int hx = h / r.x_div, hy = h / r.y_div, hz = h / r.z_div;
-            int issued = 0;
-            for (int c = 0; c < nch; ++c) {
-                const int st = c % L::Stages;
-                if (c >= L::Stages &&
-                    !wait_phase(&empty[st], ((c / L::Stages) - 1) & 1, abort_flag)) {
+        if (lane == 0) {
+            int issued = min(nch, L::Stages);
+            for (int c = L::Stages; c < nch; ++c) {
+                if (!wait_phase(&empty[c % L::Stages], ((c / L::Stages) - 1) & 1, abort_flag)) {
                     fail();
                     break;
                 }
-                uint8_t* base = smem + st * L::StageBytes;
-                const int t = t0 + chunk_at(c);
-                mbar_expect_tx(&full[st], L::StageBytes);
-                for (int d = 0; d < KP; d += 64) tma_load(base + L::OffY + d * 256, my, d, hy, t, b, &full[st]);
-                if (!STATE_ONLY)
-                    for (int d = 0; d < KP; d += 64) tma_load(base + d * 256, mx, d, hx, t, b, &full[st]);
-                for (int d = 0; d < VP; d += 64) tma_load(base + L::OffZ + d * 256, mz, d, hz, t, b, &full[st]);
+                load_chunk(c, nch, t0, b);
                 issued = c + 1;
             }
             // nothing of this CTA's loads is in flight when it ends
@@ -512,16 +525,53 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         }
     } else if (warp == L::ScoreWarp) {
         // ----------------------------------------- MMAs of the scores ---
-        if constexpr (!STATE_ONLY) {
-            const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
-            const uint32_t sb = smem_u32(smem);
-            bool ok = true;
-            for (int c = 0; c < nch; ++c) {
-                const int st = c % L::Stages, ga = c % NA;
+        // and (fp16) the scales of the keys, ahead of the state warps: each
+        // channel's largest weighted key comes out below 2^15.
+        const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
+        const uint32_t sb = smem_u32(smem);
+        bool ok = true;
+        for (int c = 0; c < nch && (F16 || !STATE_ONLY); ++c) {
+            const int st = c % L::Stages, ga = c % NA;
+            ok = wait(&full[st], c / L::Stages);
+            if (!ok) break;
+            if constexpr (F16) {
+                // eight channels a lane, every fourth (second) token
+                constexpr int kVecs = KP / 8, kRows = 32 / kVecs;
+                const int nv = chunk_n(c), v8 = lane % kVecs;
+                const uint8_t* keys = smem + st * L::StageBytes + L::OffY + (v8 >> 3) * 16384;
+                __half2 m[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.f);
+#pragma unroll 4
+                for (int j = lane / kVecs; j < nv; j += kRows) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(keys + j * 128 + (((v8 & 7) ^ (j & 7)) << 4));
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t mag = w[e] & 0x7fff7fffu;
+                        m[e] = __hmax2(m[e], *reinterpret_cast<const __half2*>(&mag));
+                    }
+                }
+                __syncwarp();
+                float* scale = reinterpret_cast<float*>(smem + L::OffMax) + st * KP + v8 * 8;
+                const float up = fabsf(r.key_scale) * fmaxf(1.f, pw[nv]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                    for (int x = kVecs; x < 32; x *= 2) m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], x));
+                    const float2 f = __half22float2(m[e]);
+                    if (lane < kVecs) {
+                        scale[2 * e] = f.x < 65536.f ? fp16_scale(f.x * up) : 1.f;
+                        scale[2 * e + 1] = f.y < 65536.f ? fp16_scale(f.y * up) : 1.f;
+                    }
+                }
+                arrive(&scale_ready[st]);
+            }
+            if constexpr (!STATE_ONLY) {
                 const uint32_t base = sb + st * L::StageBytes;
                 const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::OffY, 16, 1024, 2);
-                // the loads are there, and the score tile's last P is used up
-                ok = wait(&full[st], c / L::Stages) && (c < NA || wait(&bar_pv[ga], c / NA - 1));
+                // the score tile's last P is used up
+                if (c >= NA) ok = wait(&bar_pv[ga], c / NA - 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -531,9 +581,9 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 }
                 tc_commit_warp(&bar_s[ga]);
             }
-            if (!ok) fail();
-            tc_commit_warp(bar_fin);
         }
+        if (!ok) fail();
+        if constexpr (!STATE_ONLY) tc_commit_warp(bar_fin);
     } else if (warp == L::StateMmaWarp) {
         // ------------------------------ MMAs of the chunks' own states ---
         // The smallest parts first: the MMA truncates each sum, so few steps
@@ -808,7 +858,6 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         // (fp16) powers of two on this channel's weighted keys: the chunk's at
         // hand, and the one's whose own state is read next
         float rs = 1.f, rs_done = 1.f;
-        uint8_t* kmax_sh = smem + L::OffMax;
         uint32_t sync_phase = 0;
         auto sync_b = [&]() -> bool {                         // bounded barrier of the state warps
             arrive(wgb_bar);
@@ -947,13 +996,25 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 krow = base + L::OffY + (c8 >> 3) * 16384 + (half * 64 + (tile >> 1) * 8 + (lane & 7)) * 128;
             }
             const int c8 = (L::Stacked ? bw & 1 : bw) * 4 + (lane >> 3 & 1);
-            // the first PARTS parts of channels 16 m.., tokens 32 th.. of the half
-            auto weighted = [&](int m, int th, uint32_t (&part)[3][8], auto parts) {
-                constexpr int PARTS = decltype(parts)::value;
-                uint32_t x[8];
+            // tokens 32 th.. of the half, both groups of 16 channels: all loads first
+            struct Raw {
+                uint32_t x[2][8];
+                float2 w[4];
+            };
+            auto raw_keys = [&](int th, Raw& k) {
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    ldmatrix4_trans(krow + (2 * th + t) * 2048 + ((((c8 + 2 * m) & 7) ^ (lane & 7)) << 4), x + 4 * t);
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        ldmatrix4_trans(krow + (2 * th + t) * 2048 + ((((c8 + 2 * m) & 7) ^ (lane & 7)) << 4),
+                                        k.x[m] + 4 * t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    k.w[i] = *reinterpret_cast<const float2*>(kw + half * 64 + 32 * th + 8 * i + 2 * (lane & 3));
+            };
+            // the first PARTS parts of channels 16 m..
+            auto weighted = [&](int m, int th, const Raw& k, uint32_t (&part)[3][8], auto parts) {
+                constexpr int PARTS = decltype(parts)::value;
                 float2 sc[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
@@ -962,10 +1023,9 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 w = *reinterpret_cast<const float2*>(kw + half * 64 + 32 * th + 8 * i + 2 * (lane & 3));
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        float2 f = mul2(unpack<F16>(x[2 * i + y]), F16 ? mul2(w, sc[y]) : w);
+                        float2 f = mul2(unpack<F16>(k.x[m][2 * i + y]), F16 ? mul2(k.w[i], sc[y]) : k.w[i]);
 #pragma unroll
                         for (int q = 0; q < PARTS; ++q) {
                             part[q][2 * i + y] = pack<F16>(f.x, f.y);
@@ -993,74 +1053,42 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             const uint32_t t_kt = tbase + row + L::Kt + c % L::KtBufs * L::KtCols + half * 32;
             if (more) {
                 if constexpr (F16) {
-                    // Scale each channel so that its largest weighted key is
-                    // below 2^15, by the exponents of the maxima: a warp takes
-                    // 16 tokens, eight channels a lane at a time.
-                    constexpr int kVecs = KP / 8, kRows = 32 / kVecs;
-                    const int v8 = lane % kVecs;
-                    __half2 m[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.f);
-#pragma unroll
-                    for (int q = 0; q < 16 / kRows; ++q) {
-                        const int j = sw * 16 + q * kRows + lane / kVecs;
-                        if (j < nv) {
-                            const uint4 x = *reinterpret_cast<const uint4*>(base + L::OffY + (v8 >> 3) * 16384 + j * 128 +
-                                                                            (((v8 & 7) ^ (j & 7)) << 4));
-                            const __half2* y = reinterpret_cast<const __half2*>(&x);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) m[e] = __hmax2(m[e], __habs2(y[e]));
-                        }
-                    }
-                    uint32_t lo = 0, hi = 0;                  // eight exponents
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                        for (int x = kVecs; x < 32; x *= 2) m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], x));
-                        const uint32_t y = *reinterpret_cast<const uint32_t*>(&m[e]);
-                        const uint32_t two = (y >> 10 & 31u) | (y >> 26 & 31u) << 8;
-                        (e < 2 ? lo : hi) |= two << (e & 1) * 16;
-                    }
-                    // (the place's last maxima are read: every warp has passed a later barrier)
-                    uint8_t* kmax = kmax_sh + c % L::KtBufs * kStateWarps * KP;
-                    if (lane < kVecs) *reinterpret_cast<uint2*>(kmax + sw * KP + v8 * 8) = make_uint2(lo, hi);
-                    if (!sync_b()) return false;
-                    int top = 0;
-#pragma unroll
-                    for (int w = 0; w < kStateWarps; ++w) top = max(top, (int)kmax[w * KP + ch]);
-                    // keys below 2^(top - 14) (a channel of zeros and subnormals: below 2^-14)
-                    rs = top < 31 ? fp16_scale(__uint_as_float((uint32_t)(max(top, 1) - 15 + 127) << 23) *
-                                               fabsf(r.key_scale) * fmaxf(1.f, pw[nv])) * 0.5f
-                                  : 1.f;
+                    if (!wait(&scale_ready[st], c / L::Stages)) return false;
+                    rs = reinterpret_cast<const float*>(smem + L::OffMax)[st * KP + ch];
                 }
 #pragma unroll 1
-                for (int mt = 0; mt < 4; ++mt) {
-                    const int m = mt >> 1, th = mt & 1;
-                    const uint32_t at = t_kt + th * 16 + ((uint32_t)(m * 16) << 16);
-                    uint32_t part[3][8];
-                    if constexpr (!L::Stacked) {
-                        weighted(m, th, part, All{});
+                for (int th = 0; th < 2; ++th) {
+                    Raw k;
+                    raw_keys(th, k);
 #pragma unroll
-                        for (int q = 0; q < L::KtCols / 64; ++q) tmem_st_16x16(at + q * 64, part[q + (L::Late ? 1 : 0)]);
-                    } else if (L::Late) {
-                        // the third part, and nothing beside it
-                        if (second) {
+                    for (int m = 0; m < 2; ++m) {
+                        const uint32_t at = t_kt + th * 16 + ((uint32_t)(m * 16) << 16);
+                        uint32_t part[3][8];
+                        if constexpr (!L::Stacked) {
+                            weighted(m, th, k, part, All{});
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) part[2][j] = 0u;
+                            for (int q = 0; q < L::KtCols / 64; ++q)
+                                tmem_st_16x16(at + q * 64, part[q + (L::Late ? 1 : 0)]);
+                        } else if (L::Late) {
+                            // the third part, and nothing beside it
+                            if (second) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) part[2][j] = 0u;
+                            } else {
+                                weighted(m, th, k, part, All{});
+                            }
+                            tmem_st_16x16(at, part[2]);
+                        } else if (second) {
+                            weighted(m, th, k, part, Two{});
+                            tmem_st_16x16(at, part[1]);
+                        } else if constexpr (L::KtCols == 128) {
+                            weighted(m, th, k, part, All{});
+                            tmem_st_16x16(at, part[0]);
+                            tmem_st_16x16(at + 64, part[2]);
                         } else {
-                            weighted(m, th, part, All{});
+                            weighted(m, th, k, part, One{});
+                            tmem_st_16x16(at, part[0]);
                         }
-                        tmem_st_16x16(at, part[2]);
-                    } else if (second) {
-                        weighted(m, th, part, Two{});
-                        tmem_st_16x16(at, part[1]);
-                    } else if constexpr (L::KtCols == 128) {
-                        weighted(m, th, part, All{});
-                        tmem_st_16x16(at, part[0]);
-                        tmem_st_16x16(at + 64, part[2]);
-                    } else {
-                        weighted(m, th, part, One{});
-                        tmem_st_16x16(at, part[0]);
                     }
                 }
             }
@@ -1072,16 +1100,20 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     if (!wait(bar_kt, c)) return false;
                     tc_fence_after();
 #pragma unroll 1
-                    for (int mt = 0; mt < 4; ++mt) {
-                        const int m = mt >> 1, th = mt & 1;
-                    const uint32_t at = t_kt + th * 16 + ((uint32_t)(m * 16) << 16);
-                        uint32_t part[3][8];
-                        if (second) {
-                            weighted(m, th, part, Two{});
-                            tmem_st_16x16(at, part[1]);
-                        } else {
-                            weighted(m, th, part, One{});
-                            tmem_st_16x16(at, part[0]);
+                    for (int th = 0; th < 2; ++th) {
+                        Raw k;
+                        raw_keys(th, k);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t at = t_kt + th * 16 + ((uint32_t)(m * 16) << 16);
+                            uint32_t part[3][8];
+                            if (second) {
+                                weighted(m, th, k, part, Two{});
+                                tmem_st_16x16(at, part[1]);
+                            } else {
+                                weighted(m, th, k, part, One{});
+                                tmem_st_16x16(at, part[0]);
+                            }
                         }
                     }
                     tc_wait_st();
