@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         return (s.n + kChunk - 1) / kChunk;
     };
     auto load_chunk = [&](int c, int nch, int t0, int b) {    // by one thread
-        const int st = c % L::Stages, t = t0 + (rev ? nch - 1 - c : c) * kChunk;
+        const int st = c % L::Stages, t = t0 + (rev != STATE_ONLY ? nch - 1 - c : c) * kChunk;
         const int hx = h / r.x_div, hy = h / r.y_div, hz = h / r.z_div;
         uint8_t* base = smem + st * L::StageBytes;
         mbar_expect_tx(&full[st], L::StageBytes);
@@ -452,8 +452,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         __syncwarp();
         if (lane == 0) mbar_arrive(bar);
     };
-    // chunk c of the role's direction: its first token and number of tokens
-    auto chunk_at = [&](int c) { return (rev ? nch - 1 - c : c) * kChunk; };
+    // chunk c of the role's direction: its first token and number of tokens.
+    // (A segment's own state is summed from its end, so that what the next
+    // launch reads first is what this one leaves in L2.)
+    auto chunk_at = [&](int c) { return (rev != STATE_ONLY ? nch - 1 - c : c) * kChunk; };
     auto chunk_n = [&](int c) { return min(kChunk, n - chunk_at(c)); };
     constexpr uint32_t kFmt = F16 ? 0u : (1u << 7) | (1u << 10);
     constexpr uint32_t kTransB = 1u << 16;
@@ -896,11 +898,13 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 tmem_st16(tbase + row + L::Kt + buf * L::KtCols + 64 + half * 32 + 16, zero);
             }
         }
-        // state <- g^n state + (own state of chunk c), once its products are done
+        // state <- g^n state + (own state of chunk c), once its products are
+        // done; from the end: state <- state + g^(tokens after it) (own state)
+        float after = 1.f;
         auto advance = [&](int c) -> bool {
             if (!wait(bar_st, c)) return false;
             tc_fence_after();
-            const float keep = pw[chunk_n(c)], inv = 1.f / rs_done;
+            const float keep = STATE_ONLY ? 1.f : pw[chunk_n(c)], inv = 1.f / rs_done;
 #pragma unroll
             for (int blk = 0; blk < kCols / 32; ++blk) {
                 uint32_t s[32];
@@ -909,9 +913,13 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     const float own = F16 ? __uint_as_float(s[j]) * inv : __uint_as_float(s[j]);
-                    state[blk * 32 + j] = fmaf(keep, state[blk * 32 + j], own);
+                    if constexpr (STATE_ONLY)
+                        state[blk * 32 + j] = fmaf(after, own, state[blk * 32 + j]);
+                    else
+                        state[blk * 32 + j] = fmaf(keep, state[blk * 32 + j], own);
                 }
             }
+            after *= pw[chunk_n(c)];
             return true;
         };
         // the state in front of chunk c, and its copy for the carry product
