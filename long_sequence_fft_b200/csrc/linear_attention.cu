@@ -266,19 +266,25 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, const
     return false;
 }
 
-// Parts of the weighted keys and how they lie in TMEM: EXACT where the state
-// itself is a result (fp32, so all 24 bits of a weighted bf16 key count),
-// else 16 bits, far below the rounding of what the state then goes into.
+// Parts of the weighted keys and how they lie in TMEM.  EXACT: the state itself
+// is a result, fp32, so all 24 bits of a weighted bf16 key count (three parts;
+// fp16: two, 22 bits).  Else the state only goes into 16-bit outputs:
+//   64 channels: one part, rounded, and the carry's copy in two parts;
+//   128 channels (no room for a second copy): two parts, and the copy rounded.
+// Either way a carried term is rounded once, like a term of P.
 template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
 struct Layout {
-    // 64 channels: two parts are stacked on the 128 rows of one MMA, and the
-    // state is kept as the two rows' sum; 128 channels: one MMA a part
-    static constexpr bool Stacked = KP == 64;
-    static constexpr int Parts = F16 || !EXACT ? 2 : 3;
+    static constexpr bool Single = KP == 64 && !EXACT;
+    // 64 channels, EXACT: two parts are stacked on the 128 rows of one MMA,
+    // and the state is kept as the two rows' sum
+    static constexpr bool Stacked = KP == 64 && EXACT;
+    static constexpr int Parts = Single ? 1 : F16 || !EXACT ? 2 : 3;
+    // state warps with rows of the state
+    static constexpr int Live = Single ? 4 : kStateWarps;
     // beside P and the output three parts do not fit: the first one waits for
     // the others' columns
     static constexpr bool Late = !STATE_ONLY && Parts == 3;
-    static constexpr int KtCols = Stacked ? (Parts == 3 && !Late ? 128 : 64) : Late ? 128 : Parts * 64;
+    static constexpr int KtCols = Stacked ? (Parts == 3 && !Late ? 128 : 64) : Late ? 128 : Parts * 64;   // (Single: 64)
     // where the columns suffice, a chunk's keys are weighed while the last one's are multiplied
     static constexpr int KtBufs = STATE_ONLY || (KP == 64 && VP == 128 && !Late) ? 2 : 1;
     // the carry product has columns of its own (else P z is added to it, once it is weighted)
@@ -291,7 +297,7 @@ struct Layout {
     static constexpr int Threads = (RowWarps + kStateWarps + 4) * 32;
     static constexpr int XBytes = KP * kChunk * 2, ZBytes = VP * kChunk * 2;
     static constexpr int OffY = STATE_ONLY ? 0 : XBytes, OffZ = OffY + XBytes, StageBytes = OffZ + ZBytes;
-    static constexpr int CarryBytes = STATE_ONLY && !Stacked ? 0 : 128 * VP * 2;
+    static constexpr int CarryBytes = STATE_ONLY && !Stacked ? 0 : 128 * VP * 2;   // 64 channels: two copies
     static constexpr int Stages = StageBytes <= 49152 ? 4 : StageBytes <= 65536 ? 3 : 2;
     static constexpr int OffCarry = Stages * StageBytes;
     static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d| or 0, d = j - i in [-32, 31]
@@ -318,12 +324,12 @@ struct Layout {
 // MMAs (scores; carry product and P z; the chunk's own state), so that none
 // waits behind another's operands.  Only the carry product waits for the state, so chunks overlap.
 //
-// Rounding: P and the carry's copy are rounded once to the 16-bit type (their
-// products are the two halves of the output, each with the error of one
-// rounding of it); the weighted keys are split into two or three 16-bit parts
-// (Layout).  fp16 operands are scaled by exact powers of two (P by row, the
-// carry's copy by its largest value, the weighted keys by channel), so that
-// nothing overflows fp16's range or falls below it.
+// Rounding: P, and the weighted keys or the carry's copy (Layout), are rounded
+// once to the 16-bit type: their products are the two halves of the output,
+// each with the error of one rounding of it.  fp16 operands are scaled by
+// exact powers of two (P by row, the carry's copy by its largest value, the
+// weighted keys by channel), so that nothing overflows fp16's range or falls
+// below it.
 template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
 __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Threads, 1)
     la_kernel(const __grid_constant__ Params p) {
@@ -399,7 +405,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             for (int i = 14; i < 18; ++i) mbar_init(bars + i, 4);
             mbar_init(bar_st, 1);
             mbar_init(bar_kt, 1);
-            for (int i = 20; i < 26; ++i) mbar_init(bars + i, kStateWarps);
+            for (int i = 20; i < 26; ++i) mbar_init(bars + i, L::Live);
             mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
             if constexpr (F16)
                 for (int i = 0; i < L::Stages; ++i) mbar_init(&scale_ready[i], 1);
@@ -846,13 +852,17 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         // -------------------------------------------------- state rows ---
         // Two warps share 32 rows of the MMA: each keeps half of the columns
         // and weighs half of the tokens.  64 channels: one half of the rows
-        // carries the sums of the first (and third) part, the other, on the
-        // schedulers whose row warps have fewer columns, of the second.
+        // carries the sums of the first (and third) part, the other those of
+        // the second, or none (Single; its warps have nothing to do).  The
+        // half with less work is on the schedulers whose row warps have more
+        // columns: the last two forward in time, the first two backward.
         constexpr int kCols = VP / 2;
-        const int ts = tid - L::RowWarps * 32, sw = warp - L::RowWarps, bw = sw & 3, half = sw >> 2;
+        const int sw = warp - L::RowWarps, bw = sw & 3, half = sw >> 2;
         const int d = bw * 32 + lane;
-        const int ch = L::Stacked ? d & 63 : d;               // key channel
-        const bool second = L::Stacked && bw >= 2 == rev;     // (warp-uniform)
+        const int ch = KP == 64 ? d & 63 : d;                 // key channel
+        const bool heavy = KP == 128 || bw < 2 != rev;        // (warp-uniform)
+        const bool second = L::Stacked && heavy;
+        const int ts = L::Single ? half * 64 + ch : tid - L::RowWarps * 32;       // index among the live threads
         const int col0 = half * kCols;
         const uint32_t row = (uint32_t)(bw * 32) << 16;
         const int64_t mat = (int64_t)r.kd * r.vd;
@@ -889,7 +899,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     }
             }
         };
-        if (has_init && nch > 0) initial();
+        const bool live = !L::Single || heavy;
+        if (has_init && nch > 0 && live) initial();
         if (L::Stacked && L::KtCols == 128 && second) {
             // the third part has no second half
             const uint32_t zero[16] = {};
@@ -941,26 +952,35 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 #pragma unroll
                         for (int j = 0; j < kCols; ++j) amax = fmaxf(amax, fabsf(state[j]));
                         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
-                        if (lane == 0) amax_sh[(c & 1) * 8 + sw] = __uint_as_float(top);
+                        const int lw = L::Single ? half * 2 + (bw & 1) : sw;
+                        if (lane == 0) amax_sh[(c & 1) * 8 + lw] = __uint_as_float(top);
                         if (!sync_b()) return false;
 #pragma unroll
-                        for (int w = 0; w < kStateWarps; ++w) amax = fmaxf(amax, amax_sh[(c & 1) * 8 + w]);
+                        for (int w = 0; w < L::Live; ++w) amax = fmaxf(amax, amax_sh[(c & 1) * 8 + w]);
                         cs = fp16_scale(amax);
                     }
                     // the last carry product has read the copy
                     if (c > 0 && !wait(&bar_o[(c - 1) % NA], (c - 1) / NA)) return false;
                     if (F16 && ts == 0) carry_inv[c & 3] = 1.f / cs;
-                    uint8_t* dst = smem + L::OffCarry + d * 128;
+                    uint8_t* dst = smem + L::OffCarry + (L::Single ? ch : d) * 128;
 #pragma unroll
                     for (int q = 0; q < kCols / 8; ++q) {
-                        uint4 v;
-                        auto two = [&](int j) { return pack<F16>(state[q * 8 + j] * cs, state[q * 8 + j + 1] * cs); };
-                        v.x = two(0);
-                        v.y = two(2);
-                        v.z = two(4);
-                        v.w = two(6);
                         const int vc = col0 / 8 + q;
-                        *reinterpret_cast<uint4*>(dst + (vc >> 3) * 16384 + (((vc & 7) ^ (d & 7)) << 4)) = v;
+                        uint8_t* to = dst + (vc >> 3) * 16384 + (((vc & 7) ^ (d & 7)) << 4);
+                        uint32_t v[4], rest[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float2 f = make_float2(state[q * 8 + 2 * e], state[q * 8 + 2 * e + 1]);
+                            if constexpr (F16) f = mul2(f, make_float2(cs, cs));
+                            v[e] = pack<F16>(f.x, f.y);
+                            if constexpr (L::Single) {
+                                f = fma2(unpack<F16>(v[e]), make_float2(-1.f, -1.f), f);
+                                rest[e] = pack<F16>(f.x, f.y);
+                            }
+                        }
+                        *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
+                        if constexpr (L::Single)
+                            *reinterpret_cast<uint4*>(to + 64 * 128) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                     }
                     fence_proxy_async_smem();
                 }
@@ -987,7 +1007,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             // values must not meet the zeros of P and the weighted keys
             if (p.cu && nv < kChunk) {
                 const int rows = (nv + 15) / 16 * 16 - nv;
-                for (int e = ts; e < rows * (VP / 8); e += kStateWarps * 32) {
+                for (int e = ts; e < rows * (VP / 8); e += L::Live * 32) {
                     const int rr = nv + e / (VP / 8), vc = e % (VP / 8);
                     *reinterpret_cast<uint4*>(base + L::OffZ + (vc >> 3) * 16384 + rr * 128 + (vc & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
@@ -1000,10 +1020,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             // tokens 8 i + 2 (lane % 4) and + 1.
             const uint8_t* krow;
             {
-                const int tile = lane >> 3, c8 = (L::Stacked ? bw & 1 : bw) * 4 + (tile & 1);
+                const int tile = lane >> 3, c8 = (KP == 64 ? bw & 1 : bw) * 4 + (tile & 1);
                 krow = base + L::OffY + (c8 >> 3) * 16384 + (half * 64 + (tile >> 1) * 8 + (lane & 7)) * 128;
             }
-            const int c8 = (L::Stacked ? bw & 1 : bw) * 4 + (lane >> 3 & 1);
+            const int c8 = (KP == 64 ? bw & 1 : bw) * 4 + (lane >> 3 & 1);
             // tokens 32 th.. of the half, both groups of 16 channels: all loads first
             struct Raw {
                 uint32_t x[2][8];
@@ -1132,11 +1152,11 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             return true;
         };
         bool ok = true;
-        for (int c = 0; c < nch && ok; ++c) {
+        for (int c = 0; c < nch && ok && live; ++c) {
             ok = kAhead ? weigh_keys(c) && carry_on(c) : carry_on(c) && weigh_keys(c);
             rs_done = rs;
         }
-        if (ok && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
+        if (ok && live && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
             if (nch > 0)
                 ok = advance(nch - 1);
             else
@@ -1408,8 +1428,10 @@ cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
 
 template <int KP, int VP, bool STATE_ONLY>
 cudaError_t launch_type(const Params& p, bool f16, bool exact, int64_t ctas, cudaStream_t s) {
-    // (two fp16 parts have 22 bits: one kernel for both)
-    if (f16) return launch<KP, VP, true, STATE_ONLY, false>(p, ctas, s);
+    // (128 channels in fp16 have two parts either way)
+    if (f16)
+        return exact && KP == 64 ? launch<KP, VP, true, STATE_ONLY, KP == 64>(p, ctas, s)
+                                 : launch<KP, VP, true, STATE_ONLY, false>(p, ctas, s);
     return exact ? launch<KP, VP, false, STATE_ONLY, true>(p, ctas, s)
                  : launch<KP, VP, false, STATE_ONLY, false>(p, ctas, s);
 }
