@@ -306,9 +306,9 @@ struct Layout {
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // Segment, abort, TMEM base, scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int Bars = 27 + (F16 ? Stages : 0);
-    static constexpr int OffMax = OffBar + (Bars + 1) / 2 * 16;   // (fp16) channel scales of each stage's keys
-    static constexpr int Bytes = OffMax + (F16 ? Stages * KP * 4 : 0);
+    static constexpr int Bars = 27 + (F16 ? 4 : 0);
+    static constexpr int OffMax = OffBar + (Bars + 1) / 2 * 16;   // (fp16) channel maxima [2][state warps][32]
+    static constexpr int Bytes = OffMax + (F16 ? 2 * kStateWarps * 32 * 2 : 0);
     // TMEM columns
     static constexpr int S = 0, O = S + Groups * 128, Oc = SplitOut ? O + VP : O, C = STATE_ONLY ? 0 : Oc + VP,
                          Kt = C + VP;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     uint64_t* wgb_bar = bars + 24;
     uint64_t* c_free = bars + 25;                             // the chunk's own state read
     uint64_t* bar_fin = bars + 26;                            // all MMA warps
-    uint64_t* scale_ready = bars + 27;                        // [Stages] (fp16) scales of a stage's keys
+    uint64_t* pair_bar = bars + 27;                           // [4] (fp16) the two state warps of the same channels
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             for (int i = 20; i < 26; ++i) mbar_init(bars + i, L::Live);
             mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
             if constexpr (F16)
-                for (int i = 0; i < L::Stages; ++i) mbar_init(&scale_ready[i], 1);
+                for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
             *abort_flag = 0;
             fence_barrier_init();
             fence_proxy_async_smem();                         // the loads' engine sees the barriers
@@ -533,53 +533,16 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         }
     } else if (warp == L::ScoreWarp) {
         // ----------------------------------------- MMAs of the scores ---
-        // and (fp16) the scales of the keys, ahead of the state warps: each
-        // channel's largest weighted key comes out below 2^15.
-        const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
-        const uint32_t sb = smem_u32(smem);
-        bool ok = true;
-        for (int c = 0; c < nch && (F16 || !STATE_ONLY); ++c) {
-            const int st = c % L::Stages, ga = c % NA;
-            ok = wait(&full[st], c / L::Stages);
-            if (!ok) break;
-            if constexpr (F16) {
-                // eight channels a lane, every fourth (second) token
-                constexpr int kVecs = KP / 8, kRows = 32 / kVecs;
-                const int nv = chunk_n(c), v8 = lane % kVecs;
-                const uint8_t* keys = smem + st * L::StageBytes + L::OffY + (v8 >> 3) * 16384;
-                __half2 m[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m[e] = __float2half2_rn(0.f);
-#pragma unroll 4
-                for (int j = lane / kVecs; j < nv; j += kRows) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(keys + j * 128 + (((v8 & 7) ^ (j & 7)) << 4));
-                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t mag = w[e] & 0x7fff7fffu;
-                        m[e] = __hmax2(m[e], *reinterpret_cast<const __half2*>(&mag));
-                    }
-                }
-                __syncwarp();
-                float* scale = reinterpret_cast<float*>(smem + L::OffMax) + st * KP + v8 * 8;
-                const float up = fabsf(r.key_scale) * fmaxf(1.f, pw[nv]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-#pragma unroll
-                    for (int x = kVecs; x < 32; x *= 2) m[e] = __hmax2(m[e], __shfl_xor_sync(0xffffffffu, m[e], x));
-                    const float2 f = __half22float2(m[e]);
-                    if (lane < kVecs) {
-                        scale[2 * e] = f.x < 65536.f ? fp16_scale(f.x * up) : 1.f;
-                        scale[2 * e + 1] = f.y < 65536.f ? fp16_scale(f.y * up) : 1.f;
-                    }
-                }
-                arrive(&scale_ready[st]);
-            }
-            if constexpr (!STATE_ONLY) {
+        if constexpr (!STATE_ONLY) {
+            const uint32_t id_s = idesc_f16_f32(128, 128) | kFmt;
+            const uint32_t sb = smem_u32(smem);
+            bool ok = true;
+            for (int c = 0; c < nch; ++c) {
+                const int st = c % L::Stages, ga = c % NA;
                 const uint32_t base = sb + st * L::StageBytes;
                 const uint64_t d_x = make_desc(base, 16, 1024, 2), d_y = make_desc(base + L::OffY, 16, 1024, 2);
-                // the score tile's last P is used up
-                if (c >= NA) ok = wait(&bar_pv[ga], c / NA - 1);
+                // the loads are there, and the score tile's last P is used up
+                ok = wait(&full[st], c / L::Stages) && (c < NA || wait(&bar_pv[ga], c / NA - 1));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
@@ -589,9 +552,9 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 }
                 tc_commit_warp(&bar_s[ga]);
             }
+            if (!ok) fail();
+            tc_commit_warp(bar_fin);
         }
-        if (!ok) fail();
-        if constexpr (!STATE_ONLY) tc_commit_warp(bar_fin);
     } else if (warp == L::StateMmaWarp) {
         // ------------------------------ MMAs of the chunks' own states ---
         // The smallest parts first: the MMA truncates each sum, so few steps
@@ -989,6 +952,56 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             }
             return true;
         };
+        // 16 tokens (16 t.. of the half) of 16 channels (16 m.. of the warp's) of
+        // chunk c, transposed: a lane has channels lane / 4 and + 8, tokens
+        // 2 (lane % 4), + 1 and those + 8
+        const int c8 = (KP == 64 ? bw & 1 : bw) * 4 + (lane >> 3 & 1);
+        const uint8_t* krow =
+            smem + L::OffY + (c8 >> 3) * 16384 + (half * 64 + (lane >> 4) * 8 + (lane & 7)) * 128;
+        auto key_tile = [&](int c, int t, int m, uint32_t* x) {
+            ldmatrix4_trans(krow + c % L::Stages * L::StageBytes + t * 2048 + ((((c8 + 2 * m) & 7) ^ (lane & 7)) << 4), x);
+        };
+        // (fp16) the scale of each channel's keys of chunk c: its largest
+        // weighted key comes out below 2^15.  A warp has the maxima of its
+        // tokens, and exchanges them with the warp of the other tokens.
+        auto scale_keys = [&](int c) -> bool {
+            const int nv = chunk_n(c);
+            if (!wait(&full[c % L::Stages], c / L::Stages)) return false;
+            __half2 top[2][2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                top[m][0] = top[m][1] = __float2half2_rn(0.f);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    uint32_t x[4];
+                    key_tile(c, t, m, x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w = x[i] & 0x7fff7fffu;
+                        if (nv < kChunk) {
+                            const int left = nv - (half * 64 + 16 * t + (i >> 1) * 8 + 2 * (lane & 3));
+                            w &= left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+                        }
+                        top[m][i & 1] = __hmax2(top[m][i & 1], *reinterpret_cast<const __half2*>(&w));
+                    }
+                }
+            }
+            __half* ex = reinterpret_cast<__half*>(smem + L::OffMax) + (c & 1) * kStateWarps * 32;
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    __half2 x = top[m][y];
+                    x = __hmax2(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = __hmax2(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    if ((lane & 3) == 0) ex[sw * 32 + m * 16 + y * 8 + (lane >> 2)] = __hmax(__low2half(x), __high2half(x));
+                }
+            arrive(&pair_bar[bw]);
+            if (!wait(&pair_bar[bw], c)) return false;
+            const float f = fmaxf(__half2float(ex[sw * 32 + lane]), __half2float(ex[(sw ^ 4) * 32 + lane]));
+            rs = f < 65536.f ? fp16_scale(f * fabsf(r.key_scale) * fmaxf(1.f, pw[nv])) : 1.f;
+            return true;
+        };
         // the weighted keys of chunk c
         int kw_n = -1;
         auto weigh_keys = [&](int c) -> bool {
@@ -1018,12 +1031,6 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             // Parts of the weighted keys of 32 tokens and 16 channels a time,
             // transposed into TMEM: a lane has channels lane / 4 and + 8,
             // tokens 8 i + 2 (lane % 4) and + 1.
-            const uint8_t* krow;
-            {
-                const int tile = lane >> 3, c8 = (KP == 64 ? bw & 1 : bw) * 4 + (tile & 1);
-                krow = base + L::OffY + (c8 >> 3) * 16384 + (half * 64 + (tile >> 1) * 8 + (lane & 7)) * 128;
-            }
-            const int c8 = (KP == 64 ? bw & 1 : bw) * 4 + (lane >> 3 & 1);
             // tokens 32 th.. of the half, both groups of 16 channels: all loads first
             struct Raw {
                 uint32_t x[2][8];
@@ -1034,8 +1041,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        ldmatrix4_trans(krow + (2 * th + t) * 2048 + ((((c8 + 2 * m) & 7) ^ (lane & 7)) << 4),
-                                        k.x[m] + 4 * t);
+                        key_tile(c, 2 * th + t, m, k.x[m] + 4 * t);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     k.w[i] = *reinterpret_cast<const float2*>(kw + half * 64 + 32 * th + 8 * i + 2 * (lane & 3));
@@ -1080,10 +1086,6 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             using All = std::integral_constant<int, L::Parts>;
             const uint32_t t_kt = tbase + row + L::Kt + c % L::KtBufs * L::KtCols + half * 32;
             if (more) {
-                if constexpr (F16) {
-                    if (!wait(&scale_ready[st], c / L::Stages)) return false;
-                    rs = reinterpret_cast<const float*>(smem + L::OffMax)[st * KP + ch];
-                }
 #pragma unroll 1
                 for (int th = 0; th < 2; ++th) {
                     Raw k;
@@ -1153,7 +1155,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         };
         bool ok = true;
         for (int c = 0; c < nch && ok && live; ++c) {
-            ok = kAhead ? weigh_keys(c) && carry_on(c) : carry_on(c) && weigh_keys(c);
+            if (F16 && (c + 1 < nch || want_fin)) ok = scale_keys(c);
+            if (ok) ok = kAhead ? weigh_keys(c) && carry_on(c) : carry_on(c) && weigh_keys(c);
             rs_done = rs;
         }
         if (ok && live && want_fin && seq >= 0 && (nch > 0 || !STATE_ONLY)) {
