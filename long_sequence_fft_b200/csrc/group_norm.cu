@@ -63,11 +63,13 @@ template <typename T, int V>
 struct Pack {
     uint32_t w[V == 1 ? 1 : 4];
 };
-template <typename T, int V>
+// (LAST: no later pass reads it, so it need not stay in L2)
+template <typename T, int V, bool LAST = false>
 __device__ __forceinline__ Pack<T, V> load(const void* p, int64_t at) {
     Pack<T, V> r;
     if constexpr (V > 1) {
-        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p) + at);
+        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(p) + at);
+        const uint4 v = LAST ? __ldcs(src) : *src;
         r.w[0] = v.x;
         r.w[1] = v.y;
         r.w[2] = v.z;
@@ -120,7 +122,7 @@ __device__ __forceinline__ void store(void* p, int64_t at, const float (&f)[V]) 
             else
                 asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
         }
-        *reinterpret_cast<uint4*>(reinterpret_cast<T*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<T*>(p) + at), make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 // weight or bias of channels c .. c + V (in x's type or fp32)
@@ -371,9 +373,9 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
             for (int i = 0; i < I; ++i)
                 if (lane + i * LANES < nvec) {
                     const int at = c + i * LANES * V;
-                    px[i] = load<T, V>(a.x, r * a.ldx + at);
-                    pd[i] = load<T, V>(a.dy, r * a.ldy + at);
-                    if constexpr (GATED) pg[i] = load<T, V>(a.gate, r * a.ldg + at);
+                    px[i] = load<T, V, true>(a.x, r * a.ldx + at);
+                    pd[i] = load<T, V, true>(a.dy, r * a.ldy + at);
+                    if constexpr (GATED) pg[i] = load<T, V, true>(a.gate, r * a.ldg + at);
                 }
         }
     };
@@ -502,7 +504,7 @@ __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, flo
 // Statistics of a block's part of every group: per channel first, from sums
 // over a few positions at a time.
 template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 4) gn_stats(const Args a) {
+__global__ void __launch_bounds__(kThreads, 3) gn_stats(const Args a) {
     __shared__ float sh_m[V * kThreads], sh_q[V * kThreads], sh_n[kThreads];      // [row lane][channel of the block]
     const Tile t = tile_of<V>(a, blockIdx.x);
     const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
@@ -511,16 +513,25 @@ __global__ void __launch_bounds__(kThreads, 4) gn_stats(const Args a) {
     for (int j = 0; j < V; ++j) m[j] = q[j] = 0.f;
     if (t.on) {
         const int64_t row0 = (int64_t)t.n * a.S;
-        constexpr int kAhead = V == 8 ? 4 : 8;
-        for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
+        constexpr int kAhead = 4;
+        const int64_t step = (int64_t)t.rows * kAhead;
+        Pack<T, V> next[kAhead];
+        auto fetch = [&](int64_t s) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (s + k * t.rows < t.s1)
+                    next[k] = load<T, V>(a.x, (row0 + s + k * t.rows) * a.ldx + (int64_t)t.colv * V);
+        };
+        fetch(t.s0 + t.rl);
+        for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
             Pack<T, V> p[kAhead];
             float cnt = 0.f;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1) {
-                    p[k] = load<T, V>(a.x, (row0 + s + k * t.rows) * a.ldx + (int64_t)t.colv * V);
-                    cnt += 1.f;
-                }
+            for (int k = 0; k < kAhead; ++k) {
+                p[k] = next[k];
+                if (s + k * t.rows < t.s1) cnt += 1.f;
+            }
+            fetch(s + step);                                  // out during this step's work
             const float inv = 1.f / cnt, f = cnt / (n + cnt), nf = n * f;
             float sum[V], sq[V];
 #pragma unroll
@@ -635,15 +646,26 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply(const Args a) {
 #pragma unroll
     for (int j = 0; j < V; ++j) w[j] *= rstd[j];
     constexpr int kAhead = GATED ? 2 : 4;
-    for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
-        Pack<T, V> px[kAhead], pg[kAhead];
+    const int64_t step = (int64_t)t.rows * kAhead;
+    Pack<T, V> nx[kAhead], ng[GATED ? kAhead : 1];
+    auto fetch = [&](int64_t s) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
-                px[k] = load<T, V>(a.x, r * a.ldx + c);
-                if constexpr (GATED) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                nx[k] = load<T, V, true>(a.x, r * a.ldx + c);
+                if constexpr (GATED) ng[k] = load<T, V, true>(a.gate, r * a.ldg + c);
             }
+    };
+    fetch(t.s0 + t.rl);
+    for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
+        Pack<T, V> px[kAhead], pg[GATED ? kAhead : 1];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            px[k] = nx[k];
+            if constexpr (GATED) pg[k] = ng[k];
+        }
+        fetch(s + step);                                      // out during this step's work
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
@@ -695,17 +717,29 @@ __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_sums
         Stat<V, WHOLE> mean, rstd;
         mean.read(a.mean, (int64_t)t.n * a.G, c, a.D, 1);
         rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
-        constexpr int kAhead = 2;
-        for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
-            Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
+        constexpr int kAhead = GATED ? 1 : 2;
+        const int64_t step = (int64_t)t.rows * kAhead;
+        Pack<T, V> nx[kAhead], nd[kAhead], ng[GATED ? kAhead : 1];
+        auto fetch = [&](int64_t s) {
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (s + k * t.rows < t.s1) {
                     const int64_t r = row0 + s + k * t.rows;
-                    px[k] = load<T, V>(a.x, r * a.ldx + c);
-                    pd[k] = load<T, V>(a.dy, r * a.ldy + c);
-                    if constexpr (GATED) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                    nx[k] = load<T, V, false>(a.x, r * a.ldx + c);
+                    nd[k] = load<T, V, false>(a.dy, r * a.ldy + c);
+                    if constexpr (GATED) ng[k] = load<T, V, false>(a.gate, r * a.ldg + c);
                 }
+        };
+        fetch(t.s0 + t.rl);
+        for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
+            Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                px[k] = nx[k];
+                pd[k] = nd[k];
+                if constexpr (GATED) pg[k] = ng[k];
+            }
+            fetch(s + step);                                          // out during this step's work
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (s + k * t.rows < t.s1) {
@@ -789,17 +823,29 @@ __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_appl
     rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
     m1.read(a.sums, (int64_t)t.n * a.G, c, a.D, 2);
     m2.read(a.sums + 1, (int64_t)t.n * a.G, c, a.D, 2);
-    constexpr int kAhead = 2;
-    for (int64_t s = t.s0 + t.rl; s < t.s1; s += (int64_t)t.rows * kAhead) {
-        Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
+    constexpr int kAhead = GATED ? 1 : 2;
+    const int64_t step = (int64_t)t.rows * kAhead;
+    Pack<T, V> nx[kAhead], nd[kAhead], ng[GATED ? kAhead : 1];
+    auto fetch = [&](int64_t s) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
                 const int64_t r = row0 + s + k * t.rows;
-                px[k] = load<T, V>(a.x, r * a.ldx + c);
-                pd[k] = load<T, V>(a.dy, r * a.ldy + c);
-                if constexpr (GATED) pg[k] = load<T, V>(a.gate, r * a.ldg + c);
+                nx[k] = load<T, V, true>(a.x, r * a.ldx + c);
+                nd[k] = load<T, V, true>(a.dy, r * a.ldy + c);
+                if constexpr (GATED) ng[k] = load<T, V, true>(a.gate, r * a.ldg + c);
             }
+    };
+    fetch(t.s0 + t.rl);
+    for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
+        Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            px[k] = nx[k];
+            pd[k] = nd[k];
+            if constexpr (GATED) pg[k] = ng[k];
+        }
+        fetch(s + step);                                          // out during this step's work
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (s + k * t.rows < t.s1) {
