@@ -14,9 +14,14 @@
 //   variance take two passes over the registers.
 //   Sample form (S > 1, or wider groups): a pass for the statistics (or the
 //   sums of the backward pass), a small join, a second pass that applies them,
-//   in the opposite order of blocks so that it starts with what the first pass
-//   left in L2.  A thread keeps its channels, so groups need not be whole
-//   vectors.
+//   in the opposite order so that it starts with what the first pass left in
+//   L2.  A thread keeps its channels, so groups need not be whole vectors.
+// Arithmetic is packed, two fp32 values an instruction: with one at a time the
+// statistics took 15 instructions a value and the issue slots were the bound
+// (73 % of them used; 16 x 4095 x 760 fp16: 32.5 us, packed 28.6).  Results
+// are written, and data read for the last time is read, with streaming
+// accesses, which leave L2 to what the next pass reads (backward pass of
+// 32768 x 2048 bf16 with a gate: 147 -> 137 us).
 // Partial results are joined in a fixed order: runs repeat bit for bit.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -151,31 +156,117 @@ __device__ __forceinline__ void load_w(const void* w, int f32, int c, float none
     }
 }
 
-// exp and the reciprocal of the fast units: both within a few 2^-22 of the
-// value for the arguments where the sigmoid is not 0 or 1, below fp32's own
-// error of a sum of this kind.  (Beyond 2^126 __fdividef gives 0, the limit.)
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// fp32 arithmetic on V elements, two an instruction.  A second operand of one
+// element stands for all.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t r, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+}
+template <int V, int N>
+__device__ __forceinline__ uint64_t two(const float (&f)[N], int j) {
+    static_assert(N == V || N == 1);
+    return N == 1 ? two(f[0], f[0]) : two(f[j], f[j + (N > 1)]);
+}
+// r = a b + c
+template <int V, int NB, int NC>
+__device__ __forceinline__ void fma_v(float (&r)[V], const float (&a)[V], const float (&b)[NB], const float (&c)[NC]) {
+    if constexpr (V == 1) {
+        r[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            uint64_t d;
+            asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(two<V>(a, j)), "l"(two<V>(b, j)), "l"(two<V>(c, j)));
+            split(d, r[j], r[j + 1]);
+        }
+    }
+}
+template <int V, int NB>
+__device__ __forceinline__ void mul_v(float (&r)[V], const float (&a)[V], const float (&b)[NB]) {
+    if constexpr (V == 1) {
+        r[0] = a[0] * b[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            uint64_t d;
+            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(two<V>(a, j)), "l"(two<V>(b, j)));
+            split(d, r[j], r[j + 1]);
+        }
+    }
+}
+template <int V, int NB>
+__device__ __forceinline__ void add_v(float (&r)[V], const float (&a)[V], const float (&b)[NB]) {
+    if constexpr (V == 1) {
+        r[0] = a[0] + b[0];
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; j += 2) {
+            uint64_t d;
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(two<V>(a, j)), "l"(two<V>(b, j)));
+            split(d, r[j], r[j + 1]);
+        }
+    }
+}
+// the sum of V elements
+template <int V>
+__device__ __forceinline__ float sum_v(const float (&f)[V]) {
+    if constexpr (V == 1) {
+        return f[0];
+    } else {
+        float h[V / 2], k[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            h[j] = f[j];
+            k[j] = f[j + V / 2];
+        }
+        add_v<V / 2>(h, h, k);
+        return sum_v<V / 2>(h);
+    }
+}
+
+// s = 1 / (1 + exp(-f)) with the fast units' exp2 and reciprocal: both within
+// a few 2^-22 of the value for the arguments where the sigmoid is not 0 or 1,
+// below fp32's own error of a sum of this kind.  (An infinite exp gives 0.)
+template <int V>
+__device__ __forceinline__ void sigmoid(const float (&f)[V], float (&s)[V]) {
+    const float scale[1] = {-1.4426950408889634f}, one[1] = {1.f};
+    mul_v<V>(s, f, scale);
+#pragma unroll
+    for (int j = 0; j < V; ++j) asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(s[j]));
+    add_v<V>(s, s, one);
+#pragma unroll
+    for (int j = 0; j < V; ++j) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(s[j]));
+}
 
 // f <- act(f); slope (if wanted): act'.  One uniform branch a vector.
 template <int V, bool SLOPE>
 __device__ __forceinline__ void activate(float (&f)[V], float (&slope)[V], int act) {
+    const float one[1] = {1.f}, minus[1] = {-1.f};
     if (act == FFTCONV_ACT_NONE) {
         if (SLOPE)
 #pragma unroll
             for (int j = 0; j < V; ++j) slope[j] = 1.f;
     } else if (act == FFTCONV_ACT_SILU) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float s = sigmoid(f[j]);
-            if (SLOPE) slope[j] = s * fmaf(f[j], 1.f - s, 1.f);
-            f[j] *= s;
+        float s[V];
+        sigmoid<V>(f, s);
+        mul_v<V>(f, f, s);
+        if (SLOPE) {                                          // s + f s (1 - s)
+            fma_v<V>(slope, s, minus, one);
+            fma_v<V>(slope, f, slope, s);
         }
     } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            f[j] = sigmoid(f[j]);
-            if (SLOPE) slope[j] = f[j] * (1.f - f[j]);
+        float s[V];
+        sigmoid<V>(f, s);
+        if (SLOPE) {
+            fma_v<V>(slope, s, minus, one);
+            mul_v<V>(slope, slope, s);
         }
+#pragma unroll
+        for (int j = 0; j < V; ++j) f[j] = s[j];
     }
 }
 // y of n (in place): act(n), or n act(gate)
@@ -184,8 +275,7 @@ __device__ __forceinline__ void finish(float (&n)[V], float (&gate)[V], int act)
     float none[V];
     if constexpr (GATED) {
         activate<V, false>(gate, none, act);
-#pragma unroll
-        for (int j = 0; j < V; ++j) n[j] *= gate[j];
+        mul_v<V>(n, n, gate);
     } else {
         activate<V, false>(n, none, act);
     }
@@ -196,16 +286,14 @@ __device__ __forceinline__ void start(float (&n)[V], float (&dy)[V], float (&gat
     float slope[V];
     if constexpr (GATED) {
         activate<V, true>(gate, slope, act);
+        mul_v<V>(n, n, slope);
+        mul_v<V>(n, n, dy);
+        mul_v<V>(dy, dy, gate);
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float d = dy[j];
-            dy[j] = d * gate[j];
-            gate[j] = d * n[j] * slope[j];
-        }
+        for (int j = 0; j < V; ++j) gate[j] = n[j];
     } else {
         activate<V, true>(n, slope, act);
-#pragma unroll
-        for (int j = 0; j < V; ++j) dy[j] *= slope[j];
+        mul_v<V>(dy, dy, slope);
     }
 }
 
@@ -274,20 +362,18 @@ __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(con
             for (int i = 0; i < I; ++i)
                 if (in && lane + i * LANES < nvec) {
                     unpack<T, V>(x[u][i], f[i]);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) sum += f[i][j];
+                    sum += sum_v<V>(f[i]);
                 }
-            const float mean = lanes_sum<LANES>(sum) * inv;
+            const float mean = lanes_sum<LANES>(sum) * inv, minus_mean[1] = {-mean};
 #pragma unroll
             for (int i = 0; i < I; ++i)
                 if (in && lane + i * LANES < nvec) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        f[i][j] -= mean;
-                        sq = fmaf(f[i][j], f[i][j], sq);
-                    }
+                    float f2[V];
+                    add_v<V>(f[i], f[i], minus_mean);
+                    mul_v<V>(f2, f[i], f[i]);
+                    sq += sum_v<V>(f2);
                 }
-            const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(sq), inv, a.eps));
+            const float rstd = rsqrtf(fmaf(lanes_sum<LANES>(sq), inv, a.eps)), scale[1] = {rstd};
             if (!in) continue;
             if (lane == 0 && a.mean) {
                 a.mean[r * a.G + g] = mean;
@@ -298,15 +384,14 @@ __global__ void __launch_bounds__(kThreads, I == 1 ? 3 : 2) gn_token_forward(con
                 if (lane + i * LANES >= nvec) continue;
                 float gate[V];
                 if constexpr (GATED) unpack<T, V>(gt[u][i], gate);
+                mul_v<V>(f[i], f[i], scale);
                 if constexpr (kKeep) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * rstd, w[i][j], b[i][j]);
+                    fma_v<V>(f[i], f[i], w[i], b[i]);
                 } else {
                     float wi[V], bi[V];
                     load_w<T, V>(a.w, a.w_f32, c + i * LANES * V, 1.f, wi);
                     load_w<T, V>(a.b, a.w_f32, c + i * LANES * V, 0.f, bi);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) f[i][j] = fmaf(f[i][j] * rstd, wi[j], bi[j]);
+                    fma_v<V>(f[i], f[i], wi, bi);
                 }
                 finish<V, GATED>(f[i], gate, a.act);
                 store<T, V>(a.y, r * a.C + c + i * LANES * V, f[i]);
@@ -384,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
     for (int64_t base = (int64_t)blockIdx.x * rsubs; base < a.N; base += stride) {
         const int64_t r = base + rs;
         const bool in = on && r < a.N;
-        const float scale = rstd;
+        const float minus_mean[1] = {-mean}, scale[1] = {rstd};
         float xh[I][V], dn[I][V], gt[I][V], s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < I; ++i)
@@ -392,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
                 unpack<T, V>(px[i], xh[i]);
                 unpack<T, V>(pd[i], dn[i]);
                 if constexpr (GATED) unpack<T, V>(pg[i], gt[i]);
-#pragma unroll
-                for (int j = 0; j < V; ++j) xh[i][j] = (xh[i][j] - mean) * rstd;
+                add_v<V>(xh[i], xh[i], minus_mean);
+                mul_v<V>(xh[i], xh[i], scale);
             }
         fetch(r + stride);                                    // the next row's loads are out during this one's work
 #pragma unroll
@@ -410,27 +495,24 @@ __global__ void __launch_bounds__(kThreads, I* V <= 8 ? 3 : 2) gn_token_backward
                     bi[j] = b[i][j];
                 }
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j) n[j] = fmaf(xh[i][j], wi[j], bi[j]);
+            fma_v<V>(n, xh[i], wi, bi);
             start<V, GATED>(n, dn[i], gt[i], a.act);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                dw[i][j] = fmaf(dn[i][j], xh[i][j], dw[i][j]);
-                db[i][j] += dn[i][j];
-                dn[i][j] *= wi[j];
-                s1 += dn[i][j];
-                s2 = fmaf(dn[i][j], xh[i][j], s2);
-            }
+            fma_v<V>(dw[i], dn[i], xh[i], dw[i]);
+            add_v<V>(db[i], db[i], dn[i]);
+            mul_v<V>(dn[i], dn[i], wi);
+            s1 += sum_v<V>(dn[i]);
+            mul_v<V>(n, dn[i], xh[i]);
+            s2 += sum_v<V>(n);
             if constexpr (GATED) store<T, V>(a.dgate, r * a.C + c + i * LANES * V, gt[i]);
         }
-        s1 = lanes_sum<LANES>(s1) * inv;
-        s2 = lanes_sum<LANES>(s2) * inv;
+        const float minus_s1[1] = {-lanes_sum<LANES>(s1) * inv}, minus_s2[1] = {-lanes_sum<LANES>(s2) * inv};
         if (!in) continue;
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             if (lane + i * LANES >= nvec) continue;
-#pragma unroll
-            for (int j = 0; j < V; ++j) dn[i][j] = scale * (dn[i][j] - s1 - xh[i][j] * s2);
+            add_v<V>(dn[i], dn[i], minus_s1);
+            fma_v<V>(dn[i], xh[i], minus_s2, dn[i]);
+            mul_v<V>(dn[i], dn[i], scale);
             store<T, V>(a.dx, r * a.C + c + i * LANES * V, dn[i]);
         }
     }
@@ -467,16 +549,20 @@ __global__ void __launch_bounds__(1024) gn_sum_parts(const Args a) { sum_parts(a
 
 // ----------------------------------------------------------- sample form ---
 //
-// A block takes a range of a sample's positions (chunk) and up to 256 vectors
-// of its channels: thread = (vector column, row lane).
+// A block takes every chunks-th part of a sample's positions and up to 256
+// vectors of its channels: thread = (vector column, row lane).  The blocks of
+// a sample so read one window of memory together: 8 x 4096 x 768 fp32 applies
+// the backward pass in 38.2 us, 41.1 with a contiguous range for each block.
 
 struct Tile {
     int n, chunk, colv, rl, rows;             // rows: row lanes
-    int64_t s0, s1;
+    int count;                                // positions of this thread: first, first + step, ...
+    int64_t first, step;                      // (counted over all samples)
     bool on;
 };
 template <int V>
-__device__ __forceinline__ Tile tile_of(const Args& a, int bx) {
+__device__ __forceinline__ Tile tile_of(const Args& a, bool backwards) {
+    const int bx = blockIdx.x;
     Tile t;
     t.n = bx / a.chunks;
     t.chunk = bx % a.chunks;
@@ -485,11 +571,82 @@ __device__ __forceinline__ Tile tile_of(const Args& a, int bx) {
     t.rl = threadIdx.x / width;
     t.colv = blockIdx.y * kThreads + threadIdx.x % width;
     t.on = t.rl < t.rows;
-    const int64_t per = (a.S + a.chunks - 1) / a.chunks;
-    t.s0 = min((int64_t)t.chunk * per, a.S);
-    t.s1 = min(t.s0 + per, a.S);
+    const int64_t s0 = (int64_t)t.chunk * t.rows + t.rl;
+    t.step = (int64_t)a.chunks * t.rows;
+    t.first = (int64_t)t.n * a.S + s0;
+    t.count = s0 < a.S ? (int)((a.S - s0 + t.step - 1) / t.step) : 0;
+    if (backwards) {
+        t.first += (t.count - 1) * t.step;
+        t.step = -t.step;
+    }
     return t;
 }
+// A thread's positions, B at a time, the next ones' loads out during the work
+// on these; fewer than B at the end one by one.  fetch(row) takes the next
+// position, work(rows, integral_constant<n>) the n next ones.
+template <int B, typename Row, typename Fetch, typename Work>
+__device__ __forceinline__ void walk(int count, Fetch&& fetch, Work&& work) {
+    Row next[B], now[B];
+    int left = count;
+    if (left >= B)
+#pragma unroll
+        for (int k = 0; k < B; ++k) fetch(next[k]);
+    while (left >= B) {
+#pragma unroll
+        for (int k = 0; k < B; ++k) now[k] = next[k];
+        left -= B;
+        if (left >= B)
+#pragma unroll
+            for (int k = 0; k < B; ++k) fetch(next[k]);
+        work(now, std::integral_constant<int, B>{});
+    }
+    if constexpr (B > 1) {
+#pragma unroll
+        for (int k = 0; k < B - 1; ++k)
+            if (k < left) fetch(now[k]);
+#pragma unroll 1
+        for (int k = 0; k < left; ++k) {
+            work(now, std::integral_constant<int, 1>{});
+#pragma unroll
+            for (int i = 0; i + 1 < B; ++i) now[i] = now[i + 1];
+        }
+    }
+}
+// The vectors of one position (those that there are), and where they come from.
+template <typename T, int V, bool WITH_DY, bool GATED>
+struct Row {
+    Pack<T, V> x, dy, gate;
+};
+template <typename T, int V, bool WITH_DY, bool GATED, bool LAST>
+struct Source {
+    const T *x, *dy, *gate;
+    int64_t sx, sd, sg;
+    __device__ __forceinline__ Source(const Args& a, const Tile& t) {
+        const int64_t c = (int64_t)t.colv * V;
+        x = reinterpret_cast<const T*>(a.x) + t.first * a.ldx + c;
+        sx = t.step * a.ldx;
+        if constexpr (WITH_DY) {
+            dy = reinterpret_cast<const T*>(a.dy) + t.first * a.ldy + c;
+            sd = t.step * a.ldy;
+        }
+        if constexpr (GATED) {
+            gate = reinterpret_cast<const T*>(a.gate) + t.first * a.ldg + c;
+            sg = t.step * a.ldg;
+        }
+    }
+    __device__ __forceinline__ void operator()(Row<T, V, WITH_DY, GATED>& r) {
+        r.x = load<T, V, LAST>(x, 0);
+        x += sx;
+        if constexpr (WITH_DY) {
+            r.dy = load<T, V, LAST>(dy, 0);
+            dy += sd;
+        }
+        if constexpr (GATED) {
+            r.gate = load<T, V, LAST>(gate, 0);
+            gate += sg;
+        }
+    }
+};
 
 // (count, mean, sum of squared deviations) of two sets joined
 __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, float m2, float q2) {
@@ -506,63 +663,44 @@ __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, flo
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads, 3) gn_stats(const Args a) {
     __shared__ float sh_m[V * kThreads], sh_q[V * kThreads], sh_n[kThreads];      // [row lane][channel of the block]
-    const Tile t = tile_of<V>(a, blockIdx.x);
+    const Tile t = tile_of<V>(a, false);
     const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
     float n = 0.f, m[V], q[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) m[j] = q[j] = 0.f;
-    if (t.on) {
-        const int64_t row0 = (int64_t)t.n * a.S;
-        constexpr int kAhead = 4;
-        const int64_t step = (int64_t)t.rows * kAhead;
-        Pack<T, V> next[kAhead];
-        auto fetch = [&](int64_t s) {
+    if (t.on)
+        walk<4, Row<T, V, false, false>>(t.count, Source<T, V, false, false, false>(a, t), [&](auto& row, auto batch) {
+            constexpr int B = decltype(batch)::value;
+            const float f = (float)B / (n + (float)B);
+            const float inv[1] = {1.f / (float)B}, minus[1] = {-1.f}, part[1] = {f}, both[1] = {n * f};
+            float x[V], sum[V], sq[V], d[V];
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1)
-                    next[k] = load<T, V>(a.x, (row0 + s + k * t.rows) * a.ldx + (int64_t)t.colv * V);
-        };
-        fetch(t.s0 + t.rl);
-        for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
-            Pack<T, V> p[kAhead];
-            float cnt = 0.f;
+            for (int k = 0; k < B; ++k) {
+                unpack<T, V>(row[k].x, x);
+                if (k == 0)
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                p[k] = next[k];
-                if (s + k * t.rows < t.s1) cnt += 1.f;
+                    for (int j = 0; j < V; ++j) sum[j] = x[j];
+                else
+                    add_v<V>(sum, sum, x);
             }
-            fetch(s + step);                                  // out during this step's work
-            const float inv = 1.f / cnt, f = cnt / (n + cnt), nf = n * f;
-            float sum[V], sq[V];
+            if (B > 1) mul_v<V>(sum, sum, inv);
 #pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] = sq[j] = 0.f;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1) {
-                    float x[V];
-                    unpack<T, V>(p[k], x);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) sum[j] += x[j];
-                }
-#pragma unroll
-            for (int j = 0; j < V; ++j) sum[j] *= inv;
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1) {
-                    float x[V];
-                    unpack<T, V>(p[k], x);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) sq[j] = fmaf(x[j] - sum[j], x[j] - sum[j], sq[j]);
-                }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = sum[j] - m[j];
-                m[j] = fmaf(d, f, m[j]);
-                q[j] += fmaf(d * d, nf, sq[j]);
+            for (int k = 0; k < B; ++k) {
+                unpack<T, V>(row[k].x, x);
+                fma_v<V>(d, sum, minus, x);
+                if (k == 0)
+                    mul_v<V>(sq, d, d);
+                else
+                    fma_v<V>(sq, d, d, sq);
             }
-            n += cnt;
-        }
-    }
+            // joined with the positions before
+            fma_v<V>(d, m, minus, sum);
+            fma_v<V>(m, d, part, m);
+            mul_v<V>(d, d, d);
+            fma_v<V>(sq, d, both, sq);
+            add_v<V>(q, q, sq);
+            n += (float)B;
+        });
     if (t.on) {
         const int at = t.rl * width + (t.colv - (int)blockIdx.y * kThreads);
 #pragma unroll
@@ -624,7 +762,10 @@ __global__ void __launch_bounds__(kThreads) gn_join_stats(const Args a) {
 template <int V, bool WHOLE>
 struct Stat {
     float v[WHOLE ? 1 : V];
-    __device__ __forceinline__ float operator[](int j) const { return v[WHOLE ? 0 : j]; }
+    __device__ __forceinline__ void negate() {
+#pragma unroll
+        for (int j = 0; j < (WHOLE ? 1 : V); ++j) v[j] = -v[j];
+    }
     __device__ __forceinline__ void read(const float* p, int64_t row, int c, int D, int step) {
 #pragma unroll
         for (int j = 0; j < (WHOLE ? 1 : V); ++j) v[j] = p[(row + (c + j) / D) * step];
@@ -633,68 +774,46 @@ struct Stat {
 
 template <typename T, int V, bool WHOLE, bool GATED>
 __global__ void __launch_bounds__(kThreads, 3) gn_apply(const Args a) {
-    const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
+    const Tile t = tile_of<V>(a, true);
     if (!t.on) return;
     const int c = t.colv * V;
-    const int64_t row0 = (int64_t)t.n * a.S;
     float w[V], b[V];
     load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
     load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
     Stat<V, WHOLE> mean, rstd;
     mean.read(a.mean, (int64_t)t.n * a.G, c, a.D, 1);
     rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
+    mul_v<V>(w, w, rstd.v);
+    mean.negate();
+    T* y = reinterpret_cast<T*>(a.y) + t.first * a.C + c;
+    walk<GATED ? 2 : 4, Row<T, V, false, GATED>>(
+        t.count, Source<T, V, false, GATED, true>(a, t), [&](auto& row, auto batch) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) w[j] *= rstd[j];
-    constexpr int kAhead = GATED ? 2 : 4;
-    const int64_t step = (int64_t)t.rows * kAhead;
-    Pack<T, V> nx[kAhead], ng[GATED ? kAhead : 1];
-    auto fetch = [&](int64_t s) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (s + k * t.rows < t.s1) {
-                const int64_t r = row0 + s + k * t.rows;
-                nx[k] = load<T, V, true>(a.x, r * a.ldx + c);
-                if constexpr (GATED) ng[k] = load<T, V, true>(a.gate, r * a.ldg + c);
-            }
-    };
-    fetch(t.s0 + t.rl);
-    for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
-        Pack<T, V> px[kAhead], pg[GATED ? kAhead : 1];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            px[k] = nx[k];
-            if constexpr (GATED) pg[k] = ng[k];
-        }
-        fetch(s + step);                                      // out during this step's work
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (s + k * t.rows < t.s1) {
+            for (int k = 0; k < decltype(batch)::value; ++k) {
                 float f[V], g[V];
-                unpack<T, V>(px[k], f);
-                if constexpr (GATED) unpack<T, V>(pg[k], g);
-#pragma unroll
-                for (int j = 0; j < V; ++j) f[j] = fmaf(f[j] - mean[j], w[j], b[j]);
+                unpack<T, V>(row[k].x, f);
+                if constexpr (GATED) unpack<T, V>(row[k].gate, g);
+                add_v<V>(f, f, mean.v);
+                fma_v<V>(f, f, w, b);
                 finish<V, GATED>(f, g, a.act);
-                store<T, V>(a.y, (row0 + s + k * t.rows) * a.C + c, f);
+                store<T, V>(y, 0, f);
+                y += t.step * a.C;
             }
-    }
+        });
 }
 
-// xh, dn and dgate of one vector
+// xh, dn and dgate of one vector (mean: negated)
 template <typename T, int V, bool WHOLE, bool GATED>
-__device__ __forceinline__ void grad_of(const Args& a, const Pack<T, V>& px, const Pack<T, V>& pd,
-                                        const Pack<T, V>& pg, const Stat<V, WHOLE>& mean, const Stat<V, WHOLE>& rstd,
-                                        const float (&w)[V], const float (&b)[V], float (&xh)[V], float (&dn)[V],
-                                        float (&dg)[V]) {
+__device__ __forceinline__ void grad_of(const Args& a, const Row<T, V, true, GATED>& row, const Stat<V, WHOLE>& mean,
+                                        const Stat<V, WHOLE>& rstd, const float (&w)[V], const float (&b)[V],
+                                        float (&xh)[V], float (&dn)[V], float (&dg)[V]) {
     float n[V];
-    unpack<T, V>(px, xh);
-    unpack<T, V>(pd, dn);
-    if constexpr (GATED) unpack<T, V>(pg, dg);
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        xh[j] = (xh[j] - mean[j]) * rstd[j];
-        n[j] = fmaf(xh[j], w[j], b[j]);
-    }
+    unpack<T, V>(row.x, xh);
+    unpack<T, V>(row.dy, dn);
+    if constexpr (GATED) unpack<T, V>(row.gate, dg);
+    add_v<V>(xh, xh, mean.v);
+    mul_v<V>(xh, xh, rstd.v);
+    fma_v<V>(n, xh, w, b);
     start<V, GATED>(n, dn, dg, a.act);
 }
 
@@ -703,55 +822,30 @@ __device__ __forceinline__ void grad_of(const Args& a, const Pack<T, V>& px, con
 template <typename T, int V, bool WHOLE, bool GATED>
 __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_sums(const Args a) {
     __shared__ float sh[2][kThreads * V];
-    const Tile t = tile_of<V>(a, blockIdx.x);
+    const Tile t = tile_of<V>(a, false);
     const int width = min(a.C / V - (int)blockIdx.y * kThreads, kThreads);
     float s1[V], s2[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) s1[j] = s2[j] = 0.f;
     const int c = t.colv * V;
     if (t.on) {
-        const int64_t row0 = (int64_t)t.n * a.S;
-            float w[V], b[V];
+        float w[V], b[V];
         load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
         load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
         Stat<V, WHOLE> mean, rstd;
         mean.read(a.mean, (int64_t)t.n * a.G, c, a.D, 1);
         rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
-        constexpr int kAhead = GATED ? 1 : 2;
-        const int64_t step = (int64_t)t.rows * kAhead;
-        Pack<T, V> nx[kAhead], nd[kAhead], ng[GATED ? kAhead : 1];
-        auto fetch = [&](int64_t s) {
+        mean.negate();
+        walk<GATED ? 1 : 2, Row<T, V, true, GATED>>(
+            t.count, Source<T, V, true, GATED, false>(a, t), [&](auto& row, auto batch) {
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1) {
-                    const int64_t r = row0 + s + k * t.rows;
-                    nx[k] = load<T, V, false>(a.x, r * a.ldx + c);
-                    nd[k] = load<T, V, false>(a.dy, r * a.ldy + c);
-                    if constexpr (GATED) ng[k] = load<T, V, false>(a.gate, r * a.ldg + c);
-                }
-        };
-        fetch(t.s0 + t.rl);
-        for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
-            Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                px[k] = nx[k];
-                pd[k] = nd[k];
-                if constexpr (GATED) pg[k] = ng[k];
-            }
-            fetch(s + step);                                          // out during this step's work
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (s + k * t.rows < t.s1) {
+                for (int k = 0; k < decltype(batch)::value; ++k) {
                     float xh[V], dn[V], dg[V];
-                    grad_of<T, V, WHOLE, GATED>(a, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        s1[j] = fmaf(dn[j], xh[j], s1[j]);
-                        s2[j] += dn[j];
-                    }
+                    grad_of<T, V, WHOLE, GATED>(a, row[k], mean, rstd, w, b, xh, dn, dg);
+                    fma_v<V>(s1, dn, xh, s1);
+                    add_v<V>(s2, s2, dn);
                 }
-        }
+            });
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             sh[0][(t.rl * width + t.colv - (int)blockIdx.y * kThreads) * V + j] = s1[j];
@@ -811,10 +905,9 @@ __global__ void __launch_bounds__(1024) gn_join_sums(const Args a) {
 
 template <typename T, int V, bool WHOLE, bool GATED>
 __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_apply(const Args a) {
-    const Tile t = tile_of<V>(a, gridDim.x - 1 - blockIdx.x);
+    const Tile t = tile_of<V>(a, true);
     if (!t.on) return;
     const int c = t.colv * V;
-    const int64_t row0 = (int64_t)t.n * a.S;
     float w[V], b[V];
     load_w<T, V>(a.w, a.w_f32, c, 1.f, w);
     load_w<T, V>(a.b, a.w_f32, c, 0.f, b);
@@ -823,41 +916,27 @@ __global__ void __launch_bounds__(kThreads, WHOLE || V < 8 ? 3 : 2) gn_grad_appl
     rstd.read(a.rstd, (int64_t)t.n * a.G, c, a.D, 1);
     m1.read(a.sums, (int64_t)t.n * a.G, c, a.D, 2);
     m2.read(a.sums + 1, (int64_t)t.n * a.G, c, a.D, 2);
-    constexpr int kAhead = GATED ? 1 : 2;
-    const int64_t step = (int64_t)t.rows * kAhead;
-    Pack<T, V> nx[kAhead], nd[kAhead], ng[GATED ? kAhead : 1];
-    auto fetch = [&](int64_t s) {
+    mean.negate();
+    m1.negate();
+    m2.negate();
+    T *dx = reinterpret_cast<T*>(a.dx) + t.first * a.C + c, *dgate = reinterpret_cast<T*>(a.dgate) + t.first * a.C + c;
+    walk<GATED ? 1 : 2, Row<T, V, true, GATED>>(
+        t.count, Source<T, V, true, GATED, true>(a, t), [&](auto& row, auto batch) {
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (s + k * t.rows < t.s1) {
-                const int64_t r = row0 + s + k * t.rows;
-                nx[k] = load<T, V, true>(a.x, r * a.ldx + c);
-                nd[k] = load<T, V, true>(a.dy, r * a.ldy + c);
-                if constexpr (GATED) ng[k] = load<T, V, true>(a.gate, r * a.ldg + c);
-            }
-    };
-    fetch(t.s0 + t.rl);
-    for (int64_t s = t.s0 + t.rl; s < t.s1; s += step) {
-        Pack<T, V> px[kAhead], pd[kAhead], pg[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            px[k] = nx[k];
-            pd[k] = nd[k];
-            if constexpr (GATED) pg[k] = ng[k];
-        }
-        fetch(s + step);                                          // out during this step's work
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (s + k * t.rows < t.s1) {
-                const int64_t r = row0 + s + k * t.rows;
+            for (int k = 0; k < decltype(batch)::value; ++k) {
                 float xh[V], dn[V], dg[V];
-                grad_of<T, V, WHOLE, GATED>(a, px[k], pd[k], pg[k], mean, rstd, w, b, xh, dn, dg);
-                if constexpr (GATED) store<T, V>(a.dgate, r * a.C + c, dg);
-#pragma unroll
-                for (int j = 0; j < V; ++j) dn[j] = rstd[j] * (dn[j] * w[j] - m1[j] - xh[j] * m2[j]);
-                store<T, V>(a.dx, r * a.C + c, dn);
+                grad_of<T, V, WHOLE, GATED>(a, row[k], mean, rstd, w, b, xh, dn, dg);
+                if constexpr (GATED) {
+                    store<T, V>(dgate, 0, dg);
+                    dgate += t.step * a.C;
+                }
+                fma_v<V>(dn, dn, w, m1.v);
+                fma_v<V>(dn, xh, m2.v, dn);
+                mul_v<V>(dn, dn, rstd.v);
+                store<T, V>(dx, 0, dn);
+                dx += t.step * a.C;
             }
-    }
+        });
 }
 
 // ------------------------------------------------------------------ host ---
