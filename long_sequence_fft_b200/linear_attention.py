@@ -7,6 +7,7 @@
 from __future__ import annotations
 
 import ctypes
+import struct
 
 from . import BF16, F16, _check, _i64, _lib, _vp
 from . import _ptr as _p
@@ -20,6 +21,11 @@ class _Shape(ctypes.Structure):
                 ("K", _i64), ("V", _i64), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
                 ("zero_rest", ctypes.c_int32), ("q_stride", _i64 * 3), ("k_stride", _i64 * 3),
                 ("v_stride", _i64 * 3), ("o_stride", _i64 * 3)]
+
+
+# its bytes: quicker to write than the fields of a ctypes structure
+_pack_shape = struct.Struct("=9qifi4x12q")
+assert _pack_shape.size == ctypes.sizeof(_Shape)
 
 
 def _dtype_of(t, name):
@@ -109,13 +115,13 @@ def _check_readable(*tensors):
 
 def _shape_of(q, k, v, o_shape_stride, log_decay, nseq, scale, zero_rest):
     (B, T, Hq, K), Hk, (Hv, V) = q.shape, k.shape[2], v.shape[2:]
-    return _Shape(B, T, nseq, log_decay.shape[0], Hq, Hk, Hv, K, V, _dtype_of(q, "q"), scale, zero_rest,
-                  q.stride()[:3], k.stride()[:3], v.stride()[:3], o_shape_stride[:3])
+    return _pack_shape.pack(B, T, nseq, log_decay.shape[0], Hq, Hk, Hv, K, V, _dtype_of(q, "q"), scale, zero_rest,
+                            *q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *o_shape_stride[:3])
 
 
 def _workspace(shape, backward, device):
     import torch
-    n = int(_lib.fftconv_linear_attention_workspace_bytes(ctypes.byref(shape), backward))
+    n = int(_lib.fftconv_linear_attention_workspace_bytes(shape, backward))
     return (torch.empty(n, dtype=torch.uint8, device=device) if n else None), n
 
 
@@ -133,7 +139,7 @@ def _forward(q, k, v, log_decay, initial, cu, scale, want_state, out, stream):
         if want_state:
             state = torch.empty((nseq if cu is not None else B, H, K, V), dtype=torch.float32, device=q.device)
         ws, n = _workspace(shape, 0, q.device)
-        _check(_lib.fftconv_linear_attention(ctypes.byref(shape), _p(q), _p(k), _p(v), _p(log_decay), _p(initial),
+        _check(_lib.fftconv_linear_attention(shape, _p(q), _p(k), _p(v), _p(log_decay), _p(initial),
                                              _p(cu), _p(out), _p(state), _p(ws), n, handle))
     return out, state
 
@@ -146,7 +152,7 @@ def _backward(q, k, v, log_decay, initial, cu, scale, do, dstate, want_initial):
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         dinitial = torch.empty_like(initial) if want_initial else None
         ws, n = _workspace(shape, 1, q.device)
-        _check(_lib.fftconv_linear_attention_backward(ctypes.byref(shape), _p(q), _p(k), _p(v), _p(log_decay),
+        _check(_lib.fftconv_linear_attention_backward(shape, _p(q), _p(k), _p(v), _p(log_decay),
                                                       _p(initial), _p(cu), _p(do), _p(dstate), _p(dq), _p(dk), _p(dv),
                                                       _p(dinitial), _p(ws), n, handle))
     return dq, dk, dv, dinitial
