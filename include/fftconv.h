@@ -382,8 +382,8 @@ FFTCONV_API int fftconv_linear_attention(const fftconv_linear_attention_t* shape
  *     dq_t = a S_t do_t,   dk_t = dS_t v_t,   dv_t = dS_t^T k_t,
  *     dinitial = g dS_0  (dfinal for a sequence without tokens).
  * dq, dk, dv: contiguous, of q's, k's and v's shape; heads that are shared
- * are summed over their group in fp32.  dinitial: fp32 or NULL.  log_decay
- * has no gradient.  Rows of tokens outside every packed sequence are zero.
+ * are summed over their group in fp32.  dinitial: fp32 or NULL, no part of
+ * dfinal.  log_decay has no gradient.  Rows of tokens outside every packed sequence are zero.
  * The result does not depend on the order in which blocks run.
  * Asynchronous on `stream`; allocates nothing. */
 FFTCONV_API int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, const void* q,

@@ -65,20 +65,29 @@ struct Params {
     const int32_t* cu;
     int64_t T;
     int nroles, H, nseq, nper, seg_len, max_seg;   // nper: segments of a sequence (unpacked)
+    int split;                                // segment states and final states come before the outputs
+    int in_place;                             // ... and these take the initial states' place
 };
 
-// Which sequence and which of its tokens segment `sid` stands for.
+// A segment: which sequence, which of its segments and tokens.
 struct Segment {
     int seq, idx, count, n;                   // n: tokens
     int t0, b;                                // first token's coordinates
+    int sid;                                  // place among all segments
 };
 
-// Called by one whole warp.  Sequences without tokens have one empty segment.
-__device__ Segment find_segment(const Params& p, int sid) {
-    Segment s{-1, 0, 0, 0, 0, 0};
+// The segment that the order-th CTA of a head and role takes; called by one
+// whole warp.  Sequences without tokens have one empty segment.  Of packed
+// sequences the segments of over half the length come first: the CTAs run in
+// about this order, and the short ones fill the SMs that are free early
+// (8192 tokens in 9 sequences, 16 heads of 128/128: 112 us in the sequences'
+// order, 102 in this one).
+__device__ Segment find_segment(const Params& p, int order) {
+    Segment s{-1, 0, 0, 0, 0, 0, 0};
     if (!p.cu) {
-        s.seq = sid / p.nper;
-        s.idx = sid - s.seq * p.nper;
+        s.sid = order;
+        s.seq = order / p.nper;
+        s.idx = order - s.seq * p.nper;
         s.count = p.nper;
         s.b = s.seq;
         s.t0 = s.idx * p.seg_len;
@@ -86,33 +95,44 @@ __device__ Segment find_segment(const Params& p, int sid) {
         return s;
     }
     const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int base = 0; base < p.nseq; base += 32) {
-        const int i = base + lane;
-        int start = 0, len = 0, cnt = 0;
-        if (i < p.nseq) {
-            start = min(max(p.cu[i], 0), (int)p.T);
-            len = min(max(p.cu[i + 1], start), (int)p.T) - start;
-            cnt = max(1, (len + p.seg_len - 1) / p.seg_len);
-        }
-        int incl = cnt;
-        for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += v;
-        }
-        const int lo = before + incl - cnt;
-        const unsigned hit = __ballot_sync(0xffffffffu, sid >= lo && sid < lo + cnt);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            s.seq = base + src;
-            s.idx = sid - __shfl_sync(0xffffffffu, lo, src);
+    for (int brief = 0; brief < 2; ++brief) {
+        int before = 0;                                       // all segments of the sequences before
+        for (int base = 0; base < p.nseq; base += 32) {
+            const int i = base + lane;
+            int start = 0, len = 0, cnt = 0, mine = 0;        // mine: those of this length
+            if (i < p.nseq) {
+                start = min(max(p.cu[i], 0), (int)p.T);
+                len = min(max(p.cu[i + 1], start), (int)p.T) - start;
+                cnt = max(1, (len + p.seg_len - 1) / p.seg_len);
+                const int last_brief = len - (cnt - 1) * p.seg_len <= p.seg_len / 2;
+                mine = brief ? last_brief : cnt - last_brief;
+            }
+            const int total = __reduce_add_sync(0xffffffffu, mine);
+            if (order >= total) {
+                order -= total;
+                before += __reduce_add_sync(0xffffffffu, cnt);
+                continue;
+            }
+            int upto = mine, all = cnt;                       // sums over the lanes up to this one
+            for (int d = 1; d < 32; d <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, upto, d), v = __shfl_up_sync(0xffffffffu, all, d);
+                if (lane >= d) {
+                    upto += u;
+                    all += v;
+                }
+            }
+            const int src = __ffs(__ballot_sync(0xffffffffu, order < upto)) - 1;
             s.count = __shfl_sync(0xffffffffu, cnt, src);
+            s.idx = brief ? s.count - 1 : order - __shfl_sync(0xffffffffu, upto - mine, src);
+            const int first = before + __shfl_sync(0xffffffffu, all, src) - s.count;
+            // (offsets that decrease could count more segments than there is room for)
+            if (first + s.count <= p.max_seg) s.seq = base + src;
+            s.sid = first + s.idx;
             len = __shfl_sync(0xffffffffu, len, src);
             s.t0 = __shfl_sync(0xffffffffu, start, src) + s.idx * p.seg_len;
             s.n = min(p.seg_len, len - s.idx * p.seg_len);
             return s;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
     }
     return s;                                 // past the last segment: seq = -1
 }
@@ -370,16 +390,16 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     const int lane = tid & 31;
     const int role_i = blockIdx.x % p.nroles;
     const int h = (blockIdx.x / p.nroles) % p.H;
-    const int sid = blockIdx.x / (p.nroles * p.H);
+    const int order = blockIdx.x / (p.nroles * p.H);
     const Role& r = p.role[role_i];
     const bool rev = r.rev != 0;
 
     // a segment's chunks, and whether it is the first or last in the role's
-    // direction of time; a split sequence's last own state only matters where
-    // it is a result
+    // direction of time; the last one's own state only matters where the final
+    // state is a result
     auto first_of = [&](int idx, int count) { return rev ? idx == count - 1 : idx == 0; };
     auto chunks_of = [&](const Segment& s) {
-        if (s.seq < 0 || (STATE_ONLY && first_of(s.count - 1 - s.idx, s.count) && (s.count == 1 || r.fin == nullptr)))
+        if (s.seq < 0 || (STATE_ONLY && first_of(s.count - 1 - s.idx, s.count) && r.fin == nullptr))
             return 0;
         return (s.n + kChunk - 1) / kChunk;
     };
@@ -395,7 +415,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     };
 
     if (warp == L::LoadWarp) {
-        const Segment s = find_segment(p, sid);
+        const Segment s = find_segment(p, order);
         if (lane == 0) {
             for (int i = 0; i < 4; ++i) {
                 mbar_init(&full[i], 1);
@@ -418,6 +438,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             misc[3] = s.n;
             misc[4] = s.t0;
             misc[5] = s.b;
+            misc[28] = s.sid;
             // the first loads go out while the other warps set up
             const int nch = chunks_of(s);
             for (int c = 0; c < min(nch, L::Stages); ++c) load_chunk(c, nch, s.t0, s.b);
@@ -442,10 +463,11 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, *tmem_sh, 0);
     const int seq = misc[0], idx = misc[1], count = misc[2], n = misc[3], t0 = misc[4], b = misc[5];
+    const int sid = misc[28];
     const bool first = first_of(idx, count);
     const int nch = chunks_of(Segment{seq, idx, count, n, t0, b});
     const bool has_init = !STATE_ONLY && (first ? r.init != nullptr : true);
-    const bool want_fin = STATE_ONLY || (count == 1 && r.fin != nullptr);
+    const bool want_fin = STATE_ONLY || (!p.split && r.fin != nullptr);
 
     auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
         return __all_sync(0xffffffffu, wait_phase(bar, phase & 1, abort_flag));
@@ -844,8 +866,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         // the state in front of the first chunk
         auto initial = [&]() {
             if (second || ch >= r.kd || (first && !r.init)) return;
-            if (!first || r.init_t) {
-                const float* src = (first ? r.init + at_seq : r.seg + at_seg) + ch;
+            // (in place, the final state is already where the initial one was)
+            const bool from_seg = !first || p.in_place;
+            if (from_seg || r.init_t) {
+                const float* src = (from_seg ? r.seg + at_seg : r.init + at_seq) + ch;
 #pragma unroll
                 for (int j = 0; j < kCols; ++j)
                     if (col0 + j < r.vd) state[j] = src[(int64_t)(col0 + j) * r.kd];
@@ -1228,7 +1252,7 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
         for (int i = 0; i < 8; ++i) sid0 += before[i];
         count = cnt(seq, len);
     }
-    if (count < 2 || sid0 + count > p.max_seg) return;
+    if ((count < 2 && !r.fin) || sid0 + count > p.max_seg) return;
     // a tile of 32 x 32: a thread has four rows of a column of the segments'
     // states; where the first and the last state lie the other way, they go
     // through shared memory
@@ -1243,6 +1267,20 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
     const float ld = p.log_decay[h];
     const float whole = decay_power(ld, (float)p.seg_len);
     const float tail = decay_power(ld, (float)(len - (count - 1) * p.seg_len));
+    const int64_t step = (int64_t)p.H * mat / 4;
+    float4* at = reinterpret_cast<float4*>(r.seg + ((int64_t)sid0 * p.H + h) * mat + (int64_t)col * r.kd + row);
+    // the last segment's own state is there where the final state is wanted
+    // (and the segment has tokens)
+    const int have = !r.fin ? count - 1 : len ? count : 0, todo = in ? count : 0;
+    // the loads of four segments go out together, the first ones ahead of the
+    // initial state's: their addresses do not depend on the running state
+    float4 local[4];
+    auto fetch = [&](int s) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (in && s + q < have) local[q] = at[(int64_t)(r.rev ? count - 1 - s - q : s + q) * step];
+    };
+    fetch(0);
     float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r.init && r.init_t) {
         if (in) run = *reinterpret_cast<const float4*>(r.init + at_seq + (int64_t)col * r.kd + row);
@@ -1258,22 +1296,13 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
         run = make_float4(turn[x4][y], turn[x4 + 1][y], turn[x4 + 2][y], turn[x4 + 3][y]);
         __syncthreads();
     }
-    const int64_t step = (int64_t)p.H * mat / 4;
-    float4* at = reinterpret_cast<float4*>(r.seg + ((int64_t)sid0 * p.H + h) * mat + (int64_t)col * r.kd + row);
-    // the last segment's own state is there where the final state is wanted
-    const int have = r.fin ? count : count - 1, todo = in ? count : 0;
-    // the loads of four segments go out together: their addresses do not
-    // depend on the running state
     for (int s = 0; s < todo; s += 4) {
-        float4 local[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            if (s + q < have) local[q] = at[(int64_t)(r.rev ? count - 1 - s - q : s + q) * step];
+        if (s) fetch(s);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (s + q >= count) break;
             const int i = r.rev ? count - 1 - s - q : s + q;
-            at[(int64_t)i * step] = run;
+            if (s + q > 0 || p.in_place) at[(int64_t)i * step] = run;       // (the first one is init)
             if (s + q < have) {
                 const float g = i == count - 1 ? tail : whole;
                 run.x = fmaf(g, run.x, local[q].x);
@@ -1466,9 +1495,11 @@ Split split_of(const fftconv_linear_attention_t& d, int nroles) {
     Split s{up(d.T), 1, seqs, false};
     int64_t len;
     if (d.nseq > 0) {
-        // lengths are known on the device only: half an even share a piece
-        // evens the SMs' work out whatever they are
-        len = up((d.T * d.H * nroles + 2 * sms - 1) / (2 * sms));
+        // lengths are known on the device only.  Pieces a little longer than
+        // an even share leave room for the sequences' short ends beside them
+        // (8192 tokens in 9 sequences, 16 heads of 128/128: half a share 100
+        // us, 3/4 108, one 103, 5/4 93, 3/2 94)
+        len = up((d.T * d.H * nroles * 5 / 4 + sms - 1) / sms);
     } else {
         const int64_t share = (d.B * d.T * d.H * nroles + sms - 1) / sms;
         if (d.T * ((tasks + sms - 1) / sms) <= share + share * 3 / 5 + 4 * kChunk) return s;
@@ -1550,6 +1581,8 @@ void fill(Params& p, const fftconv_linear_attention_t& d, const Split& s, const 
     p.nper = (int)s.nper;
     p.seg_len = (int)s.seg_len;
     p.max_seg = (int)s.max_seg;
+    p.split = s.on;
+    p.in_place = 0;
 }
 
 // The launches of up to three roles, all with key and value dims within
@@ -1570,8 +1603,7 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
                              dim3(256), args, 0, stream);
         if (e != cudaSuccess) return e;
     }
-    // (packed sequences that are not cut take their final state from this launch)
-    return launch_kernel<false>(p, f16, exact && (!s.on || p.cu), kp, vp, ctas, stream);
+    return launch_kernel<false>(p, f16, exact && !s.on, kp, vp, ctas, stream);
 }
 
 cudaError_t copy_states(float* dst, const float* src, int64_t count, cudaStream_t s) {
@@ -1659,6 +1691,7 @@ int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void
     r.init = initial_state;
     r.fin = final_state;
     r.seg = (float*)workspace;
+    p.in_place = sp.on && initial_state && final_state == initial_state;
     cudaError_t e = cudaSuccess;
     if (d.nseq > 0 && d.zero_rest) e = zero_rest(o, d, d.H, d.V, d.o_stride, cu_seqlens, s);
     if (e == cudaSuccess) e = run_roles(p, d, sp, d.K > 64 ? 128 : 64, d.V > 64 ? 128 : 64, s);
@@ -1681,7 +1714,7 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
     if (!log_decay) return fail(FFTCONV_ERR_INVALID_ARG, "log_decay is NULL");
     if (!aligned16(initial_state) || !aligned16(dfinal) || !aligned16(dinitial))
         return fail(FFTCONV_ERR_ALIGNMENT, "states must be 16-byte aligned");
-    if (dinitial != dfinal && overlap(dinitial, states * 4, dfinal, states * 4))
+    if (overlap(dinitial, states * 4, dfinal, states * 4))
         return fail(FFTCONV_ERR_INVALID_ARG, "dinitial overlaps dfinal");
     if (d.T == 0) {
         const cudaError_t e = copy_states(dinitial, dfinal, states, s);
@@ -1706,7 +1739,7 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
         const int64_t nout[4] = {tok * d.Hq * d.K * 2, tok * d.Hk * d.K * 2, tok * d.Hv * d.V * 2, states * 4};
         for (int i = 0; i < 4; ++i) {
             for (int j = 0; j < 6; ++j)
-                if (!(i == 3 && j == 5) && overlap(out[i], nout[i], in[j], nin[j]))
+                if (overlap(out[i], nout[i], in[j], nin[j]))
                     return fail(FFTCONV_ERR_INVALID_ARG, "a gradient overlaps an input");
             for (int j = 0; j < i; ++j)
                 if (overlap(out[i], nout[i], out[j], nout[j]))

@@ -105,6 +105,53 @@ def test_packed_sequences(lens, heads, K, V, dtype):
     check_attention(_run(x, cu), ref, mag, DT[dtype], f"lens={lens[:6]}")
 
 
+@pytest.mark.parametrize("lens,heads,K,V,dtype", [
+    ([40] * 33 + [1700, 0, 900] + [5] * 10 + [641], KV, 128, 128, "bf16"),
+    ([1300, 1, 0, 513, 512, 511, 1024, 256, 257] + [9] * 30, MHA, 64, 128, "f16"),
+    ([700, 2048, 33, 0, 1535], QK, 128, 64, "bf16"),
+])
+def test_packed_sequences_cut_along_time(lens, heads, K, V, dtype):
+    """Long and brief pieces of many sequences, in the order of their lengths."""
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    x = _case(1, cu[-1], heads, K, V, dtype, seed=len(lens), n=len(lens))
+    ref, mag = _both(x, cu)
+    check_attention(_run(x, cu), ref, mag, DT[dtype], f"lens={lens[:6]}")
+
+
+@pytest.mark.parametrize("T,cu", [(300, None), (3000, None), (3000, [0, 700, 700, 2900, 3000])])
+@pytest.mark.parametrize("K,V", [(64, 64), (128, 128)])
+def test_final_states_in_place_of_initial_ones(T, cu, K, V):
+    """The C interface lets final_state be initial_state itself, for sequences
+    in one piece and for those cut along time."""
+    import ctypes
+
+    import long_sequence_fft_b200 as lsf
+    from long_sequence_fft_b200.linear_attention import _Shape
+    n = 1 if cu is None else len(cu) - 1
+    x = _case(1, T, MHA, K, V, "bf16", seed=T, n=n)
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    want, state = lsf.linear_attention(x["q"], x["k"], x["v"], x["log_decay"], initial_state=x["initial"],
+                                       cu_seqlens=cud, return_state=True)
+    o, both = torch.empty_like(want), x["initial"].clone()
+    H = 2
+    rows = lambda d: (T * H * d, H * d, d)                                   # noqa: E731
+    shape = _Shape(1, T, 0 if cu is None else n, H, H, H, H, K, V, lsf.BF16, K ** -0.5, 1, rows(K), rows(K), rows(V),
+                   rows(V))
+    lib = lsf.library()
+    size = lib.fftconv_linear_attention_workspace_bytes(ctypes.byref(shape), 0)
+    assert (size > 0) == (T > 1000)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device="cuda")
+    rc = lib.fftconv_linear_attention(ctypes.byref(shape), x["q"].data_ptr(), x["k"].data_ptr(), x["v"].data_ptr(),
+                                      x["log_decay"].data_ptr(), both.data_ptr(),
+                                      None if cud is None else cud.data_ptr(), o.data_ptr(), both.data_ptr(),
+                                      ws.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    _status_ok()
+    assert torch.equal(o, want) and torch.equal(both, state)
+
+
 def test_rows_outside_packed_sequences():
     """Tokens in front of and behind the packed sequences: unused whatever they
     hold (NaN here, in inputs and gradients), zero in new outputs and

@@ -73,6 +73,21 @@ def test_linear_attention_refusals(shape, args, status):
     assert lib.fftconv_last_error()
 
 
+@pytest.mark.parametrize("args,status", [
+    (dict(dinit=ST), -1),                                    # dk and dv both read dfinal
+    (dict(dinit=ST + 1024), -1), (dict(dinit=WS + 2), -3), (dict(dq=O), -1), (dict(dk=K), -1), (dict(dv=None), -1),
+    (dict(dq=(9 << 36) + 4), -3), (dict(dk=9 << 36), -1), (dict(ws=None), -1),
+])
+def test_linear_attention_backward_refusals(args, status):
+    _, lib = _lib()
+    a = dict(dq=9 << 36, dk=10 << 36, dv=11 << 36, dinit=None, ws=WS)
+    a.update(args)
+    s = _shape(Hk=2)                                          # (shared heads: partial sums need the workspace)
+    rc = lib.fftconv_linear_attention_backward(ctypes.byref(s), Q, K, V, LD, None, None, O, ST, a["dq"], a["dk"],
+                                               a["dv"], a["dinit"], a["ws"], 1 << 40, None)
+    assert rc == status and lib.fftconv_last_error()
+
+
 def test_linear_attention_workspace():
     """None where a call fills the GPU by its sequences and heads; segment
     states where it is cut along time; fp32 partial sums of shared heads."""
