@@ -383,7 +383,8 @@ FFTCONV_API int fftconv_linear_attention(const fftconv_linear_attention_t* shape
  *     dinitial = g dS_0  (dfinal for a sequence without tokens).
  * dq, dk, dv: contiguous, of q's, k's and v's shape; heads that are shared
  * are summed over their group in fp32.  dinitial: fp32 or NULL, no part of
- * dfinal.  log_decay has no gradient.  Rows of tokens outside every packed sequence are zero.
+ * dfinal.  log_decay has no gradient.  Rows of tokens outside every packed
+ * sequence are zero.
  * The result does not depend on the order in which blocks run.
  * Asynchronous on `stream`; allocates nothing. */
 FFTCONV_API int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, const void* q,

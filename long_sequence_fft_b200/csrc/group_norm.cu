@@ -1172,7 +1172,7 @@ int check(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int wdtype, int
     if (affine && wdtype != dtype && wdtype != FFTCONV_F32)
         return fail(FFTCONV_ERR_INVALID_ARG, "weight and bias must have x's type or fp32");
     if (act < FFTCONV_ACT_NONE || act > FFTCONV_ACT_SIGMOID) return fail(FFTCONV_ERR_INVALID_ARG, "unknown activation");
-    if (C >= (int64_t(1) << 24) || (double)N * (double)G >= 2147483647.0 ||
+    if (C > 65535 * kThreads || (double)N * (double)G >= 2147483647.0 ||
         (double)N * (double)most_chunks(N, S ? S : 1, C) + (double)C >= 2147483647.0)
         return fail(FFTCONV_ERR_UNSUPPORTED, "too many channels, samples or groups");
     return FFTCONV_OK;

@@ -116,7 +116,9 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
     weight and bias [C], both or neither, in x's type or fp32.  x and gate may
     be rows of wider tensors (last index contiguous, one row stride).
     activation: "none", "silu" or "sigmoid".  Differentiable in x, gate,
-    weight and bias (not together with `out` or `stream`)."""
+    weight and bias (not together with `out` or `stream`).  When a backward
+    pass is captured into a CUDA graph, let the forward call of the same leaves
+    be captured with it."""
     import torch
     if x.dim() < 2:
         raise ValueError("x must have at least 2 dimensions: sample, ..., channel")

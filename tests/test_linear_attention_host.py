@@ -137,6 +137,13 @@ def test_group_norm_refusals(change, status):
     assert back(dx=Q) == -1 and back(dw=V, db=LD) == -1 and back(dgate=V) == -1 and back(dy=None) == -1
 
 
+@pytest.mark.parametrize("N,C", [(1, 65535 * 256 + 1), (1 << 20, 1 << 12)])
+def test_group_norm_sizes_beyond_a_grid(N, C):
+    _, lib = _lib()
+    rc = lib.fftconv_group_norm(Q, None, None, None, O, None, None, N, 1, C, C, C, 0, 2, 2, 1, 1e-5, WS, 1 << 50, None)
+    assert rc == -2 and lib.fftconv_last_error()
+
+
 def test_python_refuses_cpu_tensors():
     import torch
     import long_sequence_fft_b200 as lsf
