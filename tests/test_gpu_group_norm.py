@@ -87,6 +87,15 @@ def test_forward_and_gradients(shape, G, dtype, gate, act, affine):
     _check(_run(x, G, act), x, G, act, what=f"{shape} G={G} {dtype}")
 
 
+@pytest.mark.parametrize("shape,G", [((5003, 768), 12), ((20011, 96), 4), ((9001, 1024), 2), ((4100, 35), 7)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [False, True])
+def test_more_rows_than_the_gpu_holds(shape, G, dtype, gate):
+    """Blocks that walk down many rows, the last of them beyond the end."""
+    x = _inputs(shape, dtype, seed=shape[0], gate=gate, affine=True)
+    _check(_run(x, G, "silu"), x, G, "silu", what=f"{shape} G={G} {dtype}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_parameters_in_the_tensors_type(dtype):
     x = _inputs((40, 256), dtype, seed=3, gate=True, affine=True, wdtype=dtype)

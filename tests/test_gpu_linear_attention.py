@@ -408,6 +408,51 @@ def test_streams_and_graphs():
     _status_ok()
 
 
+def test_captured_packed_call_with_other_offsets():
+    """The segments are planned on the device: a captured call takes the
+    offsets that it finds when it is replayed, and two graphs run at once."""
+    import long_sequence_fft_b200 as lsf
+    T = 4000
+    x = _case(1, T, KV, 64, 64, "bf16", seed=31, n=4, initial=False)
+    first, other = [0, 100, 3000, 3001, 4000], [0, 1700, 1700, 1764, 3999]
+    graphs = []
+    for _ in range(2):
+        cu = torch.tensor(first, dtype=torch.int32, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            o, s = lsf.linear_attention(x["q"], x["k"], x["v"], x["log_decay"], cu_seqlens=cu, return_state=True)
+        graphs.append((g, cu, o, s))
+    graphs[1][1].copy_(torch.tensor(other, dtype=torch.int32))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graphs[0][0].replay()
+    graphs[1][0].replay()
+    torch.cuda.synchronize()
+    for (_, _, o, s), offsets in zip(graphs, (first, other)):
+        want, state = lsf.linear_attention(x["q"], x["k"], x["v"], x["log_decay"], return_state=True,
+                                           cu_seqlens=torch.tensor(offsets, dtype=torch.int32, device="cuda"))
+        assert torch.equal(o, want) and torch.equal(s, state)
+    _status_ok()
+
+
+def test_more_sequences_than_one_look_of_the_plan():
+    """Over 1024 sequences, some cut, against the same ones one by one."""
+    import long_sequence_fft_b200 as lsf
+    lens = ([3] * 700 + [1500] + [0, 17]) * 2
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    x = _case(1, cu[-1], MHA, 64, 64, "bf16", seed=5, n=len(lens))
+    got = _run(x, cu)
+    ref, mag = _both(x, cu)
+    check_attention(got, ref, mag, torch.bfloat16, "many sequences")
+    o, s = lsf.linear_attention(x["q"], x["k"], x["v"], x["log_decay"], initial_state=x["initial"], return_state=True,
+                                cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    assert torch.equal(o, got["o"]) and torch.equal(s, got["state"])
+
+
 def test_refusals():
     import long_sequence_fft_b200 as lsf
     x = _case(1, 64, MHA, 64, 64, "bf16", seed=1)
