@@ -68,17 +68,19 @@ def _autograd_function():
 
     class GroupNormFunction(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, x, gate, weight, bias, ld, ld_gate, N, S, C, G, act, eps):
+        def forward(ctx, x, gate, weight, bias, args):
+            # (one argument for all that is no tensor: autograd looks at each)
+            ld, ld_gate, N, S, C, G, act, eps = args
             y, stats = _forward(x, ld, gate, ld_gate, weight, bias, N, S, C, G, act, eps, None, True, None)
             ctx.save_for_backward(x, gate, weight, bias, stats)
-            ctx.args = (ld, ld_gate, N, S, C, G, act)
+            ctx.args = args
             return y
 
         @staticmethod
         @torch.autograd.function.once_differentiable
         def backward(ctx, dy):
             x, gate, weight, bias, stats = ctx.saved_tensors
-            ld, ld_gate, N, S, C, G, act = ctx.args
+            ld, ld_gate, N, S, C, G, act, _ = ctx.args
             need = ctx.needs_input_grad
             ld_dy = _ld(dy, C)
             if ld_dy is None:
@@ -99,8 +101,9 @@ def _autograd_function():
                     _p(x), _p(gate), _p(weight), _p(bias), _p(dy), mean, mean + 4 * N * G, _p(dx), _p(dgate), dw,
                     None if dw is None else dw + 4 * C, N, S, C, G, ld, ld_gate, ld_dy, code,
                     code if weight is None else _code(weight.dtype), act, _p(ws), n, handle))
-            return (dx if need[0] else None, dgate if need[1] else None, sums[0].to(weight.dtype) if need[2] else None,
-                    sums[1].to(bias.dtype) if need[3] else None) + (None,) * 8
+            dweight, dbias = (None, None) if sums is None else sums.to(weight.dtype).unbind(0)
+            return (dx if need[0] else None, dgate if need[1] else None, dweight if need[2] else None,
+                    dbias if need[3] else None, None)
 
     _AUTOGRAD_FN = GroupNormFunction
     return _AUTOGRAD_FN
@@ -160,5 +163,5 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
     if grad:
         if out is not None or stream is not None:
             raise NotImplementedError("group_norm: no gradients with out= or stream=")
-        return _autograd_function().apply(x, gate, weight, bias, ld, ld_gate, N, S, C, G, act, float(eps))
+        return _autograd_function().apply(x, gate, weight, bias, (ld, ld_gate, N, S, C, G, act, float(eps)))
     return _forward(x, ld, gate, ld_gate, weight, bias, N, S, C, G, act, float(eps), out, False, stream)[0]
