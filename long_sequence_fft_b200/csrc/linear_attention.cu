@@ -385,7 +385,7 @@ struct Layout {
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // abort (word 6), TMEM base (7), scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int Bars = 27 + (F16 ? 4 : 0);
+    static constexpr int Bars = 28 + (F16 ? 4 : 0);
     static constexpr int OffMax = OffBar + (Bars + 1) / 2 * 16;   // (fp16) channel maxima [2][state warps][32]
     static constexpr int Bytes = OffMax + (F16 ? 2 * kStateWarps * 32 * 2 : 0);
     // TMEM columns
@@ -436,14 +436,17 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     uint64_t* o_free = bars + 16;                             // [Groups] output read
     uint64_t* bar_st = bars + 18;                             // the chunk's own state
     uint64_t* bar_kt = bars + 19;                             // its first parts (Late only)
-    uint64_t* kt_ready = bars + 20;
     uint64_t* late_ready = bars + 21;
     uint64_t* carry_ready = bars + 22;
     uint64_t* z_ready = bars + 23;                            // rows behind a packed sequence zeroed
     uint64_t* wgb_bar = bars + 24;
     uint64_t* c_free = bars + 25;                             // the chunk's own state read
     uint64_t* bar_fin = bars + 26;                            // all MMA warps
-    uint64_t* pair_bar = bars + 27;                           // [4] (fp16) the two state warps of the same channels
+    // keys weighed, a barrier for each of their buffers: with two of them the
+    // state warps may be done with chunk c + 1 before the MMA warp has seen
+    // chunk c, and two phases of one barrier look like none
+    auto kt_ready = [&](int c) { return c % L::KtBufs ? bars + 27 : bars + 20; };
+    uint64_t* pair_bar = bars + 28;                           // [4] (fp16) the two state warps of the same channels
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -489,6 +492,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             mbar_init(bar_kt, 1);
             for (int i = 20; i < 26; ++i) mbar_init(bars + i, L::Live);
             mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
+            mbar_init(bars + 27, L::Live);
             if constexpr (F16)
                 for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
             *abort_flag = 0;
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             const int ks = (chunk_n(c) + 15) / 16;
             const uint64_t d_z = make_desc(sb + st * L::StageBytes + L::OffZ, 16384, 1024, 2);
             const uint32_t t_kt = tbase + L::Kt + c % L::KtBufs * L::KtCols;
-            ok = wait(kt_ready, c);
+            ok = wait(kt_ready(c), c / L::KtBufs);
             if (!ok) break;
             if (c + 1 < nch || want_fin) {
                 if (kAhead && c > 0) ok = wait(c_free, c - 1);
@@ -1202,7 +1206,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             }
             tc_wait_st();
             tc_fence_before();
-            arrive(kt_ready);
+            arrive(kt_ready(c));
             if constexpr (L::Late) {
                 if (more) {
                     if (!wait(bar_kt, c)) return false;

@@ -105,6 +105,35 @@ def test_packed_sequences(lens, heads, K, V, dtype):
     check_attention(_run(x, cu), ref, mag, DT[dtype], f"lens={lens[:6]}")
 
 
+@pytest.mark.parametrize("heads", [(5, 5, 5, 5), (6, 2, 2, 6)])
+@pytest.mark.parametrize("K,V", [(128, 64), (64, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_mixed_widths_that_fill_the_gpu(heads, K, V, dtype):
+    """More sequences and heads than SMs: the three gradients come from two
+    launches of different widths."""
+    x = _case(10, 600, heads, K, V, dtype, seed=K + heads[1])
+    ref, mag = _both(x)
+    check_attention(_run(x), ref, mag, DT[dtype], f"K={K} V={V}")
+
+
+@pytest.mark.parametrize("K,V", [(128, 64), (64, 128), (64, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_many_repeats_wait_for_nothing(K, V, dtype):
+    """Long walks on every SM, many times over: no bounded wait may give up, and
+    the results stay the same."""
+    import long_sequence_fft_b200 as lsf
+    x = _case(8, 2048, (12, 12, 12, 12), K, V, dtype, seed=1, initial=False)
+    leaves = [x[n].requires_grad_() for n in "qkv"]
+    want = None
+    for _ in range(25):
+        o = lsf.linear_attention(*leaves, x["log_decay"])
+        got = [o.detach(), *torch.autograd.grad(o, leaves, x["do"])]
+        if want is None:
+            want = got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    _status_ok()
+
+
 @pytest.mark.parametrize("lens,heads,K,V,dtype", [
     ([40] * 33 + [1700, 0, 900] + [5] * 10 + [641], KV, 128, 128, "bf16"),
     ([1300, 1, 0, 513, 512, 511, 1024, 256, 257] + [9] * 30, MHA, 64, 128, "f16"),
