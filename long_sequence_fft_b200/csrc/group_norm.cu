@@ -997,7 +997,8 @@ int sample_threads(int64_t S, int64_t C, int V) {
     return (int)((width * rows + 31) / 32 * 32);
 }
 // Samples are cut so that all blocks are resident at once where there are few
-// samples (768 threads an SM), but no finer than 16384 values.
+// samples (768 threads an SM; twice as many chunks: 35 us instead of 30 for the
+// statistics of 16 x 4095 x 760 fp16), but no finer than 16384 values.
 int64_t chunks_of(int64_t N, int64_t S, int64_t C, int V) {
     const int64_t cols = (C / V + kThreads - 1) / kThreads > 0 ? (C / V + kThreads - 1) / kThreads : 1;
     int64_t want = 148 * (768 / sample_threads(S, C, V)) / ((N > 0 ? N : 1) * cols);

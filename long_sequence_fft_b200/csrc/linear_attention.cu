@@ -1532,7 +1532,10 @@ struct Split {
 // A sequence is one CTA's serial walk, so few sequences x heads leave SMs
 // idle; cutting along time costs a second pass over keys and values (the
 // segments' own states) and the states' round trip.  It pays where one walk
-// takes over 1.6 times what an even share of all tokens would.
+// takes over 1.6 times what an even share of all tokens would (bf16, forward:
+// at 1.54 times, 16 x 4096 tokens, 12 heads of 64/64, 117 us and 142 cut; 12 x
+// 4096, 8 heads of 128/128, 118 and 157; at 2.05 times, 8 x 4096, 9 heads of
+// 128/128, 115 and 99 cut; 64/64 61 and 60).
 Split split_of(const fftconv_linear_attention_t& d, int nroles) {
     const int64_t sms = sm_count(), seqs = d.nseq > 0 ? d.nseq : d.B;
     const int64_t tasks = seqs * d.H * nroles;
@@ -1877,9 +1880,13 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
     if (e == cudaSuccess) e = plan(p, d, sp, table, s);
     if (e == cudaSuccess) {
         const int kp = d.K > 64 ? 128 : 64, vp = d.V > 64 ? 128 : 64;
-        if (kp == vp || sp.max_seg * d.H * 3 <= sm_count()) {
-            // (mixed widths that leave SMs idle: one launch at the larger one
-            // instead of two in a row)
+        // Mixed widths: one launch at the larger one where that saves enough
+        // waves of CTAs over two in a row, whose waves are a sixth shorter
+        // (2048 tokens, heads of 128/64, bf16, one launch and two: 48
+        // sequences x heads 91 and 104 us, 72 119 and 109, 96 130 and 162)
+        const int64_t sms = sm_count(), n = sp.max_seg * d.H;
+        auto waves = [&](int64_t ctas) { return (ctas + sms - 1) / sms; };
+        if (kp == vp || waves(3 * n) * 6 <= (waves(2 * n) + waves(n)) * 5) {
             const int w = kp > vp ? kp : vp;
             e = run_roles(p, d, sp, w, w, s);
         } else {
