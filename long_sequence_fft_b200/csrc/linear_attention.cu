@@ -25,7 +25,8 @@
 // is lost is the second reading of keys and values where few heads make a cut
 // along time necessary, and the last wave (B200, 16 x 4096 tokens, 12 heads of
 // 64/64, forward and backward: 330 us, of 172 for the bytes; 65536 tokens, 16
-// heads of 128/128: 315 us, of 167).  The chunk's length is the MMA's 128 rows:
+// heads of 128/128: 320 us, of 167; both at 1965 MHz, and a fifth more once
+// seconds of it meet the power limit at 1490).  The chunk's length is the MMA's 128 rows:
 // P costs 128 (K + V) multiplications a token, the carried state 2 K V.
 // Why the products are cut between warps, how the output leaves, and the
 // asynchronous first loads were each found by what the SM spent its time on:
