@@ -84,8 +84,10 @@ def _autograd_function():
             need = ctx.needs_input_grad
             ld_dy = _ld(dy, C)
             if ld_dy is None:
-                # a gradient comes in whatever layout autograd has
-                dy, ld_dy = dy.contiguous(), C
+                # a gradient comes in whatever layout, and at whatever address,
+                # autograd has (a copy: contiguous() would return a contiguous
+                # one that is not aligned as it is)
+                dy, ld_dy = dy.clone(memory_format=torch.contiguous_format), C
             device = x.device
             with _on(device, None) as handle:
                 dx = torch.empty(x.shape, dtype=x.dtype, device=device)

@@ -191,12 +191,13 @@ def _autograd_function():
                 return (None,) * 8
             if do is None:
                 do = torch.zeros(q.shape[:2] + (log_decay.shape[0], v.shape[3]), dtype=q.dtype, device=q.device)
-            # a gradient comes in whatever layout autograd has (an expanded
-            # scalar, a transposed view)
+            # a gradient comes in whatever layout autograd has: an expanded
+            # scalar, a transposed view, a piece of a concatenation's gradient
+            # at any address (a copy, then: contiguous() would return it as it is)
             if not _usable(do):
-                do = do.contiguous()
-            if dstate is not None:
-                dstate = dstate.contiguous()
+                do = do.clone(memory_format=torch.contiguous_format)
+            if dstate is not None and not (dstate.is_contiguous() and dstate.data_ptr() % 16 == 0):
+                dstate = dstate.clone(memory_format=torch.contiguous_format)
             need = ctx.needs_input_grad
             dq, dk, dv, dinitial = _backward(q, k, v, log_decay, initial, cu, ctx.scale, do, dstate,
                                              initial is not None and need[3])

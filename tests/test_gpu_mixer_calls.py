@@ -1,0 +1,65 @@
+"""GPU tests of how torch calls linear attention and group norm: gradients as
+autograd hands them out, tensors that are saved and written, derivatives that
+the operators do not have."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(seed, *shape):
+    return torch.randn(shape, generator=_gen(seed), device="cuda")
+
+
+def _behind(t, n):
+    """t flattened behind n other values: the gradient of t is a contiguous
+    piece of the whole's gradient, n elements from its start."""
+    return torch.cat([t.new_zeros(n), t.flatten()])
+
+
+@pytest.mark.parametrize("shape,G,dtype", [((3, 35), 7, "float32"), ((5, 64), 4, "bfloat16"),
+                                           ((2, 30, 48), 4, "float16"), ((40, 256), 2, "float32")])
+@pytest.mark.parametrize("n", [1, 3])
+def test_norm_gradient_at_any_address(shape, G, dtype, n):
+    import long_sequence_fft_b200 as lsf
+    dt = getattr(torch, dtype)
+    C = shape[-1]
+    leaves = [_randn(1, *shape).to(dt), (1 + 0.1 * _randn(2, C)).to(dt), _randn(3, C).to(dt), _randn(4, *shape).to(dt)]
+    leaves = [t.requires_grad_() for t in leaves]
+
+    def call():
+        return lsf.group_norm(leaves[0], G, leaves[1], leaves[2], gate=leaves[3], activation="silu")
+
+    dy = _randn(5, *shape).to(dt)
+    want = torch.autograd.grad(call(), leaves, dy)
+    got = torch.autograd.grad(_behind(call(), n), leaves, _behind(dy, n))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cu", [None, [0, 50, 50, 130]])
+@pytest.mark.parametrize("n", [1, 3])
+def test_attention_gradients_at_any_address(cu, n):
+    """Of the outputs, of the final states, and of both."""
+    import long_sequence_fft_b200 as lsf
+    B, T, H, K, V = (1 if cu else 2), 130, 2, 64, 40
+    seqs = len(cu) - 1 if cu else B
+    leaves = [_randn(1, B, T, H, K).bfloat16(), _randn(2, B, T, H, K).bfloat16(), _randn(3, B, T, H, V).bfloat16(),
+              _randn(4, seqs, H, K, V)]
+    leaves = [t.requires_grad_() for t in leaves]
+    ld = torch.tensor([-0.3, -0.01], device="cuda")
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def call():
+        return lsf.linear_attention(*leaves[:3], ld, initial_state=leaves[3], cu_seqlens=cud, return_state=True)
+
+    do, ds = _randn(5, B, T, H, V).bfloat16(), _randn(6, seqs, H, K, V)
+    want = torch.autograd.grad(call(), leaves, (do, ds))
+    o, s = call()
+    got = torch.autograd.grad((_behind(o, n), _behind(s, n)), leaves, (_behind(do, n), _behind(ds, n)))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
