@@ -7,7 +7,7 @@ from __future__ import annotations
 
 from . import BF16, F16, F32, _check, _lib
 from . import _ptr as _p
-from .linear_attention import _on
+from .linear_attention import _on, _written
 
 ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
 _CODES = None
@@ -54,6 +54,8 @@ def _forward(x, ld, gate, ld_gate, weight, bias, N, S, C, G, act, eps, out, keep
         _check(_lib.fftconv_group_norm(_p(x), _p(gate), _p(weight), _p(bias), _p(y), mean,
                                        mean + 4 * N * G if keep else None, N, S, C, G, ld, ld_gate, code,
                                        code if weight is None else _code(weight.dtype), act, eps, _p(ws), n, handle))
+    if out is not None:
+        _written(out)
     return y, stats
 
 

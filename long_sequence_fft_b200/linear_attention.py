@@ -77,6 +77,14 @@ class _On:
 _on = _On
 
 
+def _written(*tensors):
+    """Mark the caller's tensors (None: new ones) as written in place, which a
+    launch through their addresses does not: a backward pass that saved one of
+    them then raises, as for torch's own in-place operations."""
+    import torch
+    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+
+
 def _need(t, name, dtype, shape, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -130,6 +138,7 @@ def _forward(q, k, v, log_decay, initial, cu, scale, want_state, out, stream):
     B, T = q.shape[:2]
     H, K, V = log_decay.shape[0], q.shape[3], v.shape[3]
     nseq = 0 if cu is None else cu.shape[0] - 1
+    given = out
     with _on(q.device, stream) as handle:
         zero_rest = out is None
         if out is None:
@@ -141,6 +150,8 @@ def _forward(q, k, v, log_decay, initial, cu, scale, want_state, out, stream):
         ws, n = _workspace(shape, 0, q.device)
         _check(_lib.fftconv_linear_attention(shape, _p(q), _p(k), _p(v), _p(log_decay), _p(initial),
                                              _p(cu), _p(out), _p(state), _p(ws), n, handle))
+    if given is not None:
+        _written(given)
     return out, state
 
 
@@ -297,6 +308,7 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or state.requires_grad):
         raise NotImplementedError("linear_attention_step has no gradients: use linear_attention, or torch.no_grad()")
     scale = K ** -0.5 if scale is None else float(scale)
+    given = out
     with _on(device, stream) as handle:
         if out is None:
             out = torch.empty((B, H, V), dtype=q.dtype, device=device)
@@ -306,6 +318,7 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
             _p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(slots), _p(out), B, pool, H, Hq, k.shape[1],
             v.shape[1], K, V, code, scale, _Pair(*q.stride()[:2]), _Pair(*k.stride()[:2]), _Pair(*v.stride()[:2]),
             handle))
+    _written(state, given)
     return out
 
 

@@ -63,3 +63,60 @@ def test_attention_gradients_at_any_address(cu, n):
     got = torch.autograd.grad((_behind(o, n), _behind(s, n)), leaves, (_behind(do, n), _behind(ds, n)))
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_backward_through_an_overwritten_tensor_raises():
+    """What a call writes in place counts as written: a backward pass that
+    saved it must not go on with other values."""
+    import long_sequence_fft_b200 as lsf
+    q, k, v = (_randn(i, 1, 20, 2, 64).bfloat16() for i in range(3))
+    ld = torch.tensor([-0.3, -0.01], device="cuda")
+    step = (q[:, 0], k[:, 0], v[:, 0], ld)
+    state = _randn(5, 1, 2, 64, 64)
+
+    def saved_by_attention():
+        return lsf.linear_attention(q.clone().requires_grad_(), k, v, ld, initial_state=state)
+
+    o = saved_by_attention()
+    o.sum().backward()                                       # (nothing written in between)
+    o = saved_by_attention()
+    before = state._version
+    lsf.linear_attention_step(*step, state)
+    assert state._version > before
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        o.sum().backward()
+    # a pool, through a view of it
+    pool = _randn(6, 3, 2, 64, 64)
+    o = lsf.linear_attention(q.clone().requires_grad_(), k, v, ld, initial_state=pool[1:2])
+    lsf.linear_attention_step(*step, pool, slots=torch.tensor([1], dtype=torch.int32, device="cuda"))
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        o.sum().backward()
+
+    # out= of each operator, saved by a product
+    w = torch.ones((), device="cuda", dtype=torch.bfloat16, requires_grad=True)
+    x = _randn(7, 20, 128).bfloat16()
+    for out, call in ((torch.zeros((1, 20, 2, 64), device="cuda", dtype=torch.bfloat16),
+                       lambda out: lsf.linear_attention(q, k, v, ld, out=out)),
+                      (torch.zeros((1, 2, 64), device="cuda", dtype=torch.bfloat16),
+                       lambda out: lsf.linear_attention_step(*step, state, out=out)),
+                      (torch.zeros((20, 128), device="cuda", dtype=torch.bfloat16),
+                       lambda out: lsf.group_norm(x, 4, out=out))):
+        y = out * w
+        assert call(out) is out
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            y.sum().backward()
+
+
+def test_inference_mode():
+    """Tensors without a version, and ordinary ones written in inference mode."""
+    import long_sequence_fft_b200 as lsf
+    ordinary = torch.zeros((1, 2, 64, 64), device="cuda")
+    with torch.inference_mode():
+        q, k, v = (_randn(i, 1, 20, 2, 64).bfloat16() for i in range(3))
+        ld = torch.tensor([-0.3, -0.01], device="cuda")
+        o, state = lsf.linear_attention(q, k, v, ld, return_state=True, out=torch.empty_like(q))
+        for s in (state, ordinary):
+            o = lsf.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], ld, s, out=torch.empty_like(q[:, 0]))
+        x = o.view(1, 128)
+        y = lsf.group_norm(x, 2, out=torch.empty_like(x))
+    assert torch.isfinite(y).all() and ordinary.any()
