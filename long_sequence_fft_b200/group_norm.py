@@ -7,7 +7,7 @@ from __future__ import annotations
 
 from . import BF16, F16, F32, _check, _lib
 from . import _ptr as _p
-from .linear_attention import _on, _written
+from .linear_attention import _no_tangents, _on, _written
 
 ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
 _CODES = None
@@ -123,7 +123,8 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
     weight and bias [C], both or neither, in x's type or fp32.  x and gate may
     be rows of wider tensors (last index contiguous, one row stride).
     activation: "none", "silu" or "sigmoid".  Differentiable in x, gate,
-    weight and bias (not together with `out` or `stream`).  When a backward
+    weight and bias (not in forward mode, and not together with `out` or
+    `stream`).  When a backward
     pass is captured into a CUDA graph, let the forward call of the same leaves
     be captured with it."""
     import torch
@@ -161,6 +162,7 @@ def group_norm(x, groups, weight=None, bias=None, *, gate=None, activation="none
     if ld is None or ld_gate is None:
         raise ValueError(f"{'x' if ld is None else 'gate'} must be rows of contiguous channels, one stride apart, "
                          "16-byte aligned")
+    _no_tangents(x, gate, weight, bias)
     grad = torch.is_grad_enabled() and (
         x.requires_grad or (gate is not None and gate.requires_grad) or
         (weight is not None and (weight.requires_grad or bias.requires_grad)))

@@ -85,6 +85,16 @@ def _written(*tensors):
     torch.autograd.graph.increment_version([t for t in tensors if t is not None])
 
 
+def _no_tangents(*tensors):
+    """Refuse dual tensors: they do not require a gradient, so a call would
+    return a result without a tangent, which stands for a derivative of zero."""
+    from torch.autograd import forward_ad
+    if forward_ad._current_level >= 0:                        # (inside a dual_level)
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("linear attention and group norm have no forward-mode derivatives")
+
+
 def _need(t, name, dtype, shape, device):
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
@@ -234,8 +244,8 @@ def linear_attention(q, k, v, log_decay, *, scale=None, initial_state=None, cu_s
 
     Returns o [B, T, H, V], or (o, state) with return_state: state is what
     linear_attention_step and a later call's initial_state take.
-    Differentiable in q, k, v and initial_state (not in log_decay, and not
-    together with `out` or `stream`).  When a backward pass is captured into a
+    Differentiable in q, k, v and initial_state (not in log_decay, not in
+    forward mode, and not together with `out` or `stream`).  When a backward pass is captured into a
     CUDA graph, let the forward call of the same leaves be captured with it."""
     import torch
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
@@ -260,6 +270,7 @@ def linear_attention(q, k, v, log_decay, *, scale=None, initial_state=None, cu_s
         _need_contiguous(cu_seqlens, "cu_seqlens", torch.int32, (n + 1,), device)
     if initial_state is not None:
         _need_contiguous(initial_state, "initial_state", torch.float32, (n, H, K, V), device)
+    _no_tangents(q, k, v, log_decay, initial_state)
     scale = K ** -0.5 if scale is None else float(scale)
     grad = torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or
                                         (initial_state is not None and initial_state.requires_grad))
@@ -307,6 +318,7 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
         _need_contiguous(slots, "slots", torch.int32, (B,), device)
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or state.requires_grad):
         raise NotImplementedError("linear_attention_step has no gradients: use linear_attention, or torch.no_grad()")
+    _no_tangents(q, k, v, log_decay, state)
     scale = K ** -0.5 if scale is None else float(scale)
     given = out
     with _on(device, stream) as handle:

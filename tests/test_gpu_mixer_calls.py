@@ -120,3 +120,34 @@ def test_inference_mode():
         x = o.view(1, 128)
         y = lsf.group_norm(x, 2, out=torch.empty_like(x))
     assert torch.isfinite(y).all() and ordinary.any()
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A dual tensor in any place raises, with and without reverse mode; inside
+    a level, tensors without tangents are computed as ever."""
+    from torch.autograd import forward_ad
+
+    import long_sequence_fft_b200 as lsf
+    q, k, v = (_randn(i, 1, 20, 2, 64).bfloat16() for i in range(3))
+    ld, s = torch.tensor([-0.3, -0.01], device="cuda"), _randn(4, 1, 2, 64, 64)
+    x, gate, w, b = _randn(5, 6, 64), _randn(6, 6, 64), _randn(7, 64), _randn(8, 64)
+    calls = [
+        (lambda q, k, v, ld, s: lsf.linear_attention(q, k, v, ld, initial_state=s), [q, k, v, ld, s]),
+        (lambda q, k, v, ld, s: lsf.linear_attention_step(q, k, v, ld, s), [q[:, 0], k[:, 0], v[:, 0], ld, s.clone()]),
+        (lambda x, gate, w, b: lsf.group_norm(x, 4, w, b, gate=gate), [x, gate, w, b]),
+    ]
+    for call, args in calls:
+        want = call(*[a.clone() for a in args])
+        with forward_ad.dual_level():
+            assert torch.equal(call(*[a.clone() for a in args]), want)
+            for i, a in enumerate(args):
+                dual = list(args)
+                dual[i] = forward_ad.make_dual(a, torch.ones_like(a))
+                with pytest.raises(NotImplementedError):
+                    call(*dual)
+                with torch.no_grad(), pytest.raises(NotImplementedError):
+                    call(*dual)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(x.clone().requires_grad_(), torch.ones_like(x))
+        with pytest.raises(NotImplementedError):
+            lsf.group_norm(dual, 4)
