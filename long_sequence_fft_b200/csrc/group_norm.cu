@@ -1144,8 +1144,19 @@ int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
 
 int vec_of(int dtype) { return dtype == FFTCONV_F32 ? 4 : 8; }
 
-// Sized for either vector width (which depends on strides): the token form's
-// partial sums are at most kTokenBlocks x kThreads rows, and kThreads more than x has.
+// Rows of partial sums that the token form's backward pass writes with vectors
+// of V elements (0: not the token form): those of its row blocks' sub-warps.
+int64_t token_parts(int64_t N, int64_t S, int64_t C, int64_t G, int V) {
+    const int64_t D = C / G;
+    int lanes = 0, per = 0;
+    if (S != 1 || D % V) return 0;
+    token_shape(D / V, V, lanes, per);
+    if (lanes == 0) return 0;
+    const TokenGrid t = token_grid(N, G, lanes, rows_at_once(per, true));
+    return (int64_t)t.gx * t.rsubs;
+}
+
+// Sized for any vector width (which depends on strides, and on the type).
 size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool bwd) {
     if (N == 0 || S == 0 || C == 0) return 0;
     const bool token = S == 1 && C / G <= 256;                // whatever the width
@@ -1155,12 +1166,10 @@ size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool bwd) {
         // parts of the statistics, and mean and rstd when the caller keeps none
         return (size_t)(pad256(N * G * chunks * ((C + kThreads - 1) / kThreads) * 16) + 2 * pad256(N * G * 4));
     }
-    int64_t parts = 0;
-    if (!token) parts = N * chunks;
-    if (S == 1) {
-        // (row blocks x row sub-warps, the last of them beyond the rows)
-        const int64_t most = N + kThreads < kTokenBlocks * kThreads ? N + kThreads : kTokenBlocks * kThreads;
-        if (most > parts) parts = most;
+    int64_t parts = token ? 0 : N * chunks;
+    for (int V : {1, 4, 8}) {
+        const int64_t rows = token_parts(N, S, C, G, V);
+        if (rows > parts) parts = rows;
     }
     return (size_t)(pad256(parts * 2 * C * 4) + (token ? 0 : pad256(N * G * 8)));
 }
