@@ -75,7 +75,7 @@ struct Role {
     int64_t out_b, out_t, out_h;
     const float* init;                        // [seq][H][kd][vd], or null: zeros
     float* fin;                               // carry behind the last token, or null
-    float* seg;                               // segment states [segment][H][vd][kd]: a lane's row, so that loads coalesce
+    float* seg;                               // states of cut sequences' segments [sid][H][vd][kd]: a lane's row, so that loads coalesce
 };
 
 struct Params {
@@ -84,24 +84,25 @@ struct Params {
     const float* log_decay;
     const int32_t* cu;
     int64_t T;
-    int nroles, H, nseq, nper, seg_len, max_seg;   // nper: segments of a sequence (unpacked)
+    int nroles, H, nseq, nper, seg_len, max_seg, max_cut, max_seqs;   // nper: segments of a sequence (unpacked)
     int in_place;                             // the final states take the initial states' place
     int4* table;                              // packed and cut: la_plan's segments, two words each
-    int2* seqs;                               // ... and each sequence's first segment and their number
+    int4* cuts;                               // ... those of sequences in two or more
+    int4* seqs;                               // ... and these sequences: which, its first segment's sid, their number
 };
 
 // A segment: which sequence, which of its segments and tokens.
 struct Segment {
     int seq, idx, count, n;                   // n: tokens
     int t0, b;                                // first token's coordinates
-    int sid;                                  // place among all segments
+    int sid;                                  // place among the segments of cut sequences
 };
 
 // The segment that the order-th CTA of a head and role takes (seq = -1: none).
 // Sequences without tokens have one empty segment.
-__device__ Segment find_segment(const Params& p, int order) {
-    if (p.table) {
-        const int4 u = p.table[2 * (int64_t)order], v = p.table[2 * (int64_t)order + 1];
+__device__ Segment find_segment(const Params& p, const int4* table, int order) {
+    if (table) {
+        const int4 u = table[2 * (int64_t)order], v = table[2 * (int64_t)order + 1];
         return Segment{u.x, u.y, u.z, u.w, v.x, 0, v.y};
     }
     Segment s{order, 0, 1, (int)p.T, 0, 0, order};
@@ -118,38 +119,48 @@ __device__ Segment find_segment(const Params& p, int order) {
     return s;
 }
 
-// sums of a and b over the threads before this one, and over the block
+// sums of each of x over the threads before this one, and over the block
+constexpr int kSums = 4;
 struct Sums {
-    int64_t a, b;
+    int64_t v[kSums];
 };
-__device__ Sums sums_before(Sums x, Sums& all) {
+__device__ Sums sums_before(const Sums& x, Sums& all) {
     __shared__ Sums warps[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Sums in = x;
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t a = __shfl_up_sync(0xffffffffu, in.a, d), b = __shfl_up_sync(0xffffffffu, in.b, d);
-        if (lane >= d) {
-            in.a += a;
-            in.b += b;
-        }
-    }
-    Sums r{in.a - x.a, in.b - x.b};
-    const int n = (int)blockDim.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = (int)blockDim.x >> 5;
+    Sums in = x, r;
     if (n == 1) {
-        all = Sums{__shfl_sync(0xffffffffu, in.a, 31), __shfl_sync(0xffffffffu, in.b, 31)};
+        // (32 sequences of at most 2^22 segments: 32 bits)
+#pragma unroll
+        for (int i = 0; i < kSums; ++i) {
+            int sum = (int)x.v[i];
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += y;
+            }
+            r.v[i] = sum - x.v[i];
+            all.v[i] = __shfl_sync(0xffffffffu, sum, 31);
+        }
         return r;
+    }
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, in.v[i], d);
+            if (lane >= d) in.v[i] += y;
+        }
+        r.v[i] = in.v[i] - x.v[i];
     }
     __syncthreads();                                          // (the last call's sums have been read)
     if (lane == 31) warps[warp] = in;
     __syncthreads();
-    all = Sums{0, 0};
-    for (int w = 0; w < n; ++w) {
-        if (w == warp) {
-            r.a += all.a;
-            r.b += all.b;
+#pragma unroll
+    for (int i = 0; i < kSums; ++i) {
+        int64_t sum = 0;
+        for (int w = 0; w < n; ++w) {
+            if (w == warp) r.v[i] += sum;
+            sum += warps[w].v[i];
         }
-        all.a += warps[w].a;
-        all.b += warps[w].b;
+        all.v[i] = sum;
     }
     return r;
 }
@@ -159,42 +170,71 @@ __device__ Sums sums_before(Sums x, Sums& all) {
 // fill the SMs that are free early (8192 tokens in 9 sequences, 16 heads of
 // 128/128: 112 us in the sequences' order, 102 in this one).  One block looks
 // at all offsets, once: with each CTA looking for its own segment, 2048
-// sequences of 64 tokens and 16 heads took 10.8 ms instead of 1.4.  (Sums in 64
-// bits, and bounds: offsets that decrease can count more segments than there
-// is room for.)
+// sequences of 64 tokens and 16 heads took 10.8 ms instead of 1.4.
+// Only segments of sequences in two or more have states in the workspace, and
+// a launch that sums them: a second list, in the same order, of at most
+// 2 T / seg_len of them however many sequences there are; and the sequences
+// themselves, whose order does not matter.  (Sums in 64 bits, and bounds:
+// offsets that decrease can count more segments than there is room for.)
 __global__ void __launch_bounds__(1024) la_plan(const __grid_constant__ Params p) {
-    auto look = [&](int i, int& start, int& len, int& cnt) {  // segments over half the length
-        start = len = cnt = 0;
-        if (i >= p.nseq) return 0;
-        start = min(max(p.cu[i], 0), (int)p.T);
-        len = min(max(p.cu[i + 1], start), (int)p.T) - start;
-        cnt = max(1, (len + p.seg_len - 1) / p.seg_len);
-        return cnt - (len - (cnt - 1) * p.seg_len <= p.seg_len / 2);
+    struct Look {
+        int start, len, cnt;
+        Sums n;                                               // segments over half the length, all; both of cut sequences
     };
-    int start, len, cnt;
-    Sums mine{0, 0}, all, before{0, 0};                       // long ones, all
-    for (int i = threadIdx.x; i < p.nseq; i += blockDim.x) {
-        mine.a += look(i, start, len, cnt);
-        mine.b += cnt;
-    }
-    sums_before(mine, all);
-    const Sums total = all;
-    for (int base = 0; base < p.nseq; base += blockDim.x) {
-        const int i = base + (int)threadIdx.x, longs = look(i, start, len, cnt);
-        const Sums at = sums_before(Sums{longs, cnt}, all);
-        const int64_t first = before.b + at.b, first_long = before.a + at.a;
-        const bool fits = first + cnt <= p.max_seg;
-        if (i < p.nseq) p.seqs[i] = make_int2((int)first, fits ? cnt : 0);
-        for (int j = 0; j < cnt; ++j) {
-            const int64_t order = j < longs ? first_long + j : total.a + first - first_long;
-            if (order >= p.max_seg) break;
-            p.table[2 * order] = make_int4(fits ? i : -1, j, cnt, min(p.seg_len, len - j * p.seg_len));
-            p.table[2 * order + 1] = make_int4(start + j * p.seg_len, (int)first + j, 0, 0);
+    auto look = [&](int i) {
+        Look s{0, 0, 0, {{0, 0, 0, 0}}};
+        if (i >= p.nseq) return s;
+        s.start = min(max(p.cu[i], 0), (int)p.T);
+        s.len = min(max(p.cu[i + 1], s.start), (int)p.T) - s.start;
+        s.cnt = max(1, (s.len + p.seg_len - 1) / p.seg_len);
+        const int longs = s.cnt - (s.len - (s.cnt - 1) * p.seg_len <= p.seg_len / 2);
+        s.n = Sums{{longs, s.cnt, s.cnt > 1 ? longs : 0, s.cnt > 1 ? s.cnt : 0}};
+        return s;
+    };
+    __shared__ int nseqs;
+    if (threadIdx.x == 0) nseqs = 0;
+    __syncthreads();
+    Sums total{{0, 0, 0, 0}}, all, before = total;
+    const bool once = p.nseq <= (int)blockDim.x;              // (the one scan has the totals too)
+    if (!once) {
+        Sums mine = total;
+        for (int i = threadIdx.x; i < p.nseq; i += blockDim.x) {
+            const Look s = look(i);
+            for (int e = 0; e < kSums; ++e) mine.v[e] += s.n.v[e];
         }
-        before.a += all.a;
-        before.b += all.b;
+        sums_before(mine, total);
     }
-    for (int64_t e = total.b + threadIdx.x; e < p.max_seg; e += blockDim.x) p.table[2 * e] = make_int4(-1, 0, 0, 0);
+    for (int base = 0; base < p.nseq; base += blockDim.x) {
+        const int i = base + (int)threadIdx.x;
+        const Look s = look(i);
+        Sums at = sums_before(s.n, all);
+        if (once) total = all;
+        for (int e = 0; e < kSums; ++e) at.v[e] += before.v[e];
+        const bool fits = at.v[1] + s.cnt <= p.max_seg && at.v[3] + s.n.v[3] <= p.max_cut;
+        if (s.cnt > 1 && fits) {
+            const int at_seq = atomicAdd(&nseqs, 1);
+            if (at_seq < p.max_seqs) p.seqs[at_seq] = make_int4(i, (int)at.v[3], s.cnt, 0);
+        }
+        for (int j = 0; j < s.cnt; ++j) {
+            const int4 u = make_int4(fits ? i : -1, j, s.cnt, min(p.seg_len, s.len - j * p.seg_len));
+            const int4 v = make_int4(s.start + j * p.seg_len, s.cnt > 1 ? (int)at.v[3] + j : 0, 0, 0);
+            auto list = [&](int4* table, int64_t most, int e) {
+                const int64_t order = j < (int)s.n.v[0] ? at.v[e] + j : total.v[e] + at.v[e + 1] - at.v[e];
+                if (order >= most) return false;
+                table[2 * order] = u;
+                table[2 * order + 1] = v;
+                return true;
+            };
+            const bool room = list(p.table, p.max_seg, 0);
+            if (!(s.cnt > 1 && list(p.cuts, p.max_cut, 2)) && !room) break;
+        }
+        for (int e = 0; e < kSums; ++e) before.v[e] += all.v[e];
+    }
+    const int4 none = make_int4(-1, 0, 0, 0);
+    for (int64_t e = total.v[1] + threadIdx.x; e < p.max_seg; e += blockDim.x) p.table[2 * e] = none;
+    for (int64_t e = total.v[3] + threadIdx.x; e < p.max_cut; e += blockDim.x) p.cuts[2 * e] = none;
+    __syncthreads();
+    for (int e = nseqs + (int)threadIdx.x; e < p.max_seqs; e += (int)blockDim.x) p.seqs[e] = none;
 }
 
 // g^n for g = exp(ld), the product ld * n carried in two fp32 parts.  Decays
@@ -479,7 +519,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     };
 
     // (without tokens, and without a state to pass on, the whole CTA leaves)
-    const Segment s = find_segment(p, order);
+    const Segment s = find_segment(p, STATE_ONLY ? p.cuts : p.table, order);
     if (chunks_of(s) == 0 && (STATE_ONLY || s.seq < 0 || r.fin == nullptr)) return;
     if (warp == L::LoadWarp) {
         if (lane == 0) {
@@ -1290,16 +1330,17 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
 // the final state.
 __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params p) {
     const Role& r = p.role[blockIdx.z];
-    const int seq = blockIdx.x / p.H, h = blockIdx.x % p.H;
-    int len = (int)p.T, sid0 = seq * p.nper, count = p.nper;
-    if (p.table) {
-        const int2 v = p.seqs[seq];
-        sid0 = v.x;
-        count = v.y;
+    const int h = blockIdx.x % p.H;
+    int seq = blockIdx.x / p.H, len = (int)p.T, sid0 = seq * p.nper, count = p.nper;
+    if (p.seqs) {                                             // packed
+        const int4 v = p.seqs[seq];
+        if (v.x < 0) return;
+        seq = v.x;
+        sid0 = v.y;
+        count = v.z;
         const int start = min(max(p.cu[seq], 0), (int)p.T);
         len = min(max(p.cu[seq + 1], start), (int)p.T) - start;
     }
-    if (count < 2) return;                                    // (the outputs' launch has its final state)
     // a tile of 32 x 32: a thread has four rows of a column of the segments'
     // states; where the first and the last state lie the other way, they go
     // through shared memory
@@ -1527,6 +1568,7 @@ cudaError_t launch_kernel(const Params& p, bool f16, bool exact, int kp, int vp,
 // head, role).
 struct Split {
     int64_t seg_len, nper, max_seg;           // nper: segments of a sequence (unpacked)
+    int64_t max_cut, max_seqs;                // segments of cut sequences (those with states in the workspace), cut sequences
     bool on;
 };
 
@@ -1541,7 +1583,7 @@ Split split_of(const fftconv_linear_attention_t& d, int nroles) {
     const int64_t sms = sm_count(), seqs = d.nseq > 0 ? d.nseq : d.B;
     const int64_t tasks = seqs * d.H * nroles;
     auto up = [](int64_t x) { return (x + kChunk - 1) / kChunk * kChunk; };
-    Split s{up(d.T), 1, seqs, false};
+    Split s{up(d.T), 1, seqs, 0, 0, false};
     int64_t len;
     if (d.nseq > 0) {
         // lengths are known on the device only.  Pieces a little longer than
@@ -1560,6 +1602,9 @@ Split split_of(const fftconv_linear_attention_t& d, int nroles) {
     s.seg_len = len;
     s.nper = (d.T + len - 1) / len;
     s.max_seg = d.nseq > 0 ? d.T / len + d.nseq : d.B * s.nper;
+    // (more than one segment: over len tokens, and fewer than 2 n / len segments of n)
+    s.max_cut = d.nseq > 0 && 2 * d.T / len < s.max_seg ? 2 * d.T / len : s.max_seg;
+    s.max_seqs = d.nseq > 0 && d.T / len < seqs ? d.T / len : seqs;
     s.on = true;
     return s;
 }
@@ -1605,9 +1650,14 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
     return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
 }
 
-// la_plan's table of segments and sequences
-int64_t plan_bytes(const fftconv_linear_attention_t& d, const Split& s) {
-    return pad256(s.max_seg * 2 * sizeof(int4)) + pad256(d.nseq * sizeof(int2));
+// la_plan's tables
+int64_t plan_bytes(const Split& s) {
+    return pad256(s.max_seg * 2 * sizeof(int4)) + pad256(s.max_cut * 2 * sizeof(int4)) +
+           pad256(s.max_seqs * sizeof(int4));
+}
+// the segments' states of a role
+int64_t state_bytes(const fftconv_linear_attention_t& d, const Split& s) {
+    return pad256(s.max_cut * d.H * d.K * d.V * 4);
 }
 
 size_t workspace_bytes(const fftconv_linear_attention_t& d, bool backward) {
@@ -1615,8 +1665,8 @@ size_t workspace_bytes(const fftconv_linear_attention_t& d, bool backward) {
     const int nroles = backward ? 3 : 1;
     const Split s = split_of(d, nroles);
     int64_t n = 0;
-    if (s.on) n += nroles * pad256(s.max_seg * d.H * d.K * d.V * 4);
-    if (s.on && d.nseq > 0) n += plan_bytes(d, s);
+    if (s.on) n += nroles * state_bytes(d, s);
+    if (s.on && d.nseq > 0) n += plan_bytes(s);
     if (backward) {
         if (d.Hq < d.H) n += pad256(d.T * d.B * d.H * d.K * 4);
         if (d.Hk < d.H) n += pad256(d.T * d.B * d.H * d.K * 4);
@@ -1636,14 +1686,17 @@ void fill(Params& p, const fftconv_linear_attention_t& d, const Split& s, const 
     p.nper = (int)s.nper;
     p.seg_len = (int)s.seg_len;
     p.max_seg = (int)s.max_seg;
+    p.max_cut = (int)s.max_cut;
+    p.max_seqs = (int)s.max_seqs;
     p.in_place = 0;
 }
 
-// The table of packed sequences that may be cut, at ws.
+// The tables of packed sequences that may be cut, at ws.
 cudaError_t plan(Params& p, const fftconv_linear_attention_t& d, const Split& s, uint8_t* ws, cudaStream_t stream) {
     if (!s.on || d.nseq == 0) return cudaSuccess;
     p.table = reinterpret_cast<int4*>(ws);
-    p.seqs = reinterpret_cast<int2*>(ws + pad256(s.max_seg * 2 * sizeof(int4)));
+    p.cuts = reinterpret_cast<int4*>(ws + pad256(s.max_seg * 2 * sizeof(int4)));
+    p.seqs = reinterpret_cast<int4*>((uint8_t*)p.cuts + pad256(s.max_cut * 2 * sizeof(int4)));
     la_plan<<<1, d.nseq < 1024 ? (unsigned)(d.nseq + 31) / 32 * 32 : 1024, 0, stream>>>(p);
     return cudaPeekAtLastError();
 }
@@ -1657,12 +1710,11 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
     bool exact = false;                       // a state is a result
     for (int i = 0; i < p.nroles; ++i) exact |= p.role[i].fin != nullptr;
     if (s.on) {
-        cudaError_t e = launch_kernel<true>(p, f16, exact, kp, vp, ctas, stream);
+        cudaError_t e = launch_kernel<true>(p, f16, exact, kp, vp, s.max_cut * d.H * p.nroles, stream);
         if (e != cudaSuccess) return e;
-        const int64_t seqs = d.nseq > 0 ? d.nseq : d.B;
         void* args[] = {const_cast<Params*>(&p)};
         e = cudaLaunchKernel(reinterpret_cast<const void*>(la_combine),
-                             dim3((unsigned)(seqs * d.H), (unsigned)((d.K + 31) / 32 * ((d.V + 31) / 32)), (unsigned)p.nroles),
+                             dim3((unsigned)(s.max_seqs * d.H), (unsigned)((d.K + 31) / 32 * ((d.V + 31) / 32)), (unsigned)p.nroles),
                              dim3(256), args, 0, stream);
         if (e != cudaSuccess) return e;
     }
@@ -1761,7 +1813,7 @@ int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void
     p.in_place = sp.on && initial_state && final_state == initial_state;
     cudaError_t e = cudaSuccess;
     if (d.nseq > 0 && d.zero_rest) e = zero_rest(o, d, d.H, d.V, d.o_stride, cu_seqlens, s);
-    if (e == cudaSuccess) e = plan(p, d, sp, (uint8_t*)workspace + pad256(sp.max_seg * d.H * d.K * d.V * 4), s);
+    if (e == cudaSuccess) e = plan(p, d, sp, (uint8_t*)workspace + state_bytes(d, sp), s);
     if (e == cudaSuccess) e = run_roles(p, d, sp, d.K > 64 ? 128 : 64, d.V > 64 ? 128 : 64, s);
     return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "linear attention launch");
 }
@@ -1830,8 +1882,8 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
     };
     float* seg[3] = {nullptr, nullptr, nullptr};
     if (sp.on)
-        for (int i = 0; i < 3; ++i) seg[i] = (float*)take(sp.max_seg * d.H * d.K * d.V * 4);
-    uint8_t* const table = sp.on && d.nseq > 0 ? take(plan_bytes(d, sp)) : nullptr;
+        for (int i = 0; i < 3; ++i) seg[i] = (float*)take(state_bytes(d, sp));
+    uint8_t* const table = sp.on && d.nseq > 0 ? take(plan_bytes(sp)) : nullptr;
     float* part[3] = {nullptr, nullptr, nullptr};
     if (d.Hq < d.H) part[0] = (float*)take(tok * d.H * d.K * 4);
     if (d.Hk < d.H) part[1] = (float*)take(tok * d.H * d.K * 4);

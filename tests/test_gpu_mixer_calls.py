@@ -151,3 +151,52 @@ def test_forward_mode_derivatives_are_refused():
         dual = forward_ad.make_dual(x.clone().requires_grad_(), torch.ones_like(x))
         with pytest.raises(NotImplementedError):
             lsf.group_norm(dual, 4)
+
+
+def test_packed_training_batch_of_many_short_sequences():
+    """What a call takes beside its tensors does not grow with the number of
+    sequences; the gradients are those of the sequences one by one."""
+    import long_sequence_fft_b200 as lsf
+    lens = [64] * 500 + [3000] + [1] * 40
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    T, H, D = cu[-1], 16, 128
+    q, k, v, do = (_randn(i, 1, T, H, D).bfloat16() for i in range(4))
+    ld = torch.linspace(-0.3, -0.001, H, device="cuda")
+    leaves = [t.requires_grad_() for t in (q, k, v)]
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    o = lsf.linear_attention(*leaves, ld, cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"))
+    got = torch.autograd.grad(o, leaves, do)
+    torch.cuda.synchronize()
+    # the output, three gradients, and states of a few segments (541 would be 1.7 GB)
+    assert torch.cuda.max_memory_allocated() - held < 4 * q.numel() * 2 + (100 << 20)
+    for i in (0, 499, 500, 540):
+        a, e = cu[i], cu[i + 1]
+        part = [t[:, a:e].detach().clone().requires_grad_() for t in leaves]
+        one = lsf.linear_attention(*part, ld)
+        for x, y in zip([o, *got], [one, *torch.autograd.grad(one, part, do[:, a:e].contiguous())]):
+            x, y = x[:, a:e].double(), y.double()
+            # two roundings of each side (mixer_reference)
+            assert ((x - y).norm() / y.norm()).item() <= 2 * 0.85 * 2.0 ** -8
+    assert lsf.linear_attention_status() == 0
+
+
+def test_offsets_that_decrease():
+    """Not a meaning, but no access outside either: the workspace's lists keep
+    their bounds, and a call after it is right."""
+    import long_sequence_fft_b200 as lsf
+    T, H = 6000, 2
+    q, k, v = (_randn(i, 1, T, H, 64).bfloat16() for i in range(3))
+    ld = torch.tensor([-0.3, -0.01], device="cuda")
+    good = torch.tensor([0, 3000, 3100, 6000], dtype=torch.int32, device="cuda")
+    want = lsf.linear_attention(q, k, v, ld, cu_seqlens=good, return_state=True)
+    for bad in ([0, 6000, 0, 6000], [5000, 100, 6000, 0], [0, 6000] * 40, [6000, 0] * 30):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        o, s = lsf.linear_attention(q, k, v, ld, cu_seqlens=cu, return_state=True)
+        assert o.shape == v.shape and s.shape[0] == len(bad) - 1
+        assert lsf.linear_attention_status() == 0
+    for a, b in zip(lsf.linear_attention(q, k, v, ld, cu_seqlens=good, return_state=True), want):
+        assert torch.equal(a, b)

@@ -47,3 +47,34 @@ def test_norm_workspace_of_a_wide_long_call():
     """32768 x 2048 values in 16 groups: a small part of the tensor's 134 MB."""
     assert _norm_bytes(32768, 1, 2048, 16) == 148 * 3 * 2 * 2048 * 4
     assert _norm_bytes(131072, 1, 8192, 64) <= 30 << 20
+
+
+def _attention_bytes(backward, **kw):
+    from long_sequence_fft_b200.linear_attention import _pack_shape
+    f = dict(B=1, T=1 << 17, nseq=2048, H=16, K=128, V=128)
+    f.update(kw)
+    H, K, V, T = f["H"], f["K"], f["V"], f["T"]
+    rows = lambda d: (T * H * d, H * d, d)                                   # noqa: E731
+    shape = _pack_shape.pack(f["B"], T, f["nseq"], H, H, H, H, K, V, 2, 1.0, 1, *rows(K), *rows(K), *rows(V), *rows(V))
+    return _lib().fftconv_linear_attention_workspace_bytes(shape, backward)
+
+
+@pytest.mark.parametrize("backward,roles", [(0, 1), (1, 3)])
+def test_packed_workspace_does_not_grow_with_short_sequences(backward, roles):
+    """States are kept for the segments of sequences that may be cut: fewer
+    than twice as many as pieces of the length that a cut takes, whatever the
+    number of sequences; a sequence more costs its place in the plan."""
+    state = 16 * 128 * 128 * 4
+    few, many = (_attention_bytes(backward, nseq=n) for n in (64, 1 << 16))
+    assert many - few <= ((1 << 16) - 64) * 32 + 256
+    # a piece is 5/4 of an SM's share of heads x roles x tokens, in tiles of 128 tokens
+    pieces = 148 * 4 // (5 * 16 * roles) + 1
+    assert few <= roles * 2 * pieces * state + (1 << 16)
+    assert many < 128 << 20
+
+
+def test_packed_workspace_of_few_long_sequences():
+    """No more segments than there are: one sequence of all tokens."""
+    state = 2 * 64 * 64 * 4
+    size = _attention_bytes(0, nseq=1, T=8192, H=2, K=64, V=64)
+    assert 0 < size <= (8192 // 512 + 1) * (state + 64) + 1024
