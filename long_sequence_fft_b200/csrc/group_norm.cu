@@ -47,6 +47,8 @@ struct Args {
     int64_t N, S, ldx, ldg, ldy;
     int C, G, D;
     int w_f32, act, chunks, parts;
+    int add;                     // dw and db are added to (samples before these)
+    int keep;                    // forward: mean and rstd are the caller's
     float eps;
 };
 
@@ -584,7 +586,10 @@ __device__ __forceinline__ void sum_parts(const Args& a, int block) {
     __syncthreads();
     s = lanes_sum<32>(sh[threadIdx.x % 32][r0]);
     const int c = block * 32 + r0;
-    if (threadIdx.x % 32 == 0 && c < 2 * a.C) (c < a.C ? a.dw[c] : a.db[c - a.C]) = s;
+    if (threadIdx.x % 32 == 0 && c < 2 * a.C) {
+        float& sum = c < a.C ? a.dw[c] : a.db[c - a.C];
+        sum = a.add ? sum + s : s;
+    }
 }
 __global__ void __launch_bounds__(1024) gn_sum_parts(const Args a) { sum_parts(a, blockIdx.x); }
 
@@ -594,6 +599,9 @@ __global__ void __launch_bounds__(1024) gn_sum_parts(const Args a) { sum_parts(a
 // vectors of its channels: thread = (vector column, row lane).  The blocks of
 // a sample so read one window of memory together: 8 x 4096 x 768 fp32 applies
 // the backward pass in 38.2 us, 41.1 with a contiguous range for each block.
+// Where the partial results of all samples would take over kPartBytes, some
+// samples at a time go through all passes, so that a call's workspace does not
+// grow with their number, and the passes find each other's results in L2.
 
 struct Tile {
     int n, chunk, colv, rl, rows;             // rows: row lanes
@@ -755,35 +763,42 @@ __global__ void __launch_bounds__(kThreads, 3) gn_stats(const Args a) {
     // one warp a group: its channels in every row lane
     const int c0 = (int)blockIdx.y * kThreads * V, c1 = c0 + width * V;
     const int lane = threadIdx.x % 32;
-    for (int g = threadIdx.x / 32; g < a.G; g += (int)blockDim.x / 32) {
+    const bool all = gridDim.y == 1;
+    const int g0 = all ? 0 : c0 / a.D, g1 = all ? a.G : (c1 - 1) / a.D + 1;
+    for (int g = g0 + threadIdx.x / 32; g < g1; g += (int)blockDim.x / 32) {
         float gn = 0.f, gm = 0.f, gq = 0.f;
         const int lo = max(g * a.D, c0) - c0, hi = min((g + 1) * a.D, c1) - c0;
-        if (hi > lo) {
-            for (int e = lane; e < (hi - lo) * t.rows; e += 32) {
-                const int row = e / (hi - lo), at = row * width * V + lo + e % (hi - lo);
-                join(gn, gm, gq, sh_n[row], sh_m[at], sh_q[at]);
-            }
-            for (int d = 16; d > 0; d >>= 1) {
-                const float n2 = __shfl_down_sync(0xffffffffu, gn, d), m2 = __shfl_down_sync(0xffffffffu, gm, d),
-                            q2 = __shfl_down_sync(0xffffffffu, gq, d);
-                join(gn, gm, gq, n2, m2, q2);
-            }
+        for (int e = lane; e < (hi - lo) * t.rows; e += 32) {
+            const int row = e / (hi - lo), at = row * width * V + lo + e % (hi - lo);
+            join(gn, gm, gq, sh_n[row], sh_m[at], sh_q[at]);
+        }
+        for (int d = 16; d > 0; d >>= 1) {
+            const float n2 = __shfl_down_sync(0xffffffffu, gn, d), m2 = __shfl_down_sync(0xffffffffu, gm, d),
+                        q2 = __shfl_down_sync(0xffffffffu, gq, d);
+            join(gn, gm, gq, n2, m2, q2);
         }
         if (lane == 0) {
-            const int64_t e = ((int64_t)t.n * a.G + g) * a.parts + (int64_t)blockIdx.y * a.chunks + t.chunk;
+            const int column = (int)blockIdx.y - g * a.D / (kThreads * V);    // among the blocks with channels of the group
+            const int64_t e = ((int64_t)t.n * a.G + g) * a.parts + (int64_t)column * a.chunks + t.chunk;
             reinterpret_cast<float4*>(a.part)[e] = make_float4(gn, gm, gq, 0.f);
         }
     }
 }
 
-// One warp a (sample, group): joins its parts.
-__global__ void __launch_bounds__(kThreads) gn_join_stats(const Args a) {
+// One warp a (sample, group): joins its parts, those of every block of
+// `columns` channels that the group reaches into.
+__global__ void __launch_bounds__(kThreads) gn_join_stats(const Args a, int columns) {
     const int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
     if (p >= a.N * a.G) return;
     const int lane = threadIdx.x % 32;
+    int parts = a.chunks;
+    if (a.parts > a.chunks) {
+        const int c0 = (int)((uint32_t)p % (uint32_t)a.G) * a.D;              // (N G is below 2^31)
+        parts *= (c0 + a.D - 1) / columns - c0 / columns + 1;
+    }
     float n = 0.f, m = 0.f, q = 0.f;
 #pragma unroll 4
-    for (int e = lane; e < a.parts; e += 32) {
+    for (int e = lane; e < parts; e += 32) {
         const float4 v = reinterpret_cast<const float4*>(a.part)[p * a.parts + e];
         join(n, m, q, v.x, v.y, v.z);
     }
@@ -1007,13 +1022,20 @@ int64_t chunks_of(int64_t N, int64_t S, int64_t C, int V) {
     if (want > S) want = S;
     return want > 1 ? want : 1;
 }
-int64_t most_chunks(int64_t N, int64_t S, int64_t C) {
-    int64_t m = 1;
-    for (int V : {1, 4, 8}) {
-        const int64_t k = chunks_of(N, S, C, V);
-        if (k > m) m = k;
-    }
-    return m;
+constexpr int64_t kPartBytes = 64 << 20;      // half of L2
+
+int64_t columns_of(int64_t C, int V) { return (C / V + kThreads - 1) / kThreads; }
+// Blocks of columns with channels of one group, at most.
+int64_t spread_of(int64_t C, int64_t G, int V) {
+    const int64_t width = kThreads * V, most = (C / G + width - 2) / width + 1, cols = columns_of(C, V);
+    return most < cols ? most : cols;
+}
+// Samples that go through the sample form's passes together.
+int64_t samples_at_once(int64_t N, int64_t S, int64_t C, int64_t G, int V, bool back) {
+    const int64_t chunks = chunks_of(N, S, C, V);
+    const int64_t bytes = back ? chunks * 2 * C * 4 + G * 8 : chunks * spread_of(C, G, V) * G * 16 + G * 8;
+    const int64_t most = kPartBytes / bytes > 1 ? kPartBytes / bytes : 1, times = (N + most - 1) / most;
+    return times > 1 ? (N + times - 1) / times : N;
 }
 
 // Lanes and vectors a lane of the token form for groups of nvec vectors of V
@@ -1087,24 +1109,43 @@ void token(Args a, int lanes, int per, bool back, cudaStream_t s) {
 
 template <typename T, int V, bool WHOLE, bool GATED>
 void sample_of(Args a, bool back, cudaStream_t s) {
-    const unsigned cols = (unsigned)((a.C / V + kThreads - 1) / kThreads);
+    const unsigned cols = (unsigned)columns_of(a.C, V);
     a.chunks = (int)chunks_of(a.N, a.S, a.C, V);
-    const dim3 grid((unsigned)(a.N * a.chunks), cols);
     const int threads = sample_threads(a.S, a.C, V);
-    if (!back) {
-        a.parts = (int)cols * a.chunks;
-        gn_stats<T, V><<<grid, threads, 0, s>>>(a);
-        gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a);
-        gn_apply<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
-    } else {
-        a.parts = (int)(a.N * a.chunks);
-        gn_grad_sums<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
-        const int64_t values = (int64_t)a.D * a.chunks;
-        if (a.dw)
-            gn_join_sums<T><<<(unsigned)(a.N * a.G + (2 * a.C + 31) / 32), 1024, 0, s>>>(a);
-        else
-            gn_join_sums<T><<<(unsigned)(a.N * a.G), values > 256 ? 1024 : 256, 0, s>>>(a);
-        gn_grad_apply<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
+    const int64_t all = a.N, step = samples_at_once(a.N, a.S, a.C, a.G, V, back);
+    auto on = [](auto& p, int64_t by) {
+        if (p) p = (std::remove_reference_t<decltype(p)>)((const uint8_t*)p + by);
+    };
+    for (int64_t n0 = 0; n0 < all; n0 += step) {
+        a.N = step < all - n0 ? step : all - n0;
+        const dim3 grid((unsigned)(a.N * a.chunks), cols);
+        if (!back) {
+            a.parts = (int)(spread_of(a.C, a.G, V) * a.chunks);
+            gn_stats<T, V><<<grid, threads, 0, s>>>(a);
+            gn_join_stats<<<(unsigned)((a.N * a.G + 7) / 8), kThreads, 0, s>>>(a, kThreads * V);
+            gn_apply<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
+        } else {
+            a.parts = (int)(a.N * a.chunks);
+            a.add = n0 > 0;
+            gn_grad_sums<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
+            const int64_t values = (int64_t)a.D * a.chunks;
+            if (a.dw)
+                gn_join_sums<T><<<(unsigned)(a.N * a.G + (2 * a.C + 31) / 32), 1024, 0, s>>>(a);
+            else
+                gn_join_sums<T><<<(unsigned)(a.N * a.G), values > 256 ? 1024 : 256, 0, s>>>(a);
+            gn_grad_apply<T, V, WHOLE, GATED><<<grid, threads, 0, s>>>(a);
+        }
+        const int64_t rows = step * a.S, es = sizeof(T);
+        on(a.x, rows * a.ldx * es);
+        on(a.gate, rows * a.ldg * es);
+        on(a.dy, rows * a.ldy * es);
+        on(a.y, rows * a.C * es);
+        on(a.dx, rows * a.C * es);
+        on(a.dgate, rows * a.C * es);
+        if (a.keep || back) {                                 // (else they lie in the workspace)
+            on(a.mean, step * a.G * 4);
+            on(a.rstd, step * a.G * 4);
+        }
     }
 }
 
@@ -1144,34 +1185,41 @@ int64_t pad256(int64_t b) { return (b + 255) / 256 * 256; }
 
 int vec_of(int dtype) { return dtype == FFTCONV_F32 ? 4 : 8; }
 
-// Rows of partial sums that the token form's backward pass writes with vectors
-// of V elements (0: not the token form): those of its row blocks' sub-warps.
-int64_t token_parts(int64_t N, int64_t S, int64_t C, int64_t G, int V) {
+// Workspace of a call with vectors of V elements: the sample form's sums (or
+// mean and rstd where the caller keeps none), then partial results.  Sizes of 0
+// where a form has none.
+struct Space {
+    int64_t sums, part;
+};
+Space space_of(int64_t N, int64_t S, int64_t C, int64_t G, int V, bool back) {
     const int64_t D = C / G;
     int lanes = 0, per = 0;
-    if (S != 1 || D % V) return 0;
-    token_shape(D / V, V, lanes, per);
-    if (lanes == 0) return 0;
-    const TokenGrid t = token_grid(N, G, lanes, rows_at_once(per, true));
-    return (int64_t)t.gx * t.rsubs;
+    if (S == 1 && D % V == 0) token_shape(D / V, V, lanes, per);
+    if (lanes > 0) {
+        // rows of the token form's blocks' sub-warps
+        const TokenGrid t = token_grid(N, G, lanes, rows_at_once(per, back));
+        return {0, back ? pad256((int64_t)t.gx * t.rsubs * 2 * C * 4) : 0};
+    }
+    const int64_t n = samples_at_once(N, S, C, G, V, back), chunks = chunks_of(N, S, C, V);
+    return back ? Space{pad256(n * G * 8), pad256(n * chunks * 2 * C * 4)}
+                : Space{2 * pad256(n * G * 4), pad256(n * chunks * spread_of(C, G, V) * G * 16)};
 }
 
-// Sized for any vector width (which depends on strides, and on the type).
-size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool bwd) {
+// The largest of the vector widths that a call may take (which depends on
+// strides and on the type).
+size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool back) {
     if (N == 0 || S == 0 || C == 0) return 0;
-    const bool token = S == 1 && C / G <= 256;                // whatever the width
-    const int64_t chunks = most_chunks(N, S, C);
-    if (!bwd) {
-        if (token) return 0;
-        // parts of the statistics, and mean and rstd when the caller keeps none
-        return (size_t)(pad256(N * G * chunks * ((C + kThreads - 1) / kThreads) * 16) + 2 * pad256(N * G * 4));
-    }
-    int64_t parts = token ? 0 : N * chunks;
+    Args a{};
+    a.S = S;
+    a.C = (int)C;
+    a.D = (int)(C / G);
+    int64_t most = 0;
     for (int V : {1, 4, 8}) {
-        const int64_t rows = token_parts(N, S, C, G, V);
-        if (rows > parts) parts = rows;
+        if (V > 1 && !use_vectors(a, V, true)) continue;
+        const Space w = space_of(N, S, C, G, V, back);
+        if (w.sums + w.part > most) most = w.sums + w.part;
     }
-    return (size_t)(pad256(parts * 2 * C * 4) + (token ? 0 : pad256(N * G * 8)));
+    return (size_t)most;
 }
 
 int check(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int wdtype, int act, bool affine) {
@@ -1182,8 +1230,7 @@ int check(int64_t N, int64_t S, int64_t C, int64_t G, int dtype, int wdtype, int
     if (affine && wdtype != dtype && wdtype != FFTCONV_F32)
         return fail(FFTCONV_ERR_INVALID_ARG, "weight and bias must have x's type or fp32");
     if (act < FFTCONV_ACT_NONE || act > FFTCONV_ACT_SIGMOID) return fail(FFTCONV_ERR_INVALID_ARG, "unknown activation");
-    if (C > 65535 * kThreads || (double)N * (double)G >= 2147483647.0 ||
-        (double)N * (double)most_chunks(N, S ? S : 1, C) + (double)C >= 2147483647.0)
+    if (C > 65535 * kThreads || (double)N * (double)G >= 2147483647.0 || (double)N + (double)C >= 2147483647.0 - 444.0)
         return fail(FFTCONV_ERR_UNSUPPORTED, "too many channels, samples or groups");
     return FFTCONV_OK;
 }
@@ -1251,13 +1298,12 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
     const bool vec = use_vectors(a, V, rows == 1 || (ld_x % V == 0 && (!gate || ld_gate % V == 0)));
     a.mean = mean;
     a.rstd = rstd;
-    if (need) {
-        const int64_t parts = pad256(N * G * most_chunks(N, S, C) * ((C + kThreads - 1) / kThreads) * 16);
-        a.part = (float*)workspace;
-        if (!mean) {
-            a.mean = (float*)((uint8_t*)workspace + parts);
-            a.rstd = (float*)((uint8_t*)workspace + parts + pad256(N * G * 4));
-        }
+    a.keep = mean != nullptr;
+    const Space space = space_of(N, S, C, G, vec ? V : 1, false);
+    a.part = (float*)((uint8_t*)workspace + space.sums);
+    if (!mean && space.sums) {
+        a.mean = (float*)workspace;
+        a.rstd = (float*)((uint8_t*)workspace + space.sums / 2);
     }
     dispatch(dtype, vec, [&](auto* t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
@@ -1321,9 +1367,8 @@ int fftconv_group_norm_backward(const void* x, const void* gate, const void* wei
     const int V = vec_of(dtype);
     const bool vec =
         use_vectors(a, V, rows == 1 || (ld_x % V == 0 && ld_dy % V == 0 && (!gate || ld_gate % V == 0)));
-    const int64_t sums = S == 1 && C / G <= 256 ? 0 : pad256(N * G * 8);
     a.sums = (float*)workspace;
-    a.part = (float*)((uint8_t*)workspace + sums);
+    a.part = (float*)((uint8_t*)workspace + space_of(N, S, C, G, vec ? V : 1, true).sums);
     dispatch(dtype, vec, [&](auto* t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         run<T, decltype(v)::value>(a, true, s);

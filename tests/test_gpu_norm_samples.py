@@ -1,0 +1,68 @@
+"""GPU tests of group norm's sample form where its samples go through the
+passes some at a time, and where groups lie across blocks of channels; the
+bounds are those of test_gpu_group_norm."""
+import pytest
+
+from test_gpu_group_norm import _check, _inputs, _run
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.mark.parametrize("shape,G,dtype,gate,affine", [
+    ((9001, 2048), 2, "bf16", False, True),    # one position, groups of over 512 channels: three times 3001 rows
+    ((9001, 2048), 2, "f32", True, True),
+    ((4500, 4104), 3, "f16", True, False),     # ... that are no whole blocks
+    ((13001, 1290), 2, "bf16", False, True),   # ... nor whole vectors
+    ((120001, 2, 96), 32, "bf16", False, True),
+    ((30011, 3, 512), 512, "f32", True, True),  # as many groups as channels
+    ((3001, 5, 2304), 2304, "f16", False, True),
+])
+def test_some_samples_at_a_time(shape, G, dtype, gate, affine):
+    import long_sequence_fft_b200 as lsf
+    N, S, C = shape[0], shape[1] if len(shape) == 3 else 1, shape[-1]
+    assert lsf.library().fftconv_group_norm_workspace_bytes(N, S, C, G, 1) > 16 << 20
+    x = _inputs(shape, dtype, seed=N, gate=gate, affine=affine)
+    _check(_run(x, G, "silu"), x, G, "silu", what=f"{shape} G={G} {dtype}")
+
+
+@pytest.mark.parametrize("shape,G", [((3, 7, 6000), 40), ((2, 5, 4104), 27), ((2, 3, 16384), 16384), ((2, 9, 8200), 1),
+                                     ((4, 50, 2056), 257)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("gate", [False, True])
+def test_groups_across_blocks_of_channels(shape, G, dtype, gate):
+    x = _inputs(shape, dtype, seed=G, gate=gate, affine=True)
+    _check(_run(x, G, "silu"), x, G, "silu", what=f"{shape} G={G} {dtype}")
+
+
+def test_some_samples_at_a_time_in_rows_of_wider_tensors():
+    """Strides of x, gate and gradient that differ, over several rounds; the
+    same call captured; sums that repeat bit for bit."""
+    import long_sequence_fft_b200 as lsf
+    N, C, G = 9001, 2048, 2
+    x = _inputs((N, C), "bf16", seed=3, gate=True, affine=True)
+    wide = torch.empty((N, 3, C), device="cuda", dtype=torch.bfloat16)
+    wide[:, 0], wide[:, 2] = x["x"], x["gate"]
+    whole = wide.requires_grad_()
+    w, b = x["weight"].clone().requires_grad_(), x["bias"].clone().requires_grad_()
+
+    def call():
+        y = lsf.group_norm(whole[:, 0], G, w, b, gate=whole[:, 2], activation="silu")
+        dy = torch.cat([x["dy"], x["dy"]], 1)[:, :C]
+        return [y, *torch.autograd.grad(y, [whole, w, b], dy)]
+
+    got = _run(x, G, "silu")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        captured = call()
+    g.replay()
+    torch.cuda.synchronize()
+    for y, dwide, dw, db in (call(), captured):
+        for a, e in ((y, "y"), (dwide[:, 0], "dx"), (dwide[:, 2], "dgate"), (dw, "dweight"), (db, "dbias")):
+            assert torch.equal(a, got[e]), e

@@ -78,3 +78,13 @@ def test_packed_workspace_of_few_long_sequences():
     state = 2 * 64 * 64 * 4
     size = _attention_bytes(0, nseq=1, T=8192, H=2, K=64, V=64)
     assert 0 < size <= (8192 // 512 + 1) * (state + 64) + 1024
+
+
+@pytest.mark.parametrize("S,C,G", [(1, 4096, 1), (1, 1032, 2), (1, 520, 1), (2, 1024, 1024), (16, 4096, 4096),
+                                   (4, 96, 32), (5, 35, 7), (64, 768, 12), (3, 65536, 8)])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_norm_workspace_does_not_grow_with_samples(S, C, G, backward):
+    """Partial results of some samples at a time."""
+    sizes = [_norm_bytes(N, S, C, G, backward) for N in (1, 8, 444, 5000, 1 << 17)]
+    assert max(sizes) <= (64 << 20) + 1024
+    assert sizes[0] > 0 and sizes[0] < 1 << 23
