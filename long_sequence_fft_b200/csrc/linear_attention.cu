@@ -246,6 +246,17 @@ __device__ __forceinline__ float decay_power(float ld, float n) {
     return n == 0.f ? 1.f : fmaf(e, fmaf(ld, n, -p), e);
 }
 
+// g^n in two fp32 parts, for powers that are applied again and again: a walk
+// over 512 chunks with g^128 rounded once was off by 1.7e-5, in a direction.
+// Decays of over a half keep one part: what they weigh is gone before the
+// error counts (X factors of it: 2 X 2^-23 relative of exp(-X)).
+__device__ __forceinline__ float2 decay_power2(float ld, float n) {
+    const float p = ld * n;
+    if (!(fabsf(p) < 0.5f)) return make_float2(decay_power(ld, n), 0.f);
+    const float e = expm1f(p), d = fmaf(fmaf(ld, n, -p), 1.f + e, e), hi = 1.f + d;
+    return make_float2(hi, (1.f - hi) + d);
+}
+
 __device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
@@ -422,11 +433,11 @@ struct Layout {
     static constexpr int OffCarry = Stages * StageBytes;
     static constexpr int OffTab = OffCarry + CarryBytes;      // a g^|d| or 0, d = j - i in [-32, 31]
     static constexpr int OffCol = OffTab + 64 * 4;            // column weights of an unmasked block of P
-    static constexpr int OffPow = OffCol + 32 * 4;            // g^e, e <= 128
+    static constexpr int OffPow = OffCol + 32 * 4;            // g^e, e <= 128; g^128 in two parts (129, 130)
     static constexpr int OffKw = OffPow + 132 * 4;            // key weights of the chunk
     static constexpr int OffMisc = OffKw + 128 * 4;           // abort (word 6), TMEM base (7), scales
     static constexpr int OffBar = OffMisc + 128;
-    static constexpr int Bars = 28 + (F16 ? 4 : 0);
+    static constexpr int Bars = 29 + (F16 ? 4 : 0);
     static constexpr int OffMax = OffBar + (Bars + 1) / 2 * 16;   // (fp16) channel maxima [2][state warps][32]
     static constexpr int Bytes = OffMax + (F16 ? 2 * kStateWarps * 32 * 2 : 0);
     // TMEM columns
@@ -487,7 +498,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     // state warps may be done with chunk c + 1 before the MMA warp has seen
     // chunk c, and two phases of one barrier look like none
     auto kt_ready = [&](int c) { return c % L::KtBufs ? bars + 27 : bars + 20; };
-    uint64_t* pair_bar = bars + 28;                           // [4] (fp16) the two state warps of the same channels
+    uint64_t* pow_ready = bars + 28;                          // g^128's two parts
+    uint64_t* pair_bar = bars + 29;                           // [4] (fp16) the two state warps of the same channels
 
     const int tid = threadIdx.x;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -530,6 +542,7 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             for (int i = 8; i < 14; ++i) mbar_init(bars + i, 1);
             for (int i = 14; i < 18; ++i) mbar_init(bars + i, 4);
             mbar_init(bar_st, 1);
+            mbar_init(pow_ready, 1);
             mbar_init(bar_kt, 1);
             for (int i = 20; i < 26; ++i) mbar_init(bars + i, L::Live);
             mbar_init(bar_fin, STATE_ONLY ? 1 : 3);
@@ -682,6 +695,14 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         // should meet a large one.
         const uint32_t id = idesc_f16_f32(128, VP) | kFmt | kTransB;
         const uint32_t sb = smem_u32(smem), t_c = tbase + L::C;
+        if (!STATE_ONLY && lane == 0) {
+            // (by a warp that has nothing to do before the first keys are weighed)
+            const float2 whole = decay_power2(p.log_decay[h], 128.f);
+            pw[129] = whole.x;
+            pw[130] = whole.y;
+            mbar_arrive(pow_ready);
+        }
+        __syncwarp();
         bool ok = true;
         for (int c = 0; c < nch; ++c) {
             const int st = c % L::Stages;
@@ -996,12 +1017,25 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
             }
         }
         // state <- g^n state + (own state of chunk c), once its products are
-        // done; from the end: state <- state + g^(tokens after it) (own state)
-        float after = 1.f;
+        // done; from the end: state <- state + g^(tokens after it) (own state).
+        // What rounding a chunk's g^128 leaves out (drift) is put into the next
+        // one's, so the product of any of them is off by one rounding or two.
+        int behind = 0;
+        float drift = 0.f, keep128 = 1.f;
+        const float ld = STATE_ONLY ? p.log_decay[h] : 0.f;
         auto advance = [&](int c) -> bool {
+            float after = 1.f;
+            if constexpr (STATE_ONLY) {
+                after = decay_power(ld, (float)behind);
+                behind += chunk_n(c);
+            } else if (c == 0) {
+                if (!wait(pow_ready, 0)) return false;
+                keep128 = pw[129];
+                drift = -pw[130];
+            }
             if (!wait(bar_st, c)) return false;
             tc_fence_after();
-            const float keep = STATE_ONLY ? 1.f : pw[chunk_n(c)], inv = 1.f / rs_done;
+            const float keep = STATE_ONLY ? 1.f : chunk_n(c) == kChunk ? keep128 : pw[chunk_n(c)], inv = 1.f / rs_done;
 #pragma unroll
             for (int blk = 0; blk < kCols / 32; ++blk) {
                 uint32_t s[32];
@@ -1016,7 +1050,11 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                         state[blk * 32 + j] = fmaf(keep, state[blk * 32 + j], own);
                 }
             }
-            after *= pw[chunk_n(c)];
+            if constexpr (!STATE_ONLY) {
+                const float rest = pw[130] - drift;
+                keep128 = pw[129] + rest;
+                drift = (keep128 - pw[129]) - rest;
+            }
             return true;
         };
         // the state in front of chunk c, and its copy for the carry product
@@ -1353,7 +1391,7 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
     const int nrow = row0 + y, ncol = col0 + x4;              // of a state in rows
     const bool in = row < r.kd && col < r.vd, nin = nrow < r.kd && ncol < r.vd;
     const float ld = p.log_decay[h];
-    const float whole = decay_power(ld, (float)p.seg_len);
+    const float2 whole = decay_power2(ld, (float)p.seg_len);
     const float tail = decay_power(ld, (float)(len - (count - 1) * p.seg_len));
     const int64_t step = (int64_t)p.H * mat / 4;
     float4* at = reinterpret_cast<float4*>(r.seg + ((int64_t)sid0 * p.H + h) * mat + (int64_t)col * r.kd + row);
@@ -1391,11 +1429,11 @@ __global__ void __launch_bounds__(256) la_combine(const __grid_constant__ Params
             const int i = r.rev ? count - 1 - s - q : s + q;
             if (s + q > 0 || p.in_place) at[(int64_t)i * step] = run;       // (the first one is init)
             if (s + q < have) {
-                const float g = i == count - 1 ? tail : whole;
-                run.x = fmaf(g, run.x, local[q].x);
-                run.y = fmaf(g, run.y, local[q].y);
-                run.z = fmaf(g, run.z, local[q].z);
-                run.w = fmaf(g, run.w, local[q].w);
+                const float2 g = i == count - 1 ? make_float2(tail, 0.f) : whole;
+                run.x = fmaf(g.x, run.x, fmaf(g.y, run.x, local[q].x));
+                run.y = fmaf(g.x, run.y, fmaf(g.y, run.y, local[q].y));
+                run.z = fmaf(g.x, run.z, fmaf(g.y, run.z, local[q].z));
+                run.w = fmaf(g.x, run.w, fmaf(g.y, run.w, local[q].w));
             }
         }
     }
