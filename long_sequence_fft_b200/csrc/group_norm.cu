@@ -703,7 +703,7 @@ __device__ __forceinline__ void join(float& n, float& m, float& q, float n2, flo
     if (n2 == 0.f) return;
     const float d = m2 - m, f = n2 / t;
     m = fmaf(d, f, m);
-    q += q2 + d * d * n * f;
+    q += q2 + d * (n * f) * d;                                // (the first set: 0 whatever d, whose square may overflow)
     n = t;
 }
 
@@ -745,8 +745,9 @@ __global__ void __launch_bounds__(kThreads, 3) gn_stats(const Args a) {
             // joined with the positions before
             fma_v<V>(d, m, minus, sum);
             fma_v<V>(m, d, part, m);
-            mul_v<V>(d, d, d);
-            fma_v<V>(sq, d, both, sq);
+            float e[V];
+            mul_v<V>(e, d, both);
+            fma_v<V>(sq, e, d, sq);
             add_v<V>(q, q, sq);
             n += (float)B;
         });

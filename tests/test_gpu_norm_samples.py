@@ -66,3 +66,25 @@ def test_some_samples_at_a_time_in_rows_of_wider_tensors():
     for y, dwide, dw, db in (call(), captured):
         for a, e in ((y, "y"), (dwide[:, 0], "dx"), (dwide[:, 2], "dgate"), (dw, "dweight"), (db, "dbias")):
             assert torch.equal(a, got[e]), e
+
+
+@pytest.mark.parametrize("dtype,size", [("f32", 1e20), ("f32", -3e37), ("bf16", 1e30)])
+@pytest.mark.parametrize("shape", [(2, 300, 64), (3, 5, 4104), (2, 6000)])
+def test_values_whose_square_overflows(dtype, size, shape):
+    """Far from zero, but near to each other: the variance is finite."""
+    import long_sequence_fft_b200 as lsf
+    x = _inputs(shape, dtype, seed=1, gate=False, affine=True)
+    x["x"] = torch.full(shape, size, device="cuda").to(x["x"].dtype)
+    got = _run(x, 2, "none")
+    assert torch.equal(got["y"], x["bias"].to(got["y"].dtype).expand(shape))
+    if dtype == "f32" and size == 1e20:
+        # deviations of 1e16: every value is exact to 2^-24 of 1e20, 6e-4 of a deviation
+        x["x"] = (1e20 + 1e16 * x["dy"]).float()
+        d = x["x"].double() - x["x"].double().reshape(shape[0], -1, 2, shape[-1] // 2).mean((1, 3)).repeat_interleave(
+            shape[-1] // 2, 1).reshape(shape[0], *[1] * (len(shape) - 2), shape[-1])
+        rstd = 1 / (d.reshape(shape[0], -1, 2, shape[-1] // 2) ** 2).mean((1, 3)).sqrt().repeat_interleave(
+            shape[-1] // 2, 1).reshape(shape[0], *[1] * (len(shape) - 2), shape[-1])
+        ref = d * rstd
+        y = lsf.group_norm(x["x"], 2).double()
+        # the mean is off by a few 2^-24 of 1e20 (joined over blocks): 16 of them, in deviations
+        assert (y - ref).abs().max() <= 16 * 2.0 ** -24 * 1e4 * 1.1 + 1e-5 * ref.abs().max()
