@@ -1306,11 +1306,12 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
         a.mean = (float*)workspace;
         a.rstd = (float*)((uint8_t*)workspace + space.sums / 2);
     }
+    (void)cudaGetLastError();                                 // (an earlier call's error is not this one's)
     dispatch(dtype, vec, [&](auto* t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         run<T, decltype(v)::value>(a, false, (cudaStream_t)stream);
     });
-    const cudaError_t e = cudaPeekAtLastError();
+    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? FFTCONV_OK
                             : fail(FFTCONV_ERR_CUDA, std::string("group norm launch: ") + cudaGetErrorString(e));
 }
@@ -1370,11 +1371,12 @@ int fftconv_group_norm_backward(const void* x, const void* gate, const void* wei
         use_vectors(a, V, rows == 1 || (ld_x % V == 0 && ld_dy % V == 0 && (!gate || ld_gate % V == 0)));
     a.sums = (float*)workspace;
     a.part = (float*)((uint8_t*)workspace + space_of(N, S, C, G, vec ? V : 1, true).sums);
+    (void)cudaGetLastError();                                 // (an earlier call's error is not this one's)
     dispatch(dtype, vec, [&](auto* t, auto v) {
         using T = std::remove_pointer_t<decltype(t)>;
         run<T, decltype(v)::value>(a, true, s);
     });
-    const cudaError_t e = cudaPeekAtLastError();
+    const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? FFTCONV_OK
                             : fail(FFTCONV_ERR_CUDA, std::string("group norm backward launch: ") + cudaGetErrorString(e));
 }

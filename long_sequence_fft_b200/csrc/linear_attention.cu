@@ -1504,6 +1504,7 @@ int fail(int status, const std::string& msg) {
     return status;
 }
 int cuda_fail(cudaError_t e, const char* what) {
+    (void)cudaGetLastError();                                 // (reported here, and not by the next call too)
     return fail(FFTCONV_ERR_CUDA, std::string(what) + ": " + cudaGetErrorName(e) + " (" + cudaGetErrorString(e) + ")");
 }
 
@@ -1736,7 +1737,7 @@ cudaError_t plan(Params& p, const fftconv_linear_attention_t& d, const Split& s,
     p.cuts = reinterpret_cast<int4*>(ws + pad256(s.max_seg * 2 * sizeof(int4)));
     p.seqs = reinterpret_cast<int4*>((uint8_t*)p.cuts + pad256(s.max_cut * 2 * sizeof(int4)));
     la_plan<<<1, d.nseq < 1024 ? (unsigned)(d.nseq + 31) / 32 * 32 : 1024, 0, stream>>>(p);
-    return cudaPeekAtLastError();
+    return cudaGetLastError();
 }
 
 // The launches of up to three roles, all with key and value dims within
@@ -1774,7 +1775,7 @@ cudaError_t zero_rest(void* out, const fftconv_linear_attention_t& d, int64_t H,
     const int64_t blocks = (d.T * H * D / 8 + 255) / 256;
     la_zero_rest<<<(unsigned)(blocks < 592 ? blocks : 592), 256, 0, s>>>((uint16_t*)out, d.T, (int)H, (int)D, st[1],
                                                                         st[2], cu, (int)d.nseq);
-    return cudaPeekAtLastError();
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -1830,6 +1831,7 @@ int fftconv_linear_attention(const fftconv_linear_attention_t* shape, const void
     if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return fail(FFTCONV_ERR_ALIGNMENT, "workspace not 256-byte aligned");
 
+    (void)cudaGetLastError();                                 // (an earlier call's error is not this one's)
     Params p{};
     fill(p, d, sp, log_decay, cu_seqlens, 1);
     if (int e = make_map(&p.maps[0], q, d.dtype, d.B, d.T, d.Hq, d.K, d.q_stride)) return e;
@@ -1927,6 +1929,7 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
     if (d.Hk < d.H) part[1] = (float*)take(tok * d.H * d.K * 4);
     if (d.Hv < d.H) part[2] = (float*)take(tok * d.H * d.V * 4);
 
+    (void)cudaGetLastError();                                 // (an earlier call's error is not this one's)
     Params p{};
     fill(p, d, sp, log_decay, cu_seqlens, 3);
     if (int e = make_map(&p.maps[0], q, d.dtype, d.B, d.T, d.Hq, d.K, d.q_stride)) return e;
@@ -2004,7 +2007,7 @@ int fftconv_linear_attention_backward(const fftconv_linear_attention_t* shape, c
         else
             la_sum_heads<false><<<grid, 256, 0, s>>>(part[i], (uint16_t*)out[i], tok, (int)heads[i], rep,
                                                      (int)dims[i], cu, (int)d.nseq);
-        e = cudaPeekAtLastError();
+        e = cudaGetLastError();
     }
     return e == cudaSuccess ? FFTCONV_OK : cuda_fail(e, "linear attention backward launch");
 }

@@ -202,11 +202,12 @@ extern "C" int fftconv_linear_attention_step(const void* q, const void* k, const
     a.K = (int)K; a.V = (int)V;
     a.scale = scale;
     cudaStream_t s = (cudaStream_t)stream;
+    (void)cudaGetLastError();                                 // (an earlier call's error is not this one's)
     if (dtype == FFTCONV_F16)
         launch<__half>(a, (unsigned)(B * H), s);
     else
         launch<__nv_bfloat16>(a, (unsigned)(B * H), s);
-    const cudaError_t e = cudaPeekAtLastError();
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return fail(FFTCONV_ERR_CUDA, std::string("linear attention step launch: ") + cudaGetErrorString(e));
     return FFTCONV_OK;

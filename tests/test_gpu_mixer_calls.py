@@ -200,3 +200,39 @@ def test_offsets_that_decrease():
         assert lsf.linear_attention_status() == 0
     for a, b in zip(lsf.linear_attention(q, k, v, ld, cu_seqlens=good, return_state=True), want):
         assert torch.equal(a, b)
+
+
+def test_a_failed_call_leaves_nothing_behind():
+    """The error of one call (here: a plan that finds no memory) is not the next
+    one's, of any operator."""
+    import long_sequence_fft_b200 as lsf
+    q, k, v, do = (_randn(i, 1, 300, 4, 64).bfloat16() for i in range(4))
+    k2, v2 = k[:, :, :2], v[:, :, :2]
+    ld, x = torch.full((4,), -0.1, device="cuda"), _randn(5, 6, 64)
+    big = _randn(6, 2, 300, 64)
+    cu = torch.tensor([10, 100, 200], dtype=torch.int32, device="cuda")
+
+    def fail():
+        torch.cuda.empty_cache()
+        free, _ = torch.cuda.mem_get_info()
+        hold = torch.empty(free - (256 << 20), dtype=torch.uint8, device="cuda")
+        with pytest.raises(lsf.FFTConvError):
+            lsf.Plan(1 << 20, 2, "bf16", order=5)            # (its workspace: 512 MB)
+        del hold
+        torch.cuda.empty_cache()
+
+    def train(f, *leaves):
+        leaves = [t.clone().requires_grad_() for t in leaves]
+        y = f(*leaves)
+        torch.autograd.grad(y, leaves, torch.ones_like(y))
+
+    for call in (lambda: lsf.group_norm(x, 4), lambda: lsf.group_norm(big, 4),
+                 lambda: train(lambda x: lsf.group_norm(x, 4), x),
+                 lambda: lsf.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], ld, torch.zeros((1, 4, 64, 64), device="cuda")),
+                 lambda: lsf.linear_attention(q, k, v, ld), lambda: lsf.linear_attention(q, k, v, ld, cu_seqlens=cu),
+                 lambda: train(lambda q, k, v: lsf.linear_attention(q, k, v, ld), q, k2, v2),
+                 lambda: lsf.linear_attention_status()):
+        fail()
+        call()
+    fail()
+    assert lsf.linear_attention_status() == 0
