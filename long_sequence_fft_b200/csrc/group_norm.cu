@@ -1206,6 +1206,15 @@ Space space_of(int64_t N, int64_t S, int64_t C, int64_t G, int V, bool back) {
                 : Space{2 * pad256(n * G * 4), pad256(n * chunks * spread_of(C, G, V) * G * 16)};
 }
 
+// Whether the token form's blocks of groups are within a grid's second extent
+// (8.4 M channels at least; the sample form's columns always are, see check).
+bool grid_fits(int64_t N, int64_t S, int64_t C, int64_t G, int V) {
+    const int64_t D = C / G;
+    int lanes = 0, per = 0;
+    if (S == 1 && D % V == 0) token_shape(D / V, V, lanes, per);
+    return lanes == 0 || token_grid(N, G, lanes, 1).gy <= 65535;
+}
+
 // The largest of the vector widths that a call may take (which depends on
 // strides and on the type).
 size_t workspace_bytes(int64_t N, int64_t S, int64_t C, int64_t G, bool back) {
@@ -1297,6 +1306,7 @@ int fftconv_group_norm(const void* x, const void* gate, const void* weight, cons
     a.eps = eps;
     const int V = vec_of(dtype);
     const bool vec = use_vectors(a, V, rows == 1 || (ld_x % V == 0 && (!gate || ld_gate % V == 0)));
+    if (!grid_fits(N, S, C, G, vec ? V : 1)) return fail(FFTCONV_ERR_UNSUPPORTED, "too many groups for one launch");
     a.mean = mean;
     a.rstd = rstd;
     a.keep = mean != nullptr;
@@ -1369,6 +1379,7 @@ int fftconv_group_norm_backward(const void* x, const void* gate, const void* wei
     const int V = vec_of(dtype);
     const bool vec =
         use_vectors(a, V, rows == 1 || (ld_x % V == 0 && ld_dy % V == 0 && (!gate || ld_gate % V == 0)));
+    if (!grid_fits(N, S, C, G, vec ? V : 1)) return fail(FFTCONV_ERR_UNSUPPORTED, "too many groups for one launch");
     a.sums = (float*)workspace;
     a.part = (float*)((uint8_t*)workspace + space_of(N, S, C, G, vec ? V : 1, true).sums);
     (void)cudaGetLastError();                                 // (an earlier call's error is not this one's)

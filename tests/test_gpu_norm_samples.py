@@ -88,3 +88,15 @@ def test_values_whose_square_overflows(dtype, size, shape):
         y = lsf.group_norm(x["x"], 2).double()
         # the mean is off by a few 2^-24 of 1e20 (joined over blocks): 16 of them, in deviations
         assert (y - ref).abs().max() <= 16 * 2.0 ** -24 * 1e4 * 1.1 + 1e-5 * ref.abs().max()
+
+
+@pytest.mark.parametrize("D,G", [(17, 500000), (16, 800000), (1, 65535 * 256)])
+def test_the_most_groups_of_a_launch(D, G):
+    """The last group of the widest rows that a launch takes."""
+    import long_sequence_fft_b200 as lsf
+    x = torch.randn((1, D * G), generator=torch.Generator(device="cuda").manual_seed(D), device="cuda")
+    y = lsf.group_norm(x, G)[:, -1024 * D:].double()
+    t = x[:, -1024 * D:].double().view(1024, D)
+    d = t - t.mean(1, keepdim=True)
+    ref = (d / (d * d).mean(1, keepdim=True).add(1e-5).sqrt()).view(1, -1)
+    assert (y - ref).abs().max() <= 2.0 ** -20 * 8

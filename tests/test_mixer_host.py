@@ -88,3 +88,18 @@ def test_norm_workspace_does_not_grow_with_samples(S, C, G, backward):
     sizes = [_norm_bytes(N, S, C, G, backward) for N in (1, 8, 444, 5000, 1 << 17)]
     assert max(sizes) <= (64 << 20) + 1024
     assert sizes[0] > 0 and sizes[0] < 1 << 23
+
+
+@pytest.mark.parametrize("D,G", [(17, 600000), (5, 2 << 20), (3, 5 << 20)])
+@pytest.mark.parametrize("dtype", [0, 2])
+def test_norm_groups_beyond_a_grid(D, G, dtype):
+    """Narrow groups that take more blocks of groups than a launch has: refused
+    before it, forward and backward."""
+    lib, C = _lib(), D * G
+    at = [i << 40 for i in range(1, 9)]                      # (never read)
+    rc = lib.fftconv_group_norm(at[0], None, None, None, at[1], None, None, 1, 1, C, G, C, 0, dtype, dtype, 1, 1e-5,
+                                at[2], 1 << 40, None)
+    assert rc == -2 and b"groups" in lib.fftconv_last_error()
+    rc = lib.fftconv_group_norm_backward(at[0], None, None, None, at[1], at[2], at[3], at[4], None, None, None, 1, 1,
+                                         C, G, C, 0, C, dtype, dtype, 1, at[5], 1 << 40, None)
+    assert rc == -2 and b"groups" in lib.fftconv_last_error()
