@@ -243,7 +243,7 @@ __device__ __forceinline__ float decay_power(float ld, float n) {
     ld = ld < -1e4f ? -1e4f : ld;
     const float p = ld * n;
     const float e = expf(p);
-    return n == 0.f ? 1.f : fmaf(e, fmaf(ld, n, -p), e);
+    return n == 0.f ? 1.f : isinf(e) ? e : fmaf(e, fmaf(ld, n, -p), e);
 }
 
 // g^n in two fp32 parts, for powers that are applied again and again: a walk
@@ -795,8 +795,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                         uint32_t s[32];
                         tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
-                        // (the weights are at most a; a score far above the
-                        // weighted ones costs nothing within 2^28)
+                        // (the weights are at most a, or where g is above 1 a
+                        // times the power for the row's farthest column; a
+                        // score far above the weighted ones costs nothing
+                        // within 2^28)
                         if (nv == kChunk) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
@@ -807,7 +809,8 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                                     amax = fmaxf(amax, fabsf(__uint_as_float(s[j])));
                         }
                     }
-                    scale = fp16_scale(amax * fmaxf(fabsf(r.a_in), fabsf(r.a_in) * pw[127]));
+                    const int far = max(0, jhi - jlo), half = far / 2;    // (in two steps: the power itself may overflow)
+                    scale = fp16_scale(amax * fmaxf(fabsf(r.a_in), fabsf(r.a_in) * pw[half] * pw[far - half]));
                 }
 #pragma unroll 1
                 for (int blk = 0; blk < 4; ++blk) {

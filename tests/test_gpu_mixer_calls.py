@@ -236,3 +236,31 @@ def test_a_failed_call_leaves_nothing_behind():
         call()
     fail()
     assert lsf.linear_attention_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("log_decay,T,scale", [(1.0, 60, 1e-25), (0.8, 90, 1e-30), (0.69, 128, 1e-37), (2.0, 44, 1e-37),
+                                               (0.05, 300, 1e-5)])
+def test_growth(dtype, log_decay, T, scale):
+    """g above 1: powers that leave fp32's range behind the last token do not
+    reach it, and weights above 1 count in fp16's scales."""
+    import long_sequence_fft_b200 as lsf
+    from mixer_reference import attention, magnitudes
+    dt = getattr(torch, dtype)
+    x = [_randn(i, 1, T, 2, 64).to(dt) for i in range(4)]
+    ld = torch.tensor([log_decay, -0.1], device="cuda")
+    leaves = [t.clone().requires_grad_() for t in x[:3]]
+    o = lsf.linear_attention(*leaves, ld, scale=scale)
+    got = dict(zip(("dq", "dk", "dv"), torch.autograd.grad(o, leaves, x[3])), o=o.detach())
+    args = (*x[:3], ld, scale, None, x[3], None)
+    ref, mag = attention(*args), magnitudes(*args)
+    # The growing head's (the other one's are below the type's normal range),
+    # element by element as in mixer_reference.  Its 2-norm is no statistic
+    # here: with g = 2 the last row holds most of it, and in that row two terms
+    # P_ij v_j, whose P_ij (one rounding, up to u) all 64 channels share: up to
+    # u + u for the norm as for an element.
+    u = torch.finfo(dt).eps / 2
+    for n, t in got.items():
+        r, m = ref[n][:, :, :1], mag[n][:, :, :1]
+        bound = u * r.abs() + (u + 2.0 ** -15) * m + torch.finfo(dt).smallest_normal * u
+        assert ((t[:, :, :1].double() - r).abs() <= bound).all(), n
