@@ -77,21 +77,22 @@ class _On:
 _on = _On
 
 
-def _written(*tensors):
-    """Mark the caller's tensors (None: new ones) as written in place, which a
-    launch through their addresses does not: a backward pass that saved one of
-    them then raises, as for torch's own in-place operations."""
+def _written(t):
+    """Mark the caller's tensor as written in place, which a launch through its
+    address does not: a backward pass that saved it then raises, as for torch's
+    own in-place operations."""
     import torch
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
+    torch.autograd.graph.increment_version(t)
 
 
 def _no_tangents(*tensors):
     """Refuse dual tensors: they do not require a gradient, so a call would
     return a result without a tangent, which stands for a derivative of zero."""
-    from torch.autograd import forward_ad
-    if forward_ad._current_level >= 0:                        # (inside a dual_level)
+    import torch
+    ad = torch.autograd.forward_ad
+    if ad._current_level >= 0:                                # (inside a dual_level)
         for t in tensors:
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            if t is not None and ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError("linear attention and group norm have no forward-mode derivatives")
 
 
@@ -330,7 +331,9 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
             _p(q), _p(k), _p(v), _p(log_decay), _p(state), _p(slots), _p(out), B, pool, H, Hq, k.shape[1],
             v.shape[1], K, V, code, scale, _Pair(*q.stride()[:2]), _Pair(*k.stride()[:2]), _Pair(*v.stride()[:2]),
             handle))
-    _written(state, given)
+    _written(state)
+    if given is not None:
+        _written(given)
     return out
 
 
