@@ -458,11 +458,12 @@ struct Layout {
 //
 // Rounding: P, and the weighted keys or the carry's copy (Layout), are rounded
 // once to the 16-bit type: their products are the two halves of the output,
-// each with the error of one rounding of it.  fp16 operands are scaled by
+// each with the error of one rounding of it.  FINE: P in two parts, 16 bits or
+// more, for calls of few tokens (kFineTokens).  fp16 operands are scaled by
 // exact powers of two (P by row, the carry's copy by its largest value, the
 // weighted keys by channel), so that nothing overflows fp16's range or falls
 // below it.
-template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
+template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT, bool FINE>
 __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Threads, 1)
     la_kernel(const __grid_constant__ Params p) {
     using L = Layout<KP, VP, F16, STATE_ONLY, EXACT>;
@@ -609,6 +610,19 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
         }
     };
 
+    // ... and with A = P, each 32 columns' two parts side by side
+    auto row_mma = [&](uint32_t d, uint32_t a, uint64_t d_z, uint32_t id, int ks, uint32_t acc) {
+        auto step = [&](int k) {
+            mma_ts_warp(d, a + (k >> 1) * 32 + (k & 1) * 8, d_z + (uint64_t)(k * 128), id, k > 0 ? 1u : acc);
+        };
+        if (ks == 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) step(k);
+        } else {
+            for (int k = 0; k < ks; ++k) step(k);
+        }
+    };
+
     if (warp == L::LoadWarp) {
         // ------------------------------------------------------- loads ---
         if (lane == 0) {
@@ -658,7 +672,10 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                 if (ok && p.cu && chunk_n(c) < kChunk) ok = wait(z_ready, 0);
                 if (!ok) break;
                 tc_fence_after();
-                token_mma(t_o, tbase + L::S + ga * 128, d_z, id_z, ks, carry && !L::SplitOut ? 1u : 0u);
+                const uint32_t t_p = tbase + L::S + ga * 128;
+                const uint32_t acc = carry && !L::SplitOut ? 1u : 0u;
+                if constexpr (FINE) row_mma(t_o, t_p + 16, d_z, id_z, ks, acc);
+                row_mma(t_o, t_p, d_z, id_z, ks, FINE ? 1u : acc);
                 tc_commit_warp(&bar_pv[ga]);
                 tc_commit_warp(&empty[st]);
             }
@@ -812,23 +829,33 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     const int far = max(0, jhi - jlo), half = far / 2;    // (in two steps: the power itself may overflow)
                     scale = fp16_scale(amax * fmaxf(fabsf(r.a_in), fabsf(r.a_in) * pw[half] * pw[far - half]));
                 }
+                // P (16 bit) lies over the score columns that this thread has
+                // read: each 32 columns' words, and behind them what they leave out
 #pragma unroll 1
                 for (int blk = 0; blk < 4; ++blk) {
-                    uint32_t pk[16];
+                    uint32_t s[32], pk[16];
                     if (masked(blk)) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) pk[j] = 0u;
+                        if constexpr (FINE) tmem_st16(t_s + blk * 32 + 16, pk);
                     } else {
-                        uint32_t s[32];
                         tmem_ld32(t_s + blk * 32, s);
                         tc_wait_ld();
                         weigh(s, blk, scale);
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
                             pk[j] = pack<F16>(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+                        if constexpr (FINE) {
+                            uint32_t lo[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float2 hi = unpack<F16>(pk[j]);
+                                lo[j] = pack<F16>(__uint_as_float(s[2 * j]) - hi.x, __uint_as_float(s[2 * j + 1]) - hi.y);
+                            }
+                            tmem_st16(t_s + blk * 32 + 16, lo);
+                        }
                     }
-                    // P (16 bit) lies over score columns that this thread has read
-                    tmem_st16(t_s + blk * 16, pk);
+                    tmem_st16(t_s + blk * 32, pk);
                 }
                 const float inv = F16 ? 1.f / scale : 1.f;
                 float f = r.a_carry * pw[min(128, max(0, rev ? nv - 1 - i : i + 1))];
@@ -1569,11 +1596,11 @@ int sm_count() {
     return n;
 }
 
-template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT>
+template <int KP, int VP, bool F16, bool STATE_ONLY, bool EXACT, bool FINE>
 cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
     using L = Layout<KP, VP, F16, STATE_ONLY, EXACT>;
     static std::atomic<uint64_t> ready{0};                    // devices whose kernel has its shared memory size
-    auto* kern = la_kernel<KP, VP, F16, STATE_ONLY, EXACT>;
+    auto* kern = la_kernel<KP, VP, F16, STATE_ONLY, EXACT, FINE>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1587,24 +1614,35 @@ cudaError_t launch(const Params& p, int64_t ctas, cudaStream_t s) {
                             s);
 }
 
-template <int KP, int VP, bool STATE_ONLY>
+template <int KP, int VP, bool STATE_ONLY, bool FINE>
 cudaError_t launch_type(const Params& p, bool f16, bool exact, int64_t ctas, cudaStream_t s) {
     // (128 channels in fp16 have two parts either way)
     if (f16)
-        return exact && KP == 64 ? launch<KP, VP, true, STATE_ONLY, KP == 64>(p, ctas, s)
-                                 : launch<KP, VP, true, STATE_ONLY, false>(p, ctas, s);
-    return exact ? launch<KP, VP, false, STATE_ONLY, true>(p, ctas, s)
-                 : launch<KP, VP, false, STATE_ONLY, false>(p, ctas, s);
+        return exact && KP == 64 ? launch<KP, VP, true, STATE_ONLY, KP == 64, FINE>(p, ctas, s)
+                                 : launch<KP, VP, true, STATE_ONLY, false, FINE>(p, ctas, s);
+    return exact ? launch<KP, VP, false, STATE_ONLY, true, FINE>(p, ctas, s)
+                 : launch<KP, VP, false, STATE_ONLY, false, FINE>(p, ctas, s);
 }
 
-template <bool STATE_ONLY>
+template <bool STATE_ONLY, bool FINE>
 cudaError_t launch_kernel(const Params& p, bool f16, bool exact, int kp, int vp, int64_t ctas, cudaStream_t s) {
     if (kp == 64)
-        return vp == 64 ? launch_type<64, 64, STATE_ONLY>(p, f16, exact, ctas, s)
-                        : launch_type<64, 128, STATE_ONLY>(p, f16, exact, ctas, s);
-    return vp == 64 ? launch_type<128, 64, STATE_ONLY>(p, f16, exact, ctas, s)
-                    : launch_type<128, 128, STATE_ONLY>(p, f16, exact, ctas, s);
+        return vp == 64 ? launch_type<64, 64, STATE_ONLY, FINE>(p, f16, exact, ctas, s)
+                        : launch_type<64, 128, STATE_ONLY, FINE>(p, f16, exact, ctas, s);
+    return vp == 64 ? launch_type<128, 64, STATE_ONLY, FINE>(p, f16, exact, ctas, s)
+                    : launch_type<128, 128, STATE_ONLY, FINE>(p, f16, exact, ctas, s);
 }
+
+// Calls of up to so many tokens have P in two parts.  A row of a short prompt
+// is one term or a few, and all channels of the output share the rounding of
+// its P: with one part, prompts of 1 to 20 tokens were up to 1.75 times as far
+// from the exact outputs as a form that rounds these only, over many rows
+// sqrt(2) times.  It costs the second products and a tenth of a long walk
+// (16 x 4096 tokens, 12 heads of 64/64, both passes at the power limit: 435 us
+// with one part and 475 with two), and less of a short call (16 heads, one
+// part and two: 37 tokens 8.7 us either way, 8 x 256 tokens of 128/128 bf16
+// 18.8 and 19.0, 2 x 1024 of them fp16, both passes, 95.0 and 102.4).
+constexpr int64_t kFineTokens = 2048;
 
 // How a call's sequences are cut into segments, one CTA for each (segment,
 // head, role).
@@ -1752,7 +1790,7 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
     bool exact = false;                       // a state is a result
     for (int i = 0; i < p.nroles; ++i) exact |= p.role[i].fin != nullptr;
     if (s.on) {
-        cudaError_t e = launch_kernel<true>(p, f16, exact, kp, vp, s.max_cut * d.H * p.nroles, stream);
+        cudaError_t e = launch_kernel<true, false>(p, f16, exact, kp, vp, s.max_cut * d.H * p.nroles, stream);
         if (e != cudaSuccess) return e;
         void* args[] = {const_cast<Params*>(&p)};
         e = cudaLaunchKernel(reinterpret_cast<const void*>(la_combine),
@@ -1764,7 +1802,9 @@ cudaError_t run_roles(const Params& p, const fftconv_linear_attention_t& d, cons
     // launch, all of which then runs the exact form.  With their states from
     // the launch before it 8192 tokens in 9 sequences took 90 us instead of
     // 95, but 2048 sequences of 64 tokens 2730 instead of 1870.)
-    return launch_kernel<false>(p, f16, exact && (!s.on || p.cu), kp, vp, ctas, stream);
+    exact &= !s.on || p.cu;
+    return d.B * d.T <= kFineTokens ? launch_kernel<false, true>(p, f16, exact, kp, vp, ctas, stream)
+                                    : launch_kernel<false, false>(p, f16, exact, kp, vp, ctas, stream);
 }
 
 cudaError_t copy_states(float* dst, const float* src, int64_t count, cudaStream_t s) {

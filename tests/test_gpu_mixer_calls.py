@@ -264,3 +264,29 @@ def test_growth(dtype, log_decay, T, scale):
         r, m = ref[n][:, :, :1], mag[n][:, :, :1]
         bound = u * r.abs() + (u + 2.0 ** -15) * m + torch.finfo(dt).smallest_normal * u
         assert ((t[:, :, :1].double() - r).abs() <= bound).all(), n
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("B,T,H,Hk,K,V,cu", [(1, 1, 1, 1, 128, 128, None), (3, 1, 6, 6, 64, 128, None),
+                                             (2, 5, 4, 2, 128, 64, None), (1, 19, 3, 1, 64, 64, [0, 2, 4, 4, 10, 19]),
+                                             (1, 128, 2, 2, 40, 72, None), (9, 33, 2, 1, 128, 128, None)])
+def test_short_prompts_are_rounded_once(dtype, B, T, H, Hk, K, V, cu):
+    """Sequences within a tile, without a state coming in: nothing but the
+    results is rounded to 16 bits (the weighted scores keep two parts of 8 or
+    11 bits, 2^-17 at most), so beside that rounding only the fp32 sums' bound
+    is left."""
+    import long_sequence_fft_b200 as lsf
+    from mixer_reference import attention, magnitudes
+    dt = getattr(torch, dtype)
+    x = [_randn(i, B, T, h, d).to(dt) for i, (h, d) in enumerate(((H, K), (Hk, K), (Hk, V), (H, V)))]
+    ld = -torch.logspace(-3, -0.3, H, dtype=torch.float32, device="cuda")
+    leaves = [t.clone().requires_grad_() for t in x[:3]]
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    o = lsf.linear_attention(*leaves, ld, cu_seqlens=cud)
+    got = dict(zip(("dq", "dk", "dv"), torch.autograd.grad(o, leaves, x[3])), o=o.detach())
+    args = (*x[:3], ld, K ** -0.5, None, x[3], None, cu)
+    ref, mag = attention(*args), magnitudes(*args)
+    u = torch.finfo(dt).eps / 2
+    for n, t in got.items():
+        bound = u * ref[n].abs() + 2.0 ** -15 * mag[n] + torch.finfo(dt).smallest_normal * u
+        assert ((t.double() - ref[n]).abs() <= bound).all(), n
