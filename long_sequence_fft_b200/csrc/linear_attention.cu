@@ -459,7 +459,8 @@ struct Layout {
 // Rounding: P, and the weighted keys or the carry's copy (Layout), are rounded
 // once to the 16-bit type: their products are the two halves of the output,
 // each with the error of one rounding of it.  FINE: P in two parts, 16 bits or
-// more, for calls of few tokens (kFineTokens).  fp16 operands are scaled by
+// more, for calls of few tokens (kFineTokens), and so the copy of the state in
+// front of a sequence that is one chunk.  fp16 operands are scaled by
 // exact powers of two (P by row, the carry's copy by its largest value, the
 // weighted keys by channel), so that nothing overflows fp16's range or falls
 // below it.
@@ -581,6 +582,9 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
     const int nch = chunks_of(s);
     const bool has_init = !STATE_ONLY && (first ? r.init != nullptr : true);
     const bool want_fin = STATE_ONLY || (s.count == 1 && r.fin != nullptr);
+    // one chunk: the copy of its initial state has a second part, in the next
+    // stage's place (128 channels) or that of the second sums, which are zero
+    const bool copy_in_two = L::Single || (FINE && nch == 1);
 
     auto wait = [&](uint64_t* bar, uint32_t phase) -> bool {
         return __all_sync(0xffffffffu, wait_phase(bar, phase & 1, abort_flag));
@@ -665,6 +669,16 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                         const int kx = k % (KP / 16);
                         const uint64_t step = (uint64_t)((kx >> 2) * 16384 + (kx & 3) * 32) >> 4;
                         mma_ss_warp(t_oc, d_x + step, d_carry + (uint64_t)(k * 128), id_z, k > 0);
+                    }
+                    if constexpr (FINE && KP == 128) {
+                        if (copy_in_two) {
+                            const uint64_t d_rest = make_desc(sb + L::StageBytes, 128 * 128, 1024, 2);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint64_t step = (uint64_t)((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+                                mma_ss_warp(t_oc, d_x + step, d_rest + (uint64_t)(k * 128), id_z, 1u);
+                            }
+                        }
                     }
                 }
                 tc_commit_warp(&bar_o[ga]);
@@ -1117,8 +1131,11 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                     if (c > 0 && !wait(&bar_o[(c - 1) % NA], (c - 1) / NA)) return false;
                     if (F16 && ts == 0) carry_inv[c & 3] = 1.f / cs;
                     uint8_t* dst = smem + L::OffCarry + (L::Single ? ch : d) * 128;
+                    const int rest_at = KP == 128 ? L::StageBytes - L::OffCarry : L::Single || d < 64 ? 64 * 128 : -64 * 128;
+                    const bool no_copy = L::Stacked && copy_in_two && second;
 #pragma unroll
                     for (int q = 0; q < kCols / 8; ++q) {
+                        if (no_copy) break;
                         const int vc = col0 / 8 + q;
                         uint8_t* to = dst + (vc >> 3) * 16384 + (((vc & 7) ^ (d & 7)) << 4);
                         uint32_t v[4], rest[4];
@@ -1127,14 +1144,14 @@ __global__ void __launch_bounds__(Layout<KP, VP, F16, STATE_ONLY, EXACT>::Thread
                             float2 f = make_float2(state[q * 8 + 2 * e], state[q * 8 + 2 * e + 1]);
                             if constexpr (F16) f = mul2(f, make_float2(cs, cs));
                             v[e] = pack<F16>(f.x, f.y);
-                            if constexpr (L::Single) {
+                            if (copy_in_two) {
                                 f = fma2(unpack<F16>(v[e]), make_float2(-1.f, -1.f), f);
                                 rest[e] = pack<F16>(f.x, f.y);
                             }
                         }
                         *reinterpret_cast<uint4*>(to) = make_uint4(v[0], v[1], v[2], v[3]);
-                        if constexpr (L::Single)
-                            *reinterpret_cast<uint4*>(to + 64 * 128) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+                        if (copy_in_two)
+                            *reinterpret_cast<uint4*>(to + rest_at) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
                     }
                     fence_proxy_async_smem();
                 }

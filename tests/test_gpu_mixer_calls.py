@@ -269,24 +269,36 @@ def test_growth(dtype, log_decay, T, scale):
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("B,T,H,Hk,K,V,cu", [(1, 1, 1, 1, 128, 128, None), (3, 1, 6, 6, 64, 128, None),
                                              (2, 5, 4, 2, 128, 64, None), (1, 19, 3, 1, 64, 64, [0, 2, 4, 4, 10, 19]),
-                                             (1, 128, 2, 2, 40, 72, None), (9, 33, 2, 1, 128, 128, None)])
-def test_short_prompts_are_rounded_once(dtype, B, T, H, Hk, K, V, cu):
-    """Sequences within a tile, without a state coming in: nothing but the
-    results is rounded to 16 bits (the weighted scores keep two parts of 8 or
-    11 bits, 2^-17 at most), so beside that rounding only the fp32 sums' bound
-    is left."""
+                                             (1, 128, 2, 2, 40, 72, None), (9, 33, 2, 1, 128, 128, None),
+                                             (2, 77, 2, 2, 24, 120, None)])
+@pytest.mark.parametrize("state_in,state_out", [(False, False), (True, False), (True, True), (False, True)])
+def test_short_prompts_are_rounded_once(dtype, B, T, H, Hk, K, V, cu, state_in, state_out):
+    """Sequences within a tile: nothing but the results is rounded to 16 bits
+    (the weighted scores and the state coming in keep two parts of 8 or 11
+    bits, 2^-17 at most), so beside that rounding only the fp32 sums' bound is
+    left."""
     import long_sequence_fft_b200 as lsf
     from mixer_reference import attention, magnitudes
     dt = getattr(torch, dtype)
+    n = B if cu is None else len(cu) - 1
     x = [_randn(i, B, T, h, d).to(dt) for i, (h, d) in enumerate(((H, K), (Hk, K), (Hk, V), (H, V)))]
     ld = -torch.logspace(-3, -0.3, H, dtype=torch.float32, device="cuda")
-    leaves = [t.clone().requires_grad_() for t in x[:3]]
+    initial = _randn(7, n, H, K, V) if state_in else None
+    dstate = _randn(8, n, H, K, V) if state_out else None
+    leaves = [t.clone().requires_grad_() for t in x[:3] + ([initial] if state_in else [])]
     cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
-    o = lsf.linear_attention(*leaves, ld, cu_seqlens=cud)
-    got = dict(zip(("dq", "dk", "dv"), torch.autograd.grad(o, leaves, x[3])), o=o.detach())
-    args = (*x[:3], ld, K ** -0.5, None, x[3], None, cu)
+    o, s = lsf.linear_attention(*leaves[:3], ld, initial_state=leaves[3] if state_in else None, cu_seqlens=cud,
+                                return_state=True)
+    out = [o, s] if state_out else [o]
+    got = dict(zip(("dq", "dk", "dv", "dinitial"), torch.autograd.grad(out, leaves, [x[3], dstate][:len(out)])))
+    got.update(o=o.detach(), state=s.detach())
+    alone = lsf.linear_attention(*x[:3], ld, initial_state=initial, cu_seqlens=cud)
+    args = (*x[:3], ld, K ** -0.5, initial, x[3], dstate, cu)
     ref, mag = attention(*args), magnitudes(*args)
     u = torch.finfo(dt).eps / 2
-    for n, t in got.items():
-        bound = u * ref[n].abs() + 2.0 ** -15 * mag[n] + torch.finfo(dt).smallest_normal * u
+    for n, t in [*got.items(), ("o", alone)]:
+        if t.dtype == torch.float32:
+            bound = 2.0 ** -18 * mag[n] + 1e-37
+        else:
+            bound = u * ref[n].abs() + 2.0 ** -15 * mag[n] + torch.finfo(dt).smallest_normal * u
         assert ((t.double() - ref[n]).abs() <= bound).all(), n
