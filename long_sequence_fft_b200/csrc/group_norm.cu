@@ -1003,7 +1003,10 @@ int fail(int status, const std::string& msg) {
     return status;
 }
 
-constexpr int64_t kTokenBlocks = 148 * 3;     // blocks of the token form at most, all resident: they walk down the rows
+// Blocks of the token form at most, all resident: they walk down the rows.
+// (B200's number of SMs here and in chunks_of, so that a workspace's size does
+// not depend on the current device.)
+constexpr int64_t kTokenBlocks = 148 * 3;
 
 // Threads of the sample form's blocks: whole rows of vector columns.
 int sample_threads(int64_t S, int64_t C, int V) {

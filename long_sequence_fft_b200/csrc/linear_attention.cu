@@ -1685,8 +1685,12 @@ Split split_of(const fftconv_linear_attention_t& d, int nroles) {
     if (d.nseq > 0) {
         // lengths are known on the device only.  Pieces a little longer than
         // an even share leave room for the sequences' short ends beside them
-        // (8192 tokens in 9 sequences, 16 heads of 128/128: half a share 100
-        // us, 3/4 108, one 96, 5/4 95, 3/2 94)
+        // (us with pieces of 3/4 of a share, one, 5/4 and 3/2, in a graph:
+        // 8192 tokens in 9 sequences, 16 heads of 128/128 88 79 73 83, both
+        // passes 230 204 213 222; 32768 in 40, 12 heads of 64/64 135 148 122
+        // 134; 16384 in 5, 8 heads of 64/64 77 57 60 67; 16384 in 12, 4 heads
+        // of 128/128 fp16 52 52 59 62; 65536 in 30, 6 heads of 64/64, both
+        // passes 260 224 223 251)
         len = up((d.T * d.H * nroles * 5 / 4 + sms - 1) / sms);
     } else {
         const int64_t share = (d.B * d.T * d.H * nroles + sms - 1) / sms;

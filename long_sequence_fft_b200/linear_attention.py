@@ -90,7 +90,7 @@ def _no_tangents(*tensors):
     return a result without a tangent, which stands for a derivative of zero."""
     import torch
     ad = torch.autograd.forward_ad
-    if ad._current_level >= 0:                                # (inside a dual_level)
+    if getattr(ad, "_current_level", 0) >= 0:                 # (inside a dual_level)
         for t in tensors:
             if t is not None and ad.unpack_dual(t).tangent is not None:
                 raise NotImplementedError("linear attention and group norm have no forward-mode derivatives")
@@ -244,7 +244,10 @@ def linear_attention(q, k, v, log_decay, *, scale=None, initial_state=None, cu_s
     initial_state [B or n, H, K, V] fp32: the states before the first tokens.
 
     Returns o [B, T, H, V], or (o, state) with return_state: state is what
-    linear_attention_step and a later call's initial_state take.
+    linear_attention_step and a later call's initial_state take.  (o of calls
+    with and without return_state, or with other tokens beside a sequence's,
+    can differ in its last bits: include/fftconv.h.)  The results are complete
+    unless linear_attention_status() reports a wait that gave up.
     Differentiable in q, k, v and initial_state (not in log_decay, not in
     forward mode, and not together with `out` or `stream`).  When a backward pass is captured into a
     CUDA graph, let the forward call of the same leaves be captured with it."""
@@ -297,7 +300,8 @@ def linear_attention_step(q, k, v, log_decay, state, *, slots=None, scale=None, 
     contiguous; state [pool, H, K, V] fp32, contiguous.  slots (int32 on the
     device, [B]): the state of each row; a row whose slot is outside the pool,
     or that an earlier row names already, is idle (zero output, no state
-    touched).  Without slots row b uses state b.  No gradients."""
+    touched).  Without slots row b uses state b.  No gradients; state and out
+    count as written in place for gradients of other calls that saved them."""
     import torch
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must have 3 dimensions: batch, head, channel")
