@@ -215,7 +215,14 @@ def test_a_failed_call_leaves_nothing_behind():
     def fail():
         torch.cuda.empty_cache()
         free, _ = torch.cuda.mem_get_info()
-        hold = torch.empty(free - (256 << 20), dtype=torch.uint8, device="cuda")
+        for spare in (256, 320, 384, 448):                   # (what cannot be had in one piece)
+            try:
+                hold = torch.empty(free - (spare << 20), dtype=torch.uint8, device="cuda")
+                break
+            except torch.cuda.OutOfMemoryError:
+                hold = None
+        if hold is None:
+            pytest.skip("the device's memory cannot be held")
         with pytest.raises(lsf.FFTConvError):
             lsf.Plan(1 << 20, 2, "bf16", order=5)            # (its workspace: 512 MB)
         del hold

@@ -43,27 +43,21 @@ def test_some_samples_at_a_time_in_rows_of_wider_tensors():
     x = _inputs((N, C), "bf16", seed=3, gate=True, affine=True)
     wide = torch.empty((N, 3, C), device="cuda", dtype=torch.bfloat16)
     wide[:, 0], wide[:, 2] = x["x"], x["gate"]
-    whole = wide.requires_grad_()
-    w, b = x["weight"].clone().requires_grad_(), x["bias"].clone().requires_grad_()
 
-    def call():
+    def call(whole, w, b):
         y = lsf.group_norm(whole[:, 0], G, w, b, gate=whole[:, 2], activation="silu")
         dy = torch.cat([x["dy"], x["dy"]], 1)[:, :C]
         return [y, *torch.autograd.grad(y, [whole, w, b], dy)]
 
-    got = _run(x, G, "silu")
-    side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
-    with torch.cuda.stream(side):
-        call()
-    torch.cuda.current_stream().wait_stream(side)
+    leaves = lambda: [t.clone().requires_grad_() for t in (wide, x["weight"], x["bias"])]    # noqa: E731
+    got, mine = _run(x, G, "silu"), leaves()
     g = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(g):
-        captured = call()
+        captured = call(*mine)
     g.replay()
     torch.cuda.synchronize()
-    for y, dwide, dw, db in (call(), captured):
+    for y, dwide, dw, db in (call(*leaves()), captured):
         for a, e in ((y, "y"), (dwide[:, 0], "dx"), (dwide[:, 2], "dgate"), (dw, "dweight"), (db, "dbias")):
             assert torch.equal(a, got[e]), e
 
